@@ -1,4 +1,6 @@
-"""Quantized GEMV with fused dequantization for GB300 (sm_103a).
+"""Quantized GEMV with fused dequantization for GB300 (sm_103a), and the
+operators around it in a serving step: the block-scaled fp8 product, attention
+over a paged cache, the upkeep of its pages and token log probabilities.
 
 The compute lives in the CUDA library libqgemv.so (C ABI in include/qgemv.h);
 this module is a thin ctypes binding over it with the same names. It only
@@ -15,6 +17,7 @@ on one stream are ordered by the stream.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 import threading
 
@@ -27,6 +30,8 @@ QG_OK, QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_MISALIGNED = 0, 1, 2, 3
 QG_ERR_CUDA, QG_ERR_WORKSPACE, QG_ERR_DEVICE = 4, 5, 6
 QG_OP_Q4_0, QG_OP_DUAL_Q4_0, QG_OP_Q4_K, QG_OP_AFFINE, QG_OP_AF4_G64 = 0, 1, 2, 3, 4
 QG_OP_DUAL_Q4_0_HOST = 5
+QG_OP_FP8_B128 = 6
+QG_F32, QG_F16, QG_BF16 = 0, 1, 2
 QG_OPT_PDL = 1
 QG_OPT_PREFILL_MIN_M = 2
 QG_OPT_STREAM, QG_OPT_STREAM_WARPS, QG_OPT_STREAM_SLOTS = 3, 4, 5
@@ -42,7 +47,11 @@ EXPORTS = ("qgemv_q4_0", "qgemv_dual_q4_0", "qgemv_q4_k", "qmm_affine", "qkv_spl
            "dequant_q4_0", "dequant_q4_k", "dequant_affine", "qg_workspace_size",
            "qg_status_string", "qg_last_cuda_error", "qg_device_error",
            "qg_selftest_wait_timeout", "qg_set_option", "qg_get_option",
-           "qgemv_q4_k_noalloc", "qg_prepare_af4_g64", "qmm_af4_g64", "qgemv_dual_q4_0_host")
+           "qgemv_q4_k_noalloc", "qg_prepare_af4_g64", "qmm_af4_g64", "qgemv_dual_q4_0_host",
+           "quantize_fp8_b128", "qmm_fp8_b128", "attn_paged", "attn_paged_workspace_size",
+           "kv_append", "kv_copy_pages", "kv_fork", "kv_fork_workspace_size", "kv_free",
+           "kv_compact", "kv_compact_workspace_size", "token_logprobs",
+           "token_logprobs_workspace_size")
 
 _LIB = None
 _LOCK = threading.Lock()
@@ -89,6 +98,19 @@ def lib():
             "qgemv_q4_k_noalloc": [P, P, P, I64, I64, I64, P],
             "qg_prepare_af4_g64": [P, P, P, P, P, I64, I64, P],
             "qmm_af4_g64": [P, P, P, P, I64, I64, I64, P, SZ, P],
+            "quantize_fp8_b128": [P, I, I64, P, P, I64, I64, P],
+            "qmm_fp8_b128": [P, P, P, P, P, I, I64, I64, I64, P, SZ, P],
+            "attn_paged": [P, I64] + [P] * 7 + [I] + [I64] * 9 + [C.c_float] * 2 + [I64, P, SZ, P],
+            "attn_paged_workspace_size": [I64] * 6 + [C.POINTER(SZ)],
+            "kv_append": [P, P, I64, I64, I, P, P, I, P] + [I64] * 5 + [P],
+            "kv_copy_pages": [P, I64, I64, I64, P, P, I64, P],
+            "kv_fork": [P] + [I64] * 4 + [P] * 3 + [I64, I64, P, I64, P, P, P, P, SZ, P],
+            "kv_fork_workspace_size": [I64, C.POINTER(SZ)],
+            "kv_free": [P] * 4 + [I64] * 3 + [P] * 4,
+            "kv_compact": [P, I64, I64, I64, P, I64, I64] + [P] * 6 + [SZ, P],
+            "kv_compact_workspace_size": [I64, C.POINTER(SZ)],
+            "token_logprobs": [P, I, I64, P, I64, I64, I] + [P] * 6 + [SZ, P],
+            "token_logprobs_workspace_size": [I64, I64, I, C.POINTER(SZ)],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -146,7 +168,10 @@ def workspace_size(op: int, M: int, N: int, K: int, group_size: int = 0, packed:
 
 
 def _workspace(op, M, N, K, gs, packed, device, workspace, stream):
-    need = workspace_size(op, M, N, K, gs, packed)
+    return _scratch(workspace_size(op, M, N, K, gs, packed), device, workspace, stream)
+
+
+def _scratch(need, device, workspace, stream):
     if workspace is not None:
         return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
     if need == 0:
@@ -320,6 +345,271 @@ def dequant_affine(q, scales, biases, N, K, group_size, packed, out=None, *, str
                                 _dev(out, "out", torch.float32), N, K, int(group_size),
                                 int(packed), _stream(stream)), "dequant_affine")
     return out
+
+
+# ------------------------------------------------------- serving operators
+_DTYPES = {torch.float32: QG_F32, torch.float16: QG_F16, torch.bfloat16: QG_BF16}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return d
+
+
+def _rows(t: torch.Tensor, name: str, dims: int):
+    """(address, row stride) of a CUDA tensor whose rows t[i] are dense; the
+    rows may lie apart (a part of a fused projection, a padded vocabulary)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    width = math.prod(t.shape[1:])
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    step = 1
+    for i in range(dims - 1, 0, -1):
+        if t.shape[i] > 1 and t.stride(i) != step:
+            raise ValueError(f"{name} must have dense rows")
+        step *= t.shape[i]
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+
+
+def _same(t: torch.Tensor, name: str, *shape) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+
+
+_SIZES = {}
+
+
+def _size(what: str, *args) -> int:
+    """The workspace bytes that the library asks for, asked once per shape and device."""
+    key = (what, torch.cuda.current_device(), *args)
+    n = _SIZES.get(key)
+    if n is None:
+        v = C.c_size_t(0)
+        _check(getattr(lib(), what)(*args, C.byref(v)), what)
+        if len(_SIZES) > 4096:
+            _SIZES.clear()
+        n = _SIZES[key] = int(v.value)
+    return n
+
+
+def quantize_fp8_b128(x, codes=None, scales=None, *, stream=None):
+    """(codes, scales) of x [M, K] (float32, float16 or bfloat16; its rows may
+    lie apart): e4m3 codes [M, K] and one float32 scale per 128 values of a
+    row, [M, ceil(K / 128)]."""
+    at, stride = _rows(x, "x", 2)
+    M, K = x.shape
+    KB = (K + 127) // 128
+    if codes is None:
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _same(codes, "codes", M, K)
+    if scales is None:
+        scales = torch.empty((M, KB), dtype=torch.float32, device=x.device)
+    else:
+        _same(scales, "scales", M, KB)
+    _check(lib().quantize_fp8_b128(at, _dtype(x, "x"), stride, _dev(codes, "codes", torch.float8_e4m3fn),
+                                   _dev(scales, "scales", torch.float32), M, K, _stream(stream)),
+           "quantize_fp8_b128")
+    return codes, scales
+
+
+def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, workspace=None,
+                 stream=None):
+    """y[M, N] = (a * a_scales) . (w * w_scales)^T: e4m3 codes a [M, K] with a
+    scale per row and 128 values of K, w [N, K] with one per 128 x 128 values;
+    y is float32 or bfloat16."""
+    M, K = a.shape
+    N = w.shape[0]
+    KB = (K + 127) // 128
+    _same(w, "w", N, K)
+    _same(a_scales, "a_scales", M, KB)
+    _same(w_scales, "w_scales", (N + 127) // 128, KB)
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    else:
+        _same(y, "y", M, N)
+    st = _stream(stream)
+    need = _size("qg_workspace_size", QG_OP_FP8_B128, M, N, K, 0, 0)
+    ws, wsb = _scratch(need, a.device, workspace, st)
+    _check(lib().qmm_fp8_b128(_dev(a, "a", torch.float8_e4m3fn),
+                              _dev(a_scales, "a_scales", torch.float32),
+                              _dev(w, "w", torch.float8_e4m3fn),
+                              _dev(w_scales, "w_scales", torch.float32), _dev(y, "y"),
+                              _dtype(y, "y"), M, N, K, ws, wsb, st), "qmm_fp8_b128")
+    return y
+
+
+def attn_paged(q, k_cache, v_cache, page_table, q_offsets, context_lens, out=None, lse=None, *,
+               max_new=None, scale=None, softcap=0.0, window=0, return_lse=False, workspace=None,
+               stream=None):
+    """Attention of new tokens over a paged cache that holds their keys and
+    values already; out [tokens, q_heads, head_dim], and with return_lse (or a
+    tensor lse) also the log of each row's sum, float32 [tokens, q_heads].
+
+    q [tokens, q_heads, head_dim] float16 or bfloat16 (rows may lie apart);
+    k_cache, v_cache [num_pages, kv_heads, page_size, head_dim]; page_table
+    int32 [batch, width]; q_offsets int32 [batch + 1]: sequence b's new tokens
+    are rows q_offsets[b] .. q_offsets[b + 1] - 1; context_lens int32 [batch]:
+    its keys, the new ones included. max_new: the most new tokens that any
+    sequence has (default: all of q's rows). scale: default head_dim ** -0.5.
+    softcap > 0 caps the scores, window > 0 limits how far back a row sees."""
+    at, stride = _rows(q, "q", 3)
+    T, Hq, D = q.shape
+    NP, Hkv, page, _ = k_cache.shape
+    B, width = page_table.shape
+    _same(k_cache, "k_cache", NP, Hkv, page, D)
+    _same(v_cache, "v_cache", NP, Hkv, page, D)
+    _same(q_offsets, "q_offsets", B + 1)
+    _same(context_lens, "context_lens", B)
+    dt = q.dtype
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+    else:
+        _same(out, "out", T, Hq, D)
+    if lse is not None:
+        _same(lse, "lse", T, Hq)
+    elif return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    st = _stream(stream)
+    max_new = T if max_new is None else int(max_new)
+    need = _size("attn_paged_workspace_size", T, B, max_new, Hq, Hkv, D)
+    ws, wsb = _scratch(need, q.device, workspace, st)
+    _check(lib().attn_paged(at, stride, _dev(k_cache, "k_cache", dt), _dev(v_cache, "v_cache", dt),
+                            _dev(page_table, "page_table", torch.int32),
+                            _dev(q_offsets, "q_offsets", torch.int32),
+                            _dev(context_lens, "context_lens", torch.int32), _dev(out, "out", dt),
+                            None if lse is None else _dev(lse, "lse", torch.float32),
+                            _dtype(q, "q"), T, B, max_new, Hq, Hkv, D, NP, page, width,
+                            D ** -0.5 if scale is None else scale, softcap, window, ws, wsb, st),
+           "attn_paged")
+    return (out, lse) if lse is not None else out
+
+
+def kv_append(k, v, k_cache, v_cache, slots, *, stream=None):
+    """Rows of k and v [tokens, kv_heads, head_dim] (rows may lie apart, as
+    parts of one fused projection) into a layer's k_cache and v_cache
+    [num_pages, kv_heads, page_size, head_dim], rounded to their type. slots
+    int64 [tokens]: page * page_size + place of each row; negative: skipped."""
+    ka, ks = _rows(k, "k", 3)
+    va, vs = _rows(v, "v", 3)
+    T, H, D = k.shape
+    NP, _, page, _ = k_cache.shape
+    _same(v, "v", T, H, D)
+    _same(k_cache, "k_cache", NP, H, page, D)
+    _same(v_cache, "v_cache", NP, H, page, D)
+    _same(slots, "slots", T)
+    if v.dtype != k.dtype or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k and v, and their caches, must be of one type")
+    _check(lib().kv_append(ka, va, ks, vs, _dtype(k, "k"), _dev(k_cache, "k_cache"),
+                           _dev(v_cache, "v_cache"), _dtype(k_cache, "k_cache"),
+                           _dev(slots, "slots", torch.int64), T, H, D, NP, page, _stream(stream)),
+           "kv_append")
+
+
+def _planes(cache):
+    """(address, planes, pages, bytes per page) of a cache [planes, num_pages, ...]."""
+    at = _dev(cache, "cache")
+    if cache.dim() < 3 or cache.numel() == 0:
+        raise ValueError("cache must be [planes, num_pages, ...] with at least one value")
+    planes, pages = cache.shape[:2]
+    return at, planes, pages, cache.numel() // (planes * pages) * cache.element_size()
+
+
+def kv_copy_pages(cache, src, dst, *, stream=None):
+    """In every plane of cache [planes, num_pages, ...]: page dst[i] = page
+    src[i] (int32). Pairs with a negative member are skipped."""
+    _same(dst, "dst", *src.shape)
+    _check(lib().kv_copy_pages(*_planes(cache), _dev(src, "src", torch.int32),
+                               _dev(dst, "dst", torch.int32), src.numel(), _stream(stream)),
+           "kv_copy_pages")
+
+
+def kv_fork(cache, page_table, lens, ref_counts, parents, page_size, *, workspace=None, stream=None):
+    """Continuations of sequences: child c shares the whole pages of row
+    parents[c] of page_table and gets a copy of its partly filled last page, in
+    the lowest free pages. Returns (child_table [children, width], child_lens,
+    new ref_counts); cache [planes, num_pages, ...] is changed in place."""
+    planes = _planes(cache)
+    rows, width = page_table.shape
+    n = parents.numel()
+    _same(lens, "lens", rows)
+    _same(ref_counts, "ref_counts", planes[2])
+    dev = page_table.device
+    table = torch.empty((n, width), dtype=torch.int32, device=dev)
+    child_lens = torch.empty(n, dtype=torch.int32, device=dev)
+    refs = torch.empty_like(ref_counts)
+    st = _stream(stream)
+    ws, wsb = _scratch(_size("kv_fork_workspace_size", n), dev, workspace, st)
+    _check(lib().kv_fork(*planes, int(page_size), _dev(page_table, "page_table", torch.int32),
+                         _dev(lens, "lens", torch.int32), _dev(ref_counts, "ref_counts", torch.int32),
+                         rows, width, _dev(parents, "parents", torch.int32), n, table.data_ptr(),
+                         child_lens.data_ptr(), refs.data_ptr(), ws, wsb, st), "kv_fork")
+    return table, child_lens, refs
+
+
+def kv_free(page_table, lens, ref_counts, drop, *, stream=None):
+    """New (page_table, lens, ref_counts) without the rows where drop (uint8
+    [rows]) is not 0: their entries are -1, their length 0, and each page that
+    they held counts one holder less."""
+    rows, width = page_table.shape
+    _same(lens, "lens", rows)
+    _same(drop, "drop", rows)
+    table, new_lens = torch.empty_like(page_table), torch.empty_like(lens)
+    refs = torch.empty_like(ref_counts)
+    _check(lib().kv_free(_dev(page_table, "page_table", torch.int32), _dev(lens, "lens", torch.int32),
+                         _dev(ref_counts, "ref_counts", torch.int32), _dev(drop, "drop", torch.uint8),
+                         rows, width, ref_counts.numel(), table.data_ptr(), new_lens.data_ptr(),
+                         refs.data_ptr(), _stream(stream)), "kv_free")
+    return table, new_lens, refs
+
+
+def kv_compact(cache, page_table, ref_counts, *, workspace=None, stream=None):
+    """Moves the pages of cache [planes, num_pages, ...] so that those in use
+    are 0 .. live - 1. Returns (page_table, ref_counts, page_map, live) in the
+    new numbers; page_map[p] is page p's new number, -1 if it was free."""
+    planes = _planes(cache)
+    rows, width = page_table.shape
+    _same(ref_counts, "ref_counts", planes[2])
+    dev = page_table.device
+    table, refs = torch.empty_like(page_table), torch.empty_like(ref_counts)
+    page_map = torch.empty_like(ref_counts)
+    live = torch.empty(1, dtype=torch.int32, device=dev)
+    st = _stream(stream)
+    ws, wsb = _scratch(_size("kv_compact_workspace_size", planes[2]), dev, workspace, st)
+    _check(lib().kv_compact(*planes, _dev(page_table, "page_table", torch.int32), rows, width,
+                            _dev(ref_counts, "ref_counts", torch.int32), table.data_ptr(),
+                            refs.data_ptr(), page_map.data_ptr(), live.data_ptr(), ws, wsb, st),
+           "kv_compact")
+    return table, refs, page_map, live
+
+
+def token_logprobs(logits, targets, top_k=0, *, workspace=None, stream=None):
+    """(logprobs, entropy, ranks, top_values, top_ids) of rows of logits [M, V]
+    (rows may lie apart): the log probability of each row's target (int64;
+    negative: none, 0 and rank -1), the row's entropy, how many logits are
+    greater than the target's, and the min(top_k, V) largest alternatives as log
+    probabilities and ids, ties to the lower id."""
+    at, stride = _rows(logits, "logits", 2)
+    M, V = logits.shape
+    _same(targets, "targets", M)
+    k = min(int(top_k), V)
+    dev = logits.device
+    f = torch.empty((2, M), dtype=torch.float32, device=dev)
+    ranks = torch.empty(M, dtype=torch.int32, device=dev)
+    top = torch.empty((M, k), dtype=torch.float32, device=dev)
+    ids = torch.empty((M, k), dtype=torch.int32, device=dev)
+    st = _stream(stream)
+    ws, wsb = _scratch(_size("token_logprobs_workspace_size", M, V, k), dev, workspace, st)
+    _check(lib().token_logprobs(at, _dtype(logits, "logits"), stride,
+                                _dev(targets, "targets", torch.int64), M, V, k, f.data_ptr(),
+                                f.data_ptr() + 4 * M, ranks.data_ptr(), top.data_ptr(),
+                                ids.data_ptr(), ws, wsb, st), "token_logprobs")
+    return f[0], f[1], ranks, top, ids
 
 
 def device_error(clear: bool = True) -> int:

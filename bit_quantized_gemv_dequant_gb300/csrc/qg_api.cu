@@ -253,6 +253,8 @@ int run_gemv_host(const GemvArgs& a, void* ws, size_t ws_bytes, qg_stream_t stre
 
 }  // namespace
 
+int device_ctx(const DevCtx** out) { return current_ctx(out); }
+
 int q4_k_cuda_core(const void* w, const float* x, float* y, int64_t M, int64_t N, int64_t K,
                    void* ws, size_t ws_bytes, qg_stream_t stream) {
     GemvArgs a{};
@@ -305,6 +307,17 @@ int workspace_size_impl(int op, int64_t M, int64_t N, int64_t K, int group_size,
         int rc = check_dims(M, N, K);
         if (rc) return rc;
         return (M > 32 || N % 64 || K % 64) ? QG_ERR_INVALID_ARG : QG_OK;
+    }
+    if (op == QG_OP_FP8_B128) {
+        int rc = check_dims(M, N, K);
+        if (rc) return rc;
+        const DevCtx* dc = nullptr;
+        rc = current_ctx(&dc);
+        if (rc) return rc;
+        Fp8Args f{};
+        f.M = M; f.N = N; f.K = K;
+        *bytes = fp8_workspace_bytes(*dc, f);
+        return QG_OK;
     }
     GemvArgs a{};
     switch (op) {

@@ -18,6 +18,9 @@ enum : unsigned {
     DEVERR_WAIT_DRAIN = 4u,     // copies still in flight after an error
     DEVERR_SELFTEST = 8u,       // the self-test wait ran out (expected)
     DEVERR_TC_WAIT = 16u,       // a tensor-core pipeline role gave up waiting
+    DEVERR_INDEX = 32u,         // a page, slot, row or token index out of its range
+    DEVERR_NO_PAGE = 64u,       // kv_fork found too few free pages
+    DEVERR_COUNT = 128u,        // kv_free: a page's count would fall below zero
 };
 
 // Bounded waits give up after this many nanoseconds.
@@ -231,6 +234,103 @@ int q4_k_cuda_core(const void* w, const float* x, float* y, int64_t M, int64_t N
 // Workspace of the CUDA-core path alone (qg_workspace_size also covers the
 // Q4_0 / Q4_K tensor-core prefill, which calls with a smaller workspace skip).
 int cuda_core_workspace_size(int op, int64_t M, int64_t N, int64_t K, size_t* bytes);
+
+// ------------------------------------------------- serving operators
+// The current device's context (qg_api.cu).
+int device_ctx(const DevCtx** out);
+
+// Block-scaled fp8 (fp8_quant.cu, fp8_mm.cu).
+int fp8_quantize_launch(const DevCtx& dc, const void* x, int dtype, long long stride,
+                        uint8_t* codes, float* scales, long long M, long long K, cudaStream_t s);
+
+struct Fp8Args {
+    const uint8_t* a;
+    const float* sa;
+    const uint8_t* w;
+    const float* sw;
+    void* y;
+    int y_dtype;
+    long long M, N, K;
+};
+size_t fp8_workspace_bytes(const DevCtx& dc, const Fp8Args& a);
+int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, void* ws, size_t ws_bytes, cudaStream_t s);
+
+// Attention over a paged cache (attn_paged.cu).
+struct AttnArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const int32_t* table;
+    const int32_t* offsets;
+    const int32_t* ctx;
+    void* out;
+    float* lse;
+    long long q_stride;
+    int dtype;
+    int tokens, batch, max_new, hq, hkv, d;
+    int num_pages, page_size, width;
+    float scale, softcap;
+    int window;  // 0: none
+};
+size_t attn_workspace_bytes(const DevCtx& dc, const AttnArgs& a);
+int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, size_t ws_bytes, cudaStream_t s);
+
+// Pages of a cache (kv_pages.cu).
+struct PagePlanes {
+    uint8_t* cache;
+    long long planes, num_pages, page_bytes;
+};
+struct AppendArgs {
+    const void* k;
+    const void* v;
+    long long k_stride, v_stride;
+    int x_dtype, cache_dtype;
+    void* k_cache;
+    void* v_cache;
+    const int64_t* slots;
+    long long tokens, num_pages;
+    int heads, d, page_size;
+};
+int kv_append_launch(const DevCtx& dc, const AppendArgs& a, cudaStream_t s);
+int kv_copy_launch(const DevCtx& dc, const PagePlanes& p, const int32_t* src, const int32_t* dst,
+                   long long n, cudaStream_t s);
+struct ForkArgs {
+    PagePlanes p;
+    const int32_t *table, *lens, *refs, *parents;
+    int32_t *child_table, *child_lens, *new_refs;
+    int32_t* ws;
+    int rows, width, children, page_size;
+};
+int kv_fork_launch(const DevCtx& dc, const ForkArgs& a, cudaStream_t s);
+struct FreeArgs {
+    const int32_t *table, *lens, *refs;
+    const uint8_t* drop;
+    int32_t *new_table, *new_lens, *new_refs;
+    int rows, width, num_pages;
+};
+int kv_free_launch(const DevCtx& dc, const FreeArgs& a, cudaStream_t s);
+struct CompactArgs {
+    PagePlanes p;
+    const int32_t *table, *refs;
+    int32_t *new_table, *new_refs, *map, *live;
+    int32_t* ws;
+    int rows, width;
+};
+int kv_compact_launch(const DevCtx& dc, const CompactArgs& a, cudaStream_t s);
+
+// Log probabilities (logprobs.cu).
+struct LogprobArgs {
+    const void* x;
+    int dtype;
+    long long stride;
+    const int64_t* targets;
+    long long M, V;
+    int k;
+    float *logprobs, *entropy, *top_values;
+    int32_t *ranks, *top_ids;
+};
+size_t logprobs_workspace_bytes(const DevCtx& dc, long long M, long long V, int k);
+int logprobs_launch(const DevCtx& dc, const LogprobArgs& a, void* ws, cudaStream_t s);
 
 // Record a CUDA error for qg_last_cuda_error() and return QG_ERR_CUDA.
 int cuda_fail(cudaError_t e);

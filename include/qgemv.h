@@ -88,8 +88,9 @@ enum {
     QG_OP_Q4_K = 2,
     QG_OP_AFFINE = 3,
     QG_OP_AF4_G64 = 4,
-    QG_OP_DUAL_Q4_0_HOST = 5  /* qgemv_dual_q4_0_host: the call's own workspace plus
+    QG_OP_DUAL_Q4_0_HOST = 5, /* qgemv_dual_q4_0_host: the call's own workspace plus
                                  device staging for x, y_a, y_b */
+    QG_OP_FP8_B128 = 6        /* qmm_fp8_b128 */
 };
 
 /* Single Q4_0 projection: y[M,N] = x[M,K] . dequant(w)[N,K]^T.
@@ -256,6 +257,163 @@ QG_API int qg_prepare_af4_g64(const uint8_t* codes, const uint16_t* scales_bf16,
 QG_API int qmm_af4_g64(const float* x, const uint32_t* plane, const uint32_t* metadata, float* y,
                        int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
                        qg_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the projections of a serving step: the product with
+ * block-scaled 8-bit floating point weights, attention over a paged cache,
+ * the upkeep of the cache's pages and the log probabilities of tokens. No
+ * counterpart in the source pages: additions of this library. The
+ * conventions at the top of this file hold for all of them, with these
+ * additions: element types are named by QG_F32 / QG_F16 / QG_BF16, strides
+ * count elements, and index arrays are device memory that the kernels check
+ * as they read it (an index out of its range is never followed; the device
+ * error word records it, see qg_device_error). */
+enum { QG_F32 = 0, QG_F16 = 1, QG_BF16 = 2 };
+
+/* 8-bit floating point (e4m3) with one scale per 128 values of K.
+ *
+ * quantize_fp8_b128: codes[m, k] and scales[m, b], b = k / 128, of x[M, K]
+ * (x_dtype; rows x_stride elements apart):
+ *   scales[m, b] = max_k |x[m, k]| / 448 over block b, in f32 (1 where that
+ *                  is 0),
+ *   codes[m, k]  = the e4m3 value nearest to the f32 quotient x / scale,
+ *                  ties to even, NaN kept.
+ * A block with an infinity or a NaN gets an infinite or NaN scale.
+ * codes: M*K bytes; scales: f32 [M, ceil(K / 128)].
+ *
+ * qmm_fp8_b128: y[m, n] = sum_b a_scales[m, b] * w_scales[n / 128, b] *
+ *                         sum_{k in block b} a[m, k] * w[n, k]
+ * with e4m3 codes a[M, K], w[N, K] and f32 w_scales[ceil(N / 128),
+ * ceil(K / 128)]; y [M, N] is f32 or bf16 (y_dtype). K is any positive
+ * number (its last block may be short) and so are M and N. The products are
+ * exact and summed in f32: |y - exact| <= 1e-5 * sum |terms| + one rounding
+ * to y's type. Calls with K % 16 == 0 and 16-byte aligned a and w take the
+ * tensor cores; others a CUDA-core kernel with the same result up to the
+ * order of the sum. Workspace: qg_workspace_size(QG_OP_FP8_B128, M, N, K,
+ * 0, 0). */
+QG_API int quantize_fp8_b128(const void* x, int x_dtype, int64_t x_stride, uint8_t* codes,
+                             float* scales, int64_t M, int64_t K, qg_stream_t stream);
+QG_API int qmm_fp8_b128(const uint8_t* a, const float* a_scales, const uint8_t* w,
+                        const float* w_scales, void* y, int y_dtype, int64_t M, int64_t N,
+                        int64_t K, void* workspace, size_t workspace_bytes, qg_stream_t stream);
+
+/* The paged cache of one layer: k_cache and v_cache are [num_pages,
+ * kv_heads, page_size, head_dim] of one 16-bit type, 16-byte aligned.
+ * Sequence b's key j lies in page page_table[b, j / page_size] at place
+ * j % page_size; page_table is int32 [batch, table_width], entries that no
+ * key needs may hold anything (by custom -1). page_size: a power of two,
+ * 8..256.
+ *
+ * attn_paged: attention of new tokens over the cache that already holds
+ * their own keys and values. Sequence b's new tokens are rows q_offsets[b]
+ * .. q_offsets[b + 1] - 1 of q (none is fine) and the last of its
+ * context_lens[b] keys. Row i of n sits at position p = context_len - n + i
+ * and sees the keys j <= p and, with window > 0, j > p - window:
+ *   s_j = scale * (q . k_j), with softcap > 0: softcap * tanh(s_j / softcap)
+ *   out = sum_j exp(s_j - lse) v_j,  lse = log sum_j exp(s_j)
+ * A row that sees no key gives out = 0 and lse = -infinity. Places past
+ * context_len and pages not in the table are never part of a result,
+ * whatever they hold (NaN included). Rows of q at or after q_offsets[batch]
+ * are left alone.
+ *  - q: [tokens, q_heads, head_dim] of `dtype` (QG_F16 or QG_BF16, also the
+ *    cache's and out's), rows q_stride elements apart (a multiple of 8, q
+ *    16-byte aligned); out: the same, dense; lse: f32 [tokens, q_heads] or
+ *    NULL. Head h reads kv head h / (q_heads / kv_heads).
+ *  - head_dim 64 or 128; q_heads a multiple of kv_heads, q_heads / kv_heads
+ *    <= 128.
+ *  - max_new: no sequence has more new tokens than this (rows past it are
+ *    not computed and the device error word says so).
+ *  - Scores, sums and outputs are accumulated in f32; the probabilities
+ *    enter the product with V rounded to `dtype`.
+ *  - workspace: attn_paged_workspace_size() bytes. */
+QG_API int attn_paged(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                      const int32_t* page_table, const int32_t* q_offsets,
+                      const int32_t* context_lens, void* out, float* lse, int dtype,
+                      int64_t tokens, int64_t batch, int64_t max_new, int64_t q_heads,
+                      int64_t kv_heads, int64_t head_dim, int64_t num_pages, int64_t page_size,
+                      int64_t table_width, float scale, float softcap, int64_t window,
+                      void* workspace, size_t workspace_bytes, qg_stream_t stream);
+QG_API int attn_paged_workspace_size(int64_t tokens, int64_t batch, int64_t max_new,
+                                     int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                     size_t* bytes);
+
+/* Upkeep of a paged cache. `cache` is the cache as planes (keys and values
+ * of each layer): [planes, num_pages, page_bytes], page_bytes a multiple of
+ * 16. ref_counts int32 [num_pages] says how many table entries hold each
+ * page; 0 is a free page. The calls read their tables and counts from one
+ * set of arrays and write the new ones to another, which must not overlap
+ * it; only page contents change in place.
+ *
+ * kv_append: row t of k and v ([tokens, kv_heads, head_dim] of x_dtype, rows
+ * k_stride / v_stride elements apart) goes, rounded to cache_dtype (QG_F16 /
+ * QG_BF16), to slot slots[t] = page * page_size + place of one layer's
+ * k_cache / v_cache. A negative slot skips its row. Slots must differ.
+ *
+ * kv_copy_pages: page dst[i] = page src[i] in every plane, i < n. No page may
+ * be both a source and a destination, and destinations must differ. Pairs
+ * with a negative member are skipped.
+ *
+ * kv_fork: child c continues row parents[c] of the table: it shares the
+ * parent's whole pages and gets a page of its own with a copy of the last
+ * one if that is partly filled. Its entries after that are -1. The k-th
+ * child that needs a page takes the k-th lowest free one; if there is none,
+ * the child ends at its whole pages and the device error word says so.
+ * Writes child_table [children, table_width], child_lens [children] and
+ * new_refs [num_pages] (workspace: kv_fork_workspace_size()).
+ *
+ * kv_free: the rows with drop[r] != 0 lose their pages (entries >= 0): their
+ * entries become -1, their length 0, and each page's count falls by one per
+ * entry (not below 0; a fall below is recorded). Other rows are copied.
+ *
+ * kv_compact: moves the pages so that the pages in use are 0 .. live - 1.
+ * Those numbered live or higher go, in ascending order, to the free numbers
+ * below live, in ascending order. Writes the table and counts in the new
+ * numbers, page_map[p] = the new number of page p (-1: it was free) and
+ * live[0]. Entries that name a free page become -1. Workspace:
+ * kv_compact_workspace_size(). */
+QG_API int kv_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int x_dtype,
+                     void* k_cache, void* v_cache, int cache_dtype, const int64_t* slots,
+                     int64_t tokens, int64_t kv_heads, int64_t head_dim, int64_t num_pages,
+                     int64_t page_size, qg_stream_t stream);
+QG_API int kv_copy_pages(void* cache, int64_t planes, int64_t num_pages, int64_t page_bytes,
+                         const int32_t* src, const int32_t* dst, int64_t n, qg_stream_t stream);
+QG_API int kv_fork(void* cache, int64_t planes, int64_t num_pages, int64_t page_bytes,
+                   int64_t page_size, const int32_t* page_table, const int32_t* lens,
+                   const int32_t* ref_counts, int64_t rows, int64_t table_width,
+                   const int32_t* parents, int64_t children, int32_t* child_table,
+                   int32_t* child_lens, int32_t* new_refs, void* workspace,
+                   size_t workspace_bytes, qg_stream_t stream);
+QG_API int kv_fork_workspace_size(int64_t children, size_t* bytes);
+QG_API int kv_free(const int32_t* page_table, const int32_t* lens, const int32_t* ref_counts,
+                   const uint8_t* drop, int64_t rows, int64_t table_width, int64_t num_pages,
+                   int32_t* new_table, int32_t* new_lens, int32_t* new_refs, qg_stream_t stream);
+QG_API int kv_compact(void* cache, int64_t planes, int64_t num_pages, int64_t page_bytes,
+                      const int32_t* page_table, int64_t rows, int64_t table_width,
+                      const int32_t* ref_counts, int32_t* new_table, int32_t* new_refs,
+                      int32_t* page_map, int32_t* live, void* workspace, size_t workspace_bytes,
+                      qg_stream_t stream);
+QG_API int kv_compact_workspace_size(int64_t num_pages, size_t* bytes);
+
+/* token_logprobs: of each row of logits ([M, V] of `dtype`, rows row_stride
+ * elements apart), with lse = log sum_v exp(x[v]):
+ *   logprobs[m] = x[targets[m]] - lse,
+ *   entropy[m]  = - sum_v p[v] log p[v],  p = exp(x - lse),
+ *   ranks[m]    = how many logits are greater than the target's,
+ *   top_values[m, i], top_ids[m, i] = the top_k largest logits as log
+ *     probabilities, and their ids, largest first, ties to the lower id.
+ * A negative target stands for none: logprobs 0, ranks -1 (so does a target
+ * >= V, which the device error word records). -infinity logits are masked
+ * tokens: they add nothing to lse and entropy. A row that is all -infinity
+ * has log probabilities -infinity and entropy 0. A NaN makes a row's log
+ * probabilities and entropy NaN and counts as the largest logit.
+ * top_k <= min(32, V); with top_k = 0, top_values and top_ids may be NULL.
+ * Sums are f32. Workspace: token_logprobs_workspace_size(). */
+QG_API int token_logprobs(const void* logits, int dtype, int64_t row_stride,
+                          const int64_t* targets, int64_t M, int64_t V, int top_k,
+                          float* logprobs, float* entropy, int32_t* ranks, float* top_values,
+                          int32_t* top_ids, void* workspace, size_t workspace_bytes,
+                          qg_stream_t stream);
+QG_API int token_logprobs_workspace_size(int64_t M, int64_t V, int top_k, size_t* bytes);
 
 /* Workspace bytes op (QG_OP_*) needs for the given shape; *bytes = 0 when
  * none. group_size/packed matter only for QG_OP_AFFINE. Returns a status. */

@@ -1,0 +1,245 @@
+"""attn_paged against softmax attention in 64 bits.
+
+With u the unit roundoff of the operands' type, S a bound of the scores'
+magnitudes and A = sum_j p_j |v_j|, an output may be off by u A for the
+probabilities' rounding and u |out| for its own, doubled, 1e-5 (1 + S) A for
+the f32 scores and sums, and 2^-24 n max|v| for f16 probabilities below its
+normal range; the log-sum by 1e-5 (1 + S)."""
+import math
+
+import pytest
+import torch
+
+import bit_quantized_gemv_dequant_gb300 as qg
+
+pytestmark = pytest.mark.gpu
+
+UNIT = {torch.bfloat16: 2.0**-8, torch.float16: 2.0**-11}
+
+
+def make(seed, new, ctx, hq, hkv, d, page, dtype, strided=False, spare=3):
+    """A cache whose unused places are NaN, its pages in random order."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    counts = [-(-t // page) for t in ctx]
+    n = sum(counts) + spare
+    order = torch.randperm(n, generator=g, device="cuda").to(torch.int32)
+    k = torch.full((n, hkv, page, d), float("nan"), dtype=dtype, device="cuda")
+    v = k.clone()
+    table = torch.full((len(ctx), max(max(counts), 1) + 1), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, (c, t) in enumerate(zip(counts, ctx)):
+        for i in range(c):
+            p = int(order[at + i])
+            table[b, i] = p
+            fill = min(page, t - i * page)
+            k[p, :, :fill] = torch.randn(hkv, fill, d, generator=g, device="cuda").to(dtype)
+            v[p, :, :fill] = torch.randn(hkv, fill, d, generator=g, device="cuda").to(dtype)
+        at += c
+    off = torch.tensor([0] + new, device="cuda").cumsum(0).to(torch.int32)
+    q = torch.randn(sum(new), hq + (2 * hkv if strided else 0), d, generator=g, device="cuda").to(dtype)[:, :hq]
+    return q, k, v, table, off, torch.tensor(ctx, dtype=torch.int32, device="cuda")
+
+
+def reference(q, k, v, table, off, ctx, scale, softcap, window):
+    T, hq, d = q.shape
+    hkv, page = k.shape[1], k.shape[2]
+    out = torch.zeros(T, hq, d, dtype=torch.float64, device="cuda")
+    mass, lse = torch.zeros_like(out), torch.full((T, hq), -math.inf, dtype=torch.float64, device="cuda")
+    s_max = v_max = 0.0
+    offs = off.tolist()
+    for b, n in enumerate(ctx.tolist()):
+        c = offs[b + 1] - offs[b]
+        if not c or not n:
+            continue
+        pages = table[b, : -(-n // page)].long()
+        kk = k[pages].double().transpose(0, 1).reshape(hkv, -1, d)[:, :n].repeat_interleave(hq // hkv, 0)
+        vv = v[pages].double().transpose(0, 1).reshape(hkv, -1, d)[:, :n].repeat_interleave(hq // hkv, 0)
+        qq = q[offs[b]:offs[b + 1]].double().transpose(0, 1)
+        s = qq @ kk.transpose(1, 2) * scale
+        s_max = max(s_max, float((qq.abs() @ kk.abs().transpose(1, 2)).max()) * abs(scale))
+        v_max = max(v_max, float(vv.abs().max()))
+        if softcap:
+            s = softcap * torch.tanh(s / softcap)
+        pos = torch.arange(n - c, n, device="cuda")[:, None]
+        j = torch.arange(n, device="cuda")[None, :]
+        hide = (j > pos) | (j <= pos - window if window else False)
+        s = s.masked_fill(hide, -math.inf)
+        top = s.amax(2, keepdim=True).clamp(min=-1e300)
+        e = torch.exp(s - top)
+        z = e.sum(2, keepdim=True)
+        p = torch.where(z > 0, e / z, 0.0)
+        out[offs[b]:offs[b + 1]] = (p @ vv).transpose(0, 1)
+        mass[offs[b]:offs[b + 1]] = (p @ vv.abs()).transpose(0, 1)
+        lse[offs[b]:offs[b + 1]] = (top + torch.log(z)).squeeze(2).transpose(0, 1)
+    return out, mass, lse, s_max, v_max
+
+
+def check(args, scale=None, softcap=0.0, window=0, max_new=None):
+    q, ctx = args[0], args[5]
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    out, lse = qg.attn_paged(*args, max_new=max_new, scale=scale, softcap=softcap, window=window, return_lse=True)
+    assert qg.device_error() == 0
+    ref, mass, rl, S, vm = reference(*args, scale, softcap, window)
+    u, n = UNIT[q.dtype], int(ctx.max()) if ctx.numel() else 0
+    tol = (2 * u + 1e-5 * (1 + S)) * mass + 2 * u * ref.abs() + 2.0**-24 * n * vm
+    bad = ~((out.double() - ref).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+    empty = torch.isinf(rl)
+    assert torch.equal(torch.isinf(lse), empty) and (out[empty] == 0).all()
+    assert ((lse.double() - rl)[~empty].abs() <= 1e-5 * (1 + S)).all()
+    return out
+
+
+HEADS = [(1, 1), (4, 1), (8, 2), (6, 2), (20, 4), (32, 8), (9, 9), (32, 1)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", HEADS)
+def test_single_tokens(hq, hkv, d, dtype):
+    ctx = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300, 1025]
+    check(make(hq * d, [1] * len(ctx), ctx, hq, hkv, d, 16, dtype), max_new=1)
+
+
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256])
+@pytest.mark.parametrize("d", [64, 128])
+def test_pages_and_ragged_chunks(page, d):
+    new = [1, 0, 5, 64, 17, 130, 257, 1, 300]
+    ctx = [1, 40, 5, 100, 1000, 130, 500, 700, 2000]
+    check(make(page + d, new, ctx, 8, 2, d, page, torch.bfloat16))
+
+
+@pytest.mark.parametrize("hq,hkv", HEADS)
+def test_chunk_heads(hq, hkv):
+    check(make(hq, [70, 3, 129], [70, 300, 1000], hq, hkv, 128, 32, torch.float16))
+
+
+def test_many_queries_per_key_head():
+    check(make(3, [1, 2, 9], [100, 50, 300], 128, 1, 64, 16, torch.bfloat16))
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 100, 129, 5000])
+@pytest.mark.parametrize("softcap", [0.0, 5.0, 30.0])
+def test_window_and_cap(window, softcap):
+    check(make(window, [1, 1, 200, 70, 513], [1, 900, 200, 400, 1500], 8, 2, 64, 16, torch.float16), softcap=softcap,
+          window=window)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.3, 0.02])
+def test_scale(scale):
+    check(make(7, [1, 40, 300], [333, 40, 900], 4, 4, 64, 32, torch.bfloat16), scale=scale)
+
+
+def test_rows_that_see_nothing():
+    """More new tokens than keys: the first rows sit before the first key."""
+    args = list(make(8, [3, 5, 1, 140], [3, 5, 1, 140], 8, 2, 128, 16, torch.bfloat16))
+    args[5] = torch.tensor([1, 0, 0, 100], dtype=torch.int32, device="cuda")
+    out = check(tuple(args))
+    assert (out[:2] == 0).all() and (out[3:9] == 0).all() and (out[9:9 + 40] == 0).all()
+
+
+def test_strided_queries_and_rows_past_the_last():
+    args = make(9, [2, 130, 1], [20, 600, 90], 8, 2, 128, 16, torch.bfloat16, strided=True)
+    assert not args[0].is_contiguous()
+    check(args)
+    q = torch.cat([args[0], args[0][:5]])
+    out = torch.full((q.shape[0], 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    qg.attn_paged(q, *args[1:], out=out)
+    assert (out[-5:] == 7).all() and torch.equal(out[:-5], qg.attn_paged(*args))
+
+
+def test_large_scores():
+    """Scores to +-1000 that grow along the keys: the running maximum moves at every step."""
+    args = make(10, [1, 1, 200], [700, 2000, 900], 4, 2, 64, 16, torch.float16)
+    q, k, v, table, off, ctx = args
+    k = k * 20
+    check((q, k, v, table, off, ctx), scale=1.0)
+    page = k.shape[2]
+    for b, n in enumerate(ctx.tolist()):
+        for i in range(-(-n // page)):
+            k[int(table[b, i])] = q[0, 0] * 0 + (torch.arange(page, device="cuda") + i * page).half()[None, :, None] / 500
+    q.fill_(1.0)
+    check((q, k, v, table, off, ctx), scale=1.0)
+
+
+def test_long_context_and_offsets_past_32_bits():
+    """A cache of over 2^32 bytes per side: the pages used are its last ones."""
+    page, hkv, d = 256, 8, 128
+    n = (1 << 32) // (page * hkv * d * 2) + 40
+    k = torch.empty(n, hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    g = torch.Generator("cuda").manual_seed(1)
+    table = torch.arange(n - 1, n - 37, -1, device="cuda", dtype=torch.int32).view(1, 36)
+    k[-36:] = torch.randn(36, hkv, page, d, generator=g, device="cuda").bfloat16()
+    v[-36:] = torch.randn(36, hkv, page, d, generator=g, device="cuda").bfloat16()
+    for new, ctx in ((1, 9001), (150, 9216)):
+        q = torch.randn(new, 16, d, generator=g, device="cuda").bfloat16()
+        check((q, k, v, table, torch.tensor([0, new], dtype=torch.int32, device="cuda"),
+               torch.tensor([ctx], dtype=torch.int32, device="cuda")))
+
+
+def test_repeats_to_the_bit_on_another_stream_and_in_a_graph():
+    args = make(11, [1, 1, 1, 90], [4000, 100, 2500, 1200], 32, 8, 128, 64, torch.bfloat16)
+    a = qg.attn_paged(*args)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        b = qg.attn_paged(*args)
+        out = torch.empty_like(a)
+        need = qg._size("attn_paged_workspace_size", 93, 4, 93, 32, 8, 128)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            qg.attn_paged(*args, out=out, workspace=ws)
+    s.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(a, out)
+
+
+def test_bad_indexes_are_recorded_and_not_followed():
+    for new, ctx in (([1, 1], [300, 300]), ([130, 64], [300, 300])):
+        args = make(12, new, ctx, 8, 2, 64, 16, torch.bfloat16)
+        good = qg.attn_paged(*args)
+        table = args[3].clone()
+        table[0, 3] = 10**6
+        table[0, 5] = -5
+        out = qg.attn_paged(*args[:3], table, *args[4:])
+        assert qg.device_error() == 32
+        assert torch.equal(out[new[0]:], good[new[0]:]) and torch.isfinite(out.float()).all()
+        long = args[5].clone()
+        long[1] = 10**6  # more keys than the table has room for
+        out = qg.attn_paged(*args[:5], long)
+        assert qg.device_error() == 32 and torch.equal(out[:new[0]], good[:new[0]])
+        off = args[4].clone()
+        off[2] = 10**6
+        qg.attn_paged(*args[:4], off, args[5])
+        assert qg.device_error() == 32
+    args = make(13, [5, 2], [50, 50], 8, 2, 64, 16, torch.bfloat16)
+    qg.attn_paged(*args, max_new=3)
+    assert qg.device_error() == 32
+
+
+def test_nothing_to_do_and_refusals():
+    q, k, v, table, off, ctx = make(14, [2, 3], [20, 30], 8, 2, 64, 16, torch.bfloat16)
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert qg.attn_paged(q[:0], k, v, table, none, ctx).shape == (0, 8, 64)
+    ok = (q, k, v, table, off, ctx)
+
+    def swap(i, t):
+        return ok[:i] + (t,) + ok[i + 1:]
+
+    for bad in (swap(0, q.float()), swap(1, k.half()), swap(2, v[:, :, ::2]), swap(3, table.long()), swap(4, off[:2]),
+                swap(5, ctx[:1]), swap(5, ctx.cpu()), swap(2, v[:, :1].contiguous())):
+        with pytest.raises((ValueError, qg.QGError)):
+            qg.attn_paged(*bad)
+    for kw in (dict(softcap=-1.0), dict(window=-1), dict(scale=float("nan")), dict(max_new=-1)):
+        with pytest.raises(qg.QGError):
+            qg.attn_paged(*ok, **kw)
+    with pytest.raises(qg.QGError):  # 8 query heads on 3 key heads
+        qg.attn_paged(q, k[:, :1].repeat(1, 3, 1, 1), v[:, :1].repeat(1, 3, 1, 1), table, off, ctx)
+    with pytest.raises(qg.QGError):  # a page size of 24
+        qg.attn_paged(q, k.repeat(1, 1, 3, 1)[:, :, :24].contiguous(), v.repeat(1, 1, 3, 1)[:, :, :24].contiguous(),
+                      table, off, ctx)
+    with pytest.raises(qg.QGError):  # out over q
+        qg.attn_paged(*ok, out=q)
