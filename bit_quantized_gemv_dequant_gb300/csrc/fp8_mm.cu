@@ -2,7 +2,7 @@
 // values of K on the left and per 128 x 128 values on the right.
 #include <cuda_fp8.h>
 
-#include "serve_common.cuh"
+#include "fp8_tc.cuh"
 
 namespace qg {
 namespace {
@@ -85,7 +85,10 @@ int general_launch(const Fp8Args& a, cudaStream_t s) {
 
 size_t fp8_workspace_bytes(const DevCtx&, const Fp8Args&) { return 0; }
 
-int fp8_mm_launch(const DevCtx&, const Fp8Args& a, void*, size_t, cudaStream_t s) {
+int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, void*, size_t, cudaStream_t s) {
+    const bool tma = a.K % 16 == 0 && reinterpret_cast<uintptr_t>(a.a) % 16 == 0 &&
+                     reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
+    if (tma) return a.M <= 128 ? fp8::launch_swap(dc, a, s) : fp8::launch_tile(dc, a, s);
     return a.y_dtype == QG_F32 ? general_launch<float>(a, s) : general_launch<__nv_bfloat16>(a, s);
 }
 

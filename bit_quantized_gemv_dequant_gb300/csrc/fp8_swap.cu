@@ -1,0 +1,298 @@
+// qmm_fp8_b128 for few rows of a: 128 rows of w on the tensor cores' M side, the
+// rows of a on the N side, K split over a thread-block cluster.
+#include <algorithm>
+
+#include "fp8_tc.cuh"
+
+namespace qg {
+namespace fp8 {
+namespace {
+
+// One CTA: 128 rows of w (one block of scales) times BN rows of a, over its
+// share of the 128-wide k blocks. Bound by the bytes of w, so the shape is
+// chosen for loads in flight: the ring holds up to 200 KB, and N / 128 tiles
+// times the split give about one CTA per SM.
+//
+//   warp 0    TMA producer: w tile and a tile of each k block.
+//   warp 1    issues the four MMAs of a k block into an accumulator of its own
+//             (kBufs of them in tensor memory).
+//   warps 4-7 take the accumulators into registers, times
+//             a_scale[m, b] * w_scale[n / 128, b] (f32): thread = row of w.
+//
+// The split's partial sums meet in shared memory over the cluster, each CTA
+// adding up its share of the rows of a in the order of the split: the result
+// does not depend on timing. Threads of a warp hold consecutive n, so stores
+// of y are coalesced.
+constexpr int kThreads = 256;
+constexpr int kScaleBlocks = 16;  // k blocks whose scales are staged at a time
+
+template <int BN>
+struct Geo {
+    static constexpr int kStage = 16384 + BN * 128;
+    static constexpr int kStages = BN == 128 ? 6 : BN == 64 ? 8 : 10;
+    static constexpr int kBufs = BN == 128 ? 4 : 8;       // accumulators of BN columns
+    static constexpr int kCols = kBufs * BN < 32 ? 32 : kBufs * BN;
+    static constexpr int kScaleOff = kStages * kStage;
+    static constexpr int kBarOff = kScaleOff + kScaleBlocks * BN * 4;
+    static constexpr int kSmem = 1024 + kBarOff + 512;
+    static_assert(BN * 128 * 4 <= kStages * kStage, "partial sums reuse the ring");
+    static_assert(8 * (2 * kStages + 2 * kBufs + 1) + 8 <= 512, "barriers");
+};
+
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+template <int BN, class TY>
+__global__ void __launch_bounds__(kThreads, 1)
+    swap_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                const Params p) {
+    using G = Geo<BN>;
+    constexpr uint32_t kDesc = f8_idesc(128, BN);
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    float* scales = reinterpret_cast<float*>(smem + G::kScaleOff);
+    const uint32_t bars = base + G::kBarOff;
+    auto full = [&](int i) { return bars + 8u * i; };
+    auto empty = [&](int i) { return bars + 8u * (G::kStages + i); };
+    auto t_full = [&](int i) { return bars + 8u * (2 * G::kStages + i); };
+    auto t_empty = [&](int i) { return bars + 8u * (2 * G::kStages + G::kBufs + i); };
+    const uint32_t done = bars + 8u * (2 * G::kStages + 2 * G::kBufs);
+    uint32_t* slot = reinterpret_cast<uint32_t*>(smem + G::kBarOff + 8 * (2 * G::kStages + 2 * G::kBufs + 1));
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = (int)gridDim.x, rank = (int)blockIdx.x;
+    const int n0 = (int)blockIdx.y * 128, m0 = (int)blockIdx.z * BN;
+    const int b0 = (int)((long long)p.KB * rank / split), b1 = (int)((long long)p.KB * (rank + 1) / split);
+    const int nb = b1 - b0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < G::kStages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < G::kBufs; ++i) {
+            mbar_init(t_full(i), 1);
+            mbar_init(t_empty(i), 4);
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+        prefetch_tmap(&map_w);
+        prefetch_tmap(&map_a);
+    }
+    if (warp == 1) tmem_alloc(smem_addr(slot), G::kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    pdl_trigger();
+    pdl_wait();
+
+    float2 acc[BN / 2];
+#pragma unroll
+    for (int i = 0; i < BN / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+    const int row = (warp & 3) * 32 + lane;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int i = 0; i < nb; ++i) {
+                const int st = i % G::kStages;
+                if (i >= G::kStages && !mbar_wait_sleep(empty(st), ((i / G::kStages) & 1) ^ 1)) {
+                    report_error(p.err, DEVERR_TC_WAIT);
+                    break;
+                }
+                const uint32_t sb = base + st * G::kStage;
+                mbar_arrive_expect_tx(full(st), G::kStage);
+                tma_load_2d(sb, &map_w, (b0 + i) * 128, n0, full(st));
+                tma_load_2d(sb + 16384, &map_a, (b0 + i) * 128, m0, full(st));
+                issued = i + 1;
+            }
+            for (int i = max(0, issued - G::kStages); i < issued; ++i)
+                if (!mbar_wait(full(i % G::kStages), (i / G::kStages) & 1))
+                    report_error(p.err, DEVERR_WAIT_DRAIN);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int i = 0; i < nb; ++i) {
+                const int st = i % G::kStages, tb = i % G::kBufs;
+                if (!mbar_wait(full(st), (i / G::kStages) & 1) ||
+                    (i >= G::kBufs && !mbar_wait(t_empty(tb), ((i / G::kBufs) & 1) ^ 1))) {
+                    report_error(p.err, DEVERR_TC_WAIT);
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t dw = sw128_desc(base + st * G::kStage);
+                const uint64_t da = sw128_desc(base + st * G::kStage + 16384);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_f8(tmem + tb * BN, dw + 2 * k, da + 2 * k, kDesc, k > 0);
+                tc_commit(empty(st));
+                tc_commit(t_full(tb));
+            }
+            tc_commit(done);
+            if (!mbar_wait(done, 0)) report_error(p.err, DEVERR_WAIT_DRAIN);
+        }
+    } else if (warp >= 4) {
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const float* sw = p.sw + (long long)blockIdx.y * p.KB + b0;
+        for (int i0 = 0; i0 < nb; i0 += kScaleBlocks) {
+            // The scales of the next blocks: [block][row of a], both factors in one.
+            const int nk = min(kScaleBlocks, nb - i0);
+            if (i0) named_bar_sync(1, 128);
+            for (int j = threadIdx.x - 128; j < nk * BN; j += 128) {
+                const int m = j / nk, b = j % nk;  // consecutive threads, consecutive blocks of a row
+                scales[b * BN + m] = m0 + m < p.M
+                    ? __ldg(p.sa + (long long)(m0 + m) * p.KB + b0 + i0 + b) * __ldg(sw + i0 + b) : 0.f;
+            }
+            named_bar_sync(1, 128);
+            for (int b = 0; b < nk; ++b) {
+                const int i = i0 + b, tb = i % G::kBufs;
+                if (!warp_wait(t_full(tb), (i / G::kBufs) & 1)) {
+                    if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
+                    i0 = nb;  // the sums are lost; the barriers below are still met
+                    break;
+                }
+                tc_fence_after();
+                const float4* sc = reinterpret_cast<const float4*>(scales + b * BN);
+                constexpr int kChunk = BN < 32 ? 16 : 32;
+#pragma unroll
+                for (int c = 0; c < BN; c += kChunk) {
+                    uint32_t r[kChunk];
+                    if constexpr (kChunk == 16) {
+                        tmem_ld16(tmem + lanes + tb * BN + c, r);
+                    } else {
+                        tmem_ld32_async(tmem + lanes + tb * BN + c, r);
+                        tmem_wait32(r);
+                    }
+                    if (c + kChunk == BN) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(t_empty(tb));
+                    }
+#pragma unroll
+                    for (int j = 0; j < kChunk; j += 4) {
+                        const float4 s = sc[(c + j) / 4];
+                        float2& a0 = acc[(c + j) / 2];
+                        float2& a1 = acc[(c + j) / 2 + 1];
+                        a0 = fma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                  make_float2(s.x, s.y), a0);
+                        a1 = fma2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                                  make_float2(s.z, s.w), a1);
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    TY* y = static_cast<TY*>(p.y);
+    const long long n = n0 + row;
+    if (split == 1) {
+        if (warp >= 4 && n < p.N) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+                if (m0 + c < p.M) y[(m0 + c) * (long long)p.N + n] = from_f32<TY>(c & 1 ? acc[c / 2].y : acc[c / 2].x);
+        }
+    } else {
+        float* part = reinterpret_cast<float*>(smem);  // [row of a][row of w]; the ring is idle
+        const int rows = min(BN, p.M - m0);
+        if (warp >= 4) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+                if (c < rows) part[c * 128 + row] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
+        }
+        cluster_arrive();
+        cluster_wait();
+        for (int e = rank * kThreads + threadIdx.x; e < rows * 128; e += split * kThreads) {
+            float v = 0.f;
+            for (int r = 0; r < split; ++r) v += ld_cluster(base + e * 4, r);
+            const long long m = m0 + e / 128, col = n0 + e % 128;
+            if (col < p.N) y[m * p.N + col] = from_f32<TY>(v);
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, G::kCols);
+    }
+}
+
+template <int BN, class TY>
+int launch(const DevCtx& dc, const Fp8Args& a, int split, cudaStream_t s) {
+    using G = Geo<BN>;
+    static int configured[64] = {0};
+    auto kern = swap_kernel<BN, TY>;
+    if (!configured[dc.device]) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        configured[dc.device] = 1;
+    }
+    CUtensorMap mw, ma;
+    int rc = code_map(&mw, a.w, a.N, a.K, 128);
+    if (rc == QG_OK) rc = code_map(&ma, a.a, a.M, a.K, BN);
+    if (rc) return rc;
+    const Params p{a.sa, a.sw, a.y, (int)a.M, (int)a.N, (int)((a.K + 127) / 128), false, dc.err};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)split, (unsigned)((a.N + 127) / 128), (unsigned)((a.M + BN - 1) / BN));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = G::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, ma, p);
+    return e == cudaSuccess ? QG_OK : cuda_fail(e);
+}
+
+template <int BN>
+int launch_bn(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
+    // About one CTA per SM, at least two k blocks each.
+    const long long tiles = ((a.N + 127) / 128) * ((a.M + BN - 1) / BN), kb = (a.K + 127) / 128;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= dc.num_sms && kb >= split * 4) split *= 2;
+    return a.y_dtype == QG_F32 ? launch<BN, float>(dc, a, split, s) : launch<BN, __nv_bfloat16>(dc, a, split, s);
+}
+
+}  // namespace
+
+int launch_swap(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
+    if (a.M <= 16) return launch_bn<16>(dc, a, s);
+    if (a.M <= 32) return launch_bn<32>(dc, a, s);
+    if (a.M <= 64) return launch_bn<64>(dc, a, s);
+    return launch_bn<128>(dc, a, s);
+}
+
+int code_map(CUtensorMap* m, const uint8_t* ptr, long long rows, long long cols, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    int rc = encoder(&encode);
+    if (rc) return rc;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, es[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(ptr), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QG_OK
+               : QG_ERR_UNSUPPORTED;
+}
+
+}  // namespace fp8
+}  // namespace qg
