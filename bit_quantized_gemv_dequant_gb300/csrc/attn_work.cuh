@@ -1,0 +1,237 @@
+// How attn_paged's work is cut up, and the pieces its kernels share.
+//
+// The rows of one sequence and key head are its new tokens times the query
+// heads of the group, row r = token * group + head, in tiles of RT rows. A row
+// tile meets the keys that any of its rows sees in tiles of KT keys. All
+// (row tile, key tile) pairs of the batch, in the order sequence, key head,
+// row tile, key tile, are one line of W steps; CTA c of G takes the steps
+// W c / G .. W (c + 1) / G - 1, so every CTA has the same work to within one
+// step whatever the lengths. Where a cut falls inside a row tile its parts
+// leave (m, l, O) in the workspace and combine_kernel joins them, in the order
+// of the keys. A CTA has at most two such parts: its first segment (slot 0)
+// and its last (slot 1).
+#pragma once
+
+#include "fp8_tc.cuh"
+
+namespace qg {
+namespace attn {
+
+using fp8::pdl_trigger;
+using fp8::pdl_wait;
+using prefill::prefetch_tmap;
+using prefill::warp_wait;
+using prefill::warp_wait_sleep;
+
+struct Work {
+    AttnArgs a;
+    int group;
+    int rows_min, rows_max;  // sequences with rows in (rows_min, rows_max]
+    float scale_log2;        // scale * log2(e); without a cap scores go straight to base 2
+    float cap_in, cap_out;   // 2 log2(e) scale / softcap, softcap * log2(e)
+    float* part;             // [G][2][RT][D] unnormalised outputs of cut row tiles
+    float2* ml;              // [G][2][RT] their maximum (base 2) and sum
+    int ctas;
+    unsigned* err;
+};
+
+struct Seq {
+    int first, n, rows, ctx;  // rows: 0 where this kernel has nothing to do
+};
+
+__device__ __forceinline__ Seq seq_at(const Work& w, int b) {
+    Seq s;
+    const int lo = w.a.offsets[b], hi = w.a.offsets[b + 1];
+    s.first = lo;
+    s.n = hi - lo;
+    s.ctx = w.a.ctx[b];
+    bool bad = lo < 0 || hi < lo || hi > w.a.tokens;
+    if (bad) s.n = 0;
+    const long long most = (long long)w.a.width * w.a.page_size;
+    if (s.ctx < 0 || s.ctx > most) {
+        bad = true;
+        s.ctx = s.ctx < 0 ? 0 : (int)most;
+    }
+    bad |= s.n > w.a.max_new;
+    if (bad) report_error(w.err, DEVERR_INDEX);
+    s.rows = min(s.n, w.a.max_new) * w.group;
+    if (s.rows <= w.rows_min || s.rows > w.rows_max) s.rows = 0;
+    return s;
+}
+
+// The key tiles [lo, hi) that row tile i meets, and the first key that none of
+// its rows sees. A row tile that sees nothing has one (empty) step.
+struct Span {
+    int lo, hi, end;
+};
+template <int RT, int KT>
+__device__ __forceinline__ Span span_of(const Work& w, const Seq& s, int i) {
+    const int r0 = i * RT, r1 = min(s.rows, r0 + RT) - 1;
+    const int first = s.ctx - s.n + r0 / w.group, last = s.ctx - s.n + r1 / w.group;
+    Span p;
+    p.end = last + 1;
+    if (p.end <= 0) return Span{0, 1, 0};
+    p.lo = w.a.window ? max(0, first - w.a.window + 1) / KT : 0;
+    p.hi = (p.end + KT - 1) / KT;
+    return p;
+}
+
+template <int RT, int KT>
+__device__ __forceinline__ long long steps_of(const Work& w, const Seq& s) {
+    long long t = 0;
+    for (int i = 0; i * RT < s.rows; ++i) {
+        const Span p = span_of<RT, KT>(w, s, i);
+        t += p.hi - p.lo;
+    }
+    return t;
+}
+
+// Where a step lies: sequence, key head, row tile, and how many steps of the
+// row tile come before it. b = batch: past the end.
+struct Place {
+    int b, head, tile;
+    int at;
+};
+
+// Places of step `t` (t < W gives a sequence), found by the whole block of NT
+// threads: a scan over the sequences, then the head and the tile in it.
+// scratch: NT / 32 + 4 long longs of shared memory.
+template <int RT, int KT, int NT>
+__device__ Place locate(const Work& w, long long t, long long* total, long long* scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long before = 0;
+    Place at{w.a.batch, 0, 0, 0};
+    long long* found = scratch + NT / 32;
+    if (threadIdx.x == 0) found[0] = -1;
+    for (int b0 = 0; b0 < w.a.batch; b0 += NT) {
+        const int b = b0 + threadIdx.x;
+        long long v = 0;
+        if (b < w.a.batch) v = steps_of<RT, KT>(w, seq_at(w, b)) * w.a.hkv;
+        long long x = v;
+#pragma unroll
+        for (int i = 1; i < 32; i *= 2) {
+            const long long o = __shfl_up_sync(0xFFFFFFFFu, x, i);
+            if (lane >= i) x += o;
+        }
+        __syncthreads();
+        if (lane == 31) scratch[warp] = x;
+        __syncthreads();
+        long long base = before, all = 0;
+        for (int i = 0; i < NT / 32; ++i) {
+            if (i < warp) base += scratch[i];
+            all += scratch[i];
+        }
+        const long long begin = base + x - v;
+        if (t >= begin && t < begin + v) {
+            found[0] = b;
+            found[1] = t - begin;
+        }
+        before += all;
+    }
+    __syncthreads();
+    *total = before;
+    const long long b = found[0], rest = found[1];
+    __syncthreads();
+    if (b < 0) return at;
+    const Seq s = seq_at(w, (int)b);
+    const long long per = steps_of<RT, KT>(w, s);
+    at.b = (int)b;
+    at.head = (int)(rest / per);
+    long long left = rest % per;
+    for (;; ++at.tile) {
+        const Span p = span_of<RT, KT>(w, s, at.tile);
+        if (left < p.hi - p.lo) break;
+        left -= p.hi - p.lo;
+    }
+    at.at = (int)left;
+    return at;
+}
+
+__device__ __forceinline__ long long cut(long long total, int c, int ctas) { return total * c / ctas; }
+
+// Walks the segments of a CTA's steps: for each, a row tile and the key tiles
+// lo .. hi - 1 of it that are this CTA's.
+template <int RT, int KT>
+struct Walk {
+    const Work& w;
+    long long left;   // steps still to do
+    Place p;
+    Seq s;
+    Span span;
+    int lo, hi;
+    bool whole;       // the segment is its row tile's only one
+    int slot;         // where its part goes if not
+    bool first;
+
+    __device__ Walk(const Work& work, const Place& at, long long n) : w(work), left(n), p(at), first(true) {
+        if (left > 0) {
+            s = seq_at(w, p.b);
+            span = span_of<RT, KT>(w, s, p.tile);
+        }
+    }
+    __device__ bool next() {
+        if (left <= 0) return false;
+        if (!first) {  // the row tile after the one just done
+            p.at = 0;
+            ++p.tile;
+            if (p.tile * RT >= s.rows) {
+                p.tile = 0;
+                if (++p.head == w.a.hkv) {
+                    p.head = 0;
+                    do s = seq_at(w, ++p.b);
+                    while (s.rows == 0);  // steps are left, so one with rows follows
+                }
+            }
+            span = span_of<RT, KT>(w, s, p.tile);
+        }
+        lo = span.lo + p.at;
+        const int n = (int)min((long long)(span.hi - lo), left);
+        hi = lo + n;
+        left -= n;
+        whole = lo == span.lo && hi == span.hi;
+        slot = first ? 0 : 1;
+        first = false;
+        return true;
+    }
+};
+
+// Key `j` of sequence b: its page's number, or num_pages (whose rows TMA fills
+// with zeros) where the table holds no page.
+__device__ __forceinline__ int page_of(const Work& w, int b, int j) {
+    const int page = w.a.table[(long long)b * w.a.width + j / w.a.page_size];
+    if (page >= 0 && page < w.a.num_pages) return page;
+    report_error(w.err, DEVERR_INDEX);
+    return w.a.num_pages;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Score of a dot product, in base 2: softcap * tanh(scale x / softcap) with
+// tanh(z) = 1 - 2 / (1 + e^2z), whose absolute error is a few 2^-24.
+template <bool CAP>
+__device__ __forceinline__ float score(const Work& w, float x) {
+    if (!CAP) return x * w.scale_log2;
+    return w.cap_out * (1.f - __fdividef(2.f, 1.f + ex2(fminf(x * w.cap_in, 126.f))));
+}
+
+// Largest grid and workspace; see attn_paged.cu.
+int launch_few(const DevCtx& dc, const Work& w, int row_blocks, cudaStream_t s);
+
+// A map of k or v: [num_pages][hkv * page_size][d], boxes of `rows` x 64 values.
+int cache_map(CUtensorMap* m, const AttnArgs& a, const void* p, int rows);
+
+}  // namespace attn
+}  // namespace qg
