@@ -1,0 +1,470 @@
+// attn_paged for chunks of new tokens: bound by the tensor cores and by the
+// exponentials.
+#include <algorithm>
+
+#include "attn_join.cuh"
+
+namespace qg {
+namespace attn {
+namespace {
+
+using namespace prefill;
+using fp8::fma2;
+using fp8::tmem_alloc;
+using fp8::tmem_dealloc;
+using fp8::tmem_ld32_async;
+using fp8::tmem_wait32;
+
+// A row tile is two blocks of 128 rows, a step 128 keys. Both blocks share the
+// keys and values in shared memory, and while one block's scores are turned
+// into probabilities by its warpgroup the tensor cores work on the other's:
+//
+//   S_t = Q_t K^T        t = 0, 1; 128 x 128 f32 in tensor memory
+//   P_t = 2^(s S_t - m)  by warpgroup t, thread = row; over S_t's columns
+//   O_t += P_t V         P_t from tensor memory
+//
+// in the order S0 S1 | O0 S0' O1 S1' | O0' S0'' ..., where the MMAs that one
+// thread issues run in order, so that S_t' may overwrite P_t and "S_t' is
+// there" implies "O_t is up to date".
+//
+// The maximum m follows the scores lazily: O and the sum are rescaled only when
+// a row's new maximum is over 2^8 times the one in use (probabilities up to
+// 2^8 cost nothing in f16 or bf16, and the quotient by the sum is the same).
+// Rows past the last one repeat it; their results are not stored.
+//
+//   warps 0-3, 4-7  softmax and output of block 0, 1
+//   warp 8          TMA producer: ring of K and V tiles, taken alternately
+//   warp 9          MMA issuer
+//   warps 10-11     gather Q into shared memory
+constexpr int kKT = 128;
+constexpr int kRT = 256;
+constexpr int kThreads = 384;
+constexpr float kLazy = 8.f;
+
+template <int D>
+struct Geo {
+    static constexpr int kHalf = 128 * 128;            // 64 columns of 128 rows
+    static constexpr int kTile = kHalf * (D / 64);     // one K, V or Q block
+    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kRingOff = 2 * kTile;
+    static constexpr int kBarOff = kRingOff + kStages * kTile;
+    static constexpr int kScratchOff = kBarOff + 16 * kStages + 128;
+    static constexpr int kSmem = 1024 + kScratchOff + 256;
+    static constexpr uint32_t kO = 256;                // tensor memory: S0, S1, O0, O1
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Operand with its rows along the product's inner dimension (V: a row is a
+// key): 128-byte-swizzled atoms of 64 columns x 8 rows, atoms of the next 8
+// rows 1024 bytes on, of the next 64 columns `half` bytes on.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t half) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(half >> 4) << 16) | (64ull << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+template <class T>
+constexpr uint32_t idesc(int n, bool b_rows_are_k) {
+    constexpr uint32_t type = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
+    return (1u << 4) | (type << 7) | (type << 10) | (b_rows_are_k ? 1u << 16 : 0u) |
+           ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void fence_async_proxy() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// GEN: scores are formed one by one first (a cap, or a scale that is not
+// positive, under which the largest dot product need not be the largest score).
+template <class T, int D, bool GEN>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const Work w) {
+    using G = Geo<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const uint32_t bars = base + G::kBarOff;
+    auto full = [&](int i) { return bars + 8u * i; };
+    auto empty = [&](int i) { return bars + 8u * (G::kStages + i); };
+    const uint32_t more = bars + 16u * G::kStages;
+    auto s_full = [&](int t) { return more + 8u * t; };
+    auto p_full = [&](int t) { return more + 16u + 8u * t; };
+    auto o_full = [&](int t) { return more + 32u + 8u * t; };
+    const uint32_t q_full = more + 48u, q_free = more + 56u, tail = more + 64u, done = more + 72u;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(smem + G::kBarOff + 16 * G::kStages + 80);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < G::kStages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full(t), 1);
+            mbar_init(p_full(t), 4);
+            mbar_init(o_full(t), 1);
+        }
+        mbar_init(q_full, 2);
+        mbar_init(q_free, 1);
+        mbar_init(tail, 1);
+        mbar_init(done, 1);
+        fence_mbar_init();
+        prefetch_tmap(&map_k);
+        prefetch_tmap(&map_v);
+    }
+    if (warp == 9) tmem_alloc(smem_addr(slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    pdl_trigger();
+    pdl_wait();
+    long long total;
+    long long* scratch = reinterpret_cast<long long*>(smem + G::kScratchOff);
+    locate<kRT, kKT, kThreads>(w, -1, &total, scratch);
+    const long long begin = cut(total, blockIdx.x, w.ctas), n = cut(total, blockIdx.x + 1, w.ctas) - begin;
+    if (n > 0) {
+        const Place place = locate<kRT, kKT, kThreads>(w, begin, &total, scratch);
+        Walk<kRT, kKT> walk(w, place, n);
+        bool ok = true;
+        if (warp == 8) {
+            // -------------------------------------------------------- producer
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            const int rows = min(w.a.page_size, kKT);
+            int i = 0, tails = 0;
+            while (ok && walk.next()) {
+                for (int t = walk.lo; ok && t < walk.hi; ++t) {
+                    const int keys = max(0, min(kKT, walk.span.end - t * kKT));
+                    const int copies = (keys + rows - 1) / rows;
+                    int page = 0, y = 0;
+                    if (lane < copies) {
+                        const int j = t * kKT + lane * rows;
+                        page = page_of(w, walk.p.b, j);
+                        y = walk.p.head * w.a.page_size + j % w.a.page_size;
+                    }
+                    for (int kv = 0; kv < 2; ++kv, ++i) {
+                        const int st = i % G::kStages;
+                        if (i >= G::kStages && !warp_wait_sleep(empty(st), ((i / G::kStages) & 1) ^ 1)) {
+                            if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
+                            ok = false;
+                            break;
+                        }
+                        const bool part = kv && keys < kKT;  // values past the last key are cleared
+                        const uint32_t bar = part ? tail : full(st);
+                        const uint32_t dst = base + G::kRingOff + st * G::kTile;
+                        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(copies * rows * D * 2));
+                        __syncwarp();
+                        if (lane < copies) {
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_3d(dst + h * G::kHalf + lane * rows * 128, kv ? &map_v : &map_k, h * 64, y,
+                                            page, bar);
+                        }
+                        if (part) {
+                            if (!warp_wait(tail, tails & 1)) {
+                                if (lane == 0) report_error(w.err, DEVERR_WAIT_DRAIN);
+                                ok = false;
+                            }
+                            ++tails;
+                            uint4* v = reinterpret_cast<uint4*>(smem + G::kRingOff + st * G::kTile);
+                            for (int h = 0; h < D / 64; ++h)
+                                for (int e = keys * 8 + lane; e < kKT * 8; e += 32)
+                                    v[h * (G::kHalf / 16) + e] = make_uint4(0u, 0u, 0u, 0u);
+                            fence_async_proxy();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(full(st));
+                        }
+                    }
+                }
+            }
+            for (int j = max(0, i - G::kStages); j < i; ++j)
+                if (!warp_wait(full(j % G::kStages), (j / G::kStages) & 1) && lane == 0)
+                    report_error(w.err, DEVERR_WAIT_DRAIN);
+        } else if (warp == 9) {
+            // ------------------------------------------------------------- MMA
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            if (lane == 0) {
+                constexpr uint32_t kQK = idesc<T>(128, false), kPV = idesc<T>(D, true);
+                int i = 0, seg = 0;       // ring entries, segments
+                int steps[2] = {0, 0};    // steps of each block
+                auto wait = [&](uint32_t bar, uint32_t parity) {
+                    if (ok && !mbar_wait(bar, parity)) {
+                        report_error(w.err, DEVERR_TC_WAIT);
+                        ok = false;
+                    }
+                    return ok;
+                };
+                auto score_mma = [&](int t, int st) {
+                    const uint32_t q = base + t * G::kTile, k = base + G::kRingOff + st * G::kTile;
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            mma_ss(tmem + t * 128, sw128_desc(q + h * G::kHalf) + 2 * c,
+                                   sw128_desc(k + h * G::kHalf) + 2 * c, kQK, h + c > 0);
+                    tc_commit(s_full(t));
+                };
+                auto out_mma = [&](int t, int st, bool acc) {
+                    const uint64_t v = mn_desc(base + G::kRingOff + st * G::kTile, G::kHalf);
+#pragma unroll
+                    for (int c = 0; c < kKT / 16; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
+                        tc_mma_ts(tmem + G::kO + t * D, tmem + t * 128 + c * 8, v + c * 128, kPV, acc || c > 0);
+                };
+                while (ok && walk.next()) {
+                    const bool two = walk.s.rows - walk.p.tile * kRT > 128;
+                    const int nt = walk.hi - walk.lo;
+                    if (!wait(q_full, seg & 1) || !wait(full(i % G::kStages), (i / G::kStages) & 1)) break;
+                    tc_fence_after();
+                    score_mma(0, i % G::kStages);
+                    if (two) score_mma(1, i % G::kStages);
+                    tc_commit(empty(i % G::kStages));
+                    if (nt == 1) tc_commit(q_free);
+                    ++i;
+                    for (int j = 0; j < nt; ++j) {
+                        const int vs = i % G::kStages, ks = (i + 1) % G::kStages;
+                        if (!wait(full(vs), (i / G::kStages) & 1) || !wait(p_full(0), steps[0]++ & 1)) break;
+                        tc_fence_after();
+                        out_mma(0, vs, j > 0);
+                        const bool last = j + 1 == nt;
+                        if (last) {
+                            tc_commit(o_full(0));
+                        } else {
+                            if (!wait(full(ks), ((i + 1) / G::kStages) & 1)) break;
+                            tc_fence_after();
+                            score_mma(0, ks);
+                        }
+                        if (two) {
+                            if (!wait(p_full(1), steps[1]++ & 1)) break;
+                            tc_fence_after();
+                            out_mma(1, vs, j > 0);
+                        }
+                        tc_commit(empty(vs));
+                        if (last) {
+                            if (two) tc_commit(o_full(1));
+                            ++i;
+                        } else {
+                            if (two) score_mma(1, ks);
+                            tc_commit(empty(ks));
+                            if (j + 2 == nt) tc_commit(q_free);
+                            i += 2;
+                        }
+                    }
+                    ++seg;
+                }
+                tc_commit(done);
+                if (!mbar_wait(done, 0)) report_error(w.err, DEVERR_WAIT_DRAIN);
+            }
+        } else if (warp >= 10) {
+            // --------------------------------------------------------------- Q
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            int seg = 0;
+            while (ok && walk.next()) {
+                if (seg && !warp_wait_sleep(q_free, (seg - 1) & 1)) {
+                    if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
+                    ok = false;
+                    break;
+                }
+                const int r0 = walk.p.tile * kRT;
+                const int n_rows = walk.s.rows - r0 > 128 ? 256 : 128;
+                constexpr int C = D / 8;  // 16-byte chunks per row
+                for (int e = (int)threadIdx.x - 320; e < n_rows * C; e += 64) {
+                    const int row = e / C, c = e % C, r = min(r0 + row, walk.s.rows - 1);
+                    const T* src = static_cast<const T*>(w.a.q) +
+                                   (long long)(walk.s.first + r / w.group) * w.a.q_stride +
+                                   (long long)(walk.p.head * w.group + r % w.group) * D + c * 8;
+                    const int rr = row % 128;
+                    cp_async16(base + (row / 128) * G::kTile + (c / 8) * G::kHalf + rr * 128 +
+                                   (((c & 7) ^ (rr & 7)) << 4), src);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+                ++seg;
+            }
+        } else {
+            // --------------------------------------------------------- softmax
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+            const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + G::kO + t * D;
+            int steps = 0, seg = 0;
+            while (walk.next()) {
+                const Seq s = walk.s;
+                const int r0 = walk.p.tile * kRT, nt = walk.hi - walk.lo;
+                if (s.rows - r0 <= t * 128) continue;  // no such block
+                const int r = min(r0 + t * 128 + row, s.rows - 1);
+                const int pos = s.ctx - s.n + r / w.group;
+                const int pos_lo = __shfl_sync(0xFFFFFFFFu, pos, 0), pos_hi = __shfl_sync(0xFFFFFFFFu, pos, 31);
+                float m = -INFINITY, l = 0.f;
+                for (int j = 0; j < nt; ++j, ++steps) {
+                    const int j0 = (walk.lo + j) * kKT;
+                    if (ok && !warp_wait(s_full(t), steps & 1)) {
+                        if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
+                        ok = false;  // the results are lost; the barriers are still met
+                    }
+                    tc_fence_after();
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32_async(s_at + c * 32, x[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_wait32(x[c]);
+                    if constexpr (GEN) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float v = __uint_as_float(x[c][e]);
+                                x[c][e] = __float_as_uint(w.a.softcap > 0.f ? score<true>(w, v) : score<false>(w, v));
+                            }
+                    }
+                    if (j0 + kKT - 1 > pos_lo || (w.a.window && j0 <= pos_hi - w.a.window)) {
+                        const int hi = pos - j0;                                       // last key seen
+                        const int lo = w.a.window ? pos - w.a.window - j0 : -1;        // first key seen - 1
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (c * 32 + e > hi || c * 32 + e <= lo) x[c][e] = 0xFF800000u;
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            top = fmaxf(top, fmaxf(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
+                    if (!GEN) top *= w.scale_log2;
+                    if (__any_sync(0xFFFFFFFFu, top > m + kLazy)) {
+                        const float mn = fmaxf(m, top);
+                        const float f = ex2(m - (mn == -INFINITY ? 0.f : mn));
+                        m = mn;
+                        l *= f;
+                        if (j) {
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(o_at + c, o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(o_at + c, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const float2 sc = make_float2(GEN ? 1.f : w.scale_log2, GEN ? 1.f : w.scale_log2);
+                    const float2 off = make_float2(-ref, -ref);
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 v = fma2(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc, off);
+                            v.x = ex2(v.x);
+                            v.y = ex2(v.y);
+                            sum = __fadd2_rn(sum, v);
+                            p[e / 2] = pack2<T>(v.x, v.y);
+                        }
+                        tmem_st16(s_at + c * 16, p);
+                    }
+                    l += sum.x + sum.y;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(t));
+                }
+                // ------------------------------------------- end of a segment
+                if (ok && !warp_wait(o_full(t), seg & 1)) {
+                    if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
+                    ok = false;
+                }
+                ++seg;
+                tc_fence_after();
+                const bool live = r0 + t * 128 + row < s.rows;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const long long at = (long long)(s.first + r / w.group) * w.a.hq + walk.p.head * w.group + r % w.group;
+                const long long pt = ((long long)blockIdx.x * 2 + walk.slot) * kRT + t * 128 + row;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    __syncwarp();
+                    tmem_ld16(o_at + c, o);
+                    if (live && walk.whole) {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            h[e] = pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(w.a.out) + at * D + c);
+                        dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                        dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                    } else if (live) {
+                        uint4* dst = reinterpret_cast<uint4*>(w.part + pt * D + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+                tc_fence_before();
+                if (live) {
+                    if (!walk.whole) w.ml[pt] = make_float2(m, l);
+                    else if (w.a.lse) w.a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <class T, int D, bool GEN>
+int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
+    static int configured[64] = {0};
+    auto kern = chunk_kernel<T, D, GEN>;
+    if (!configured[dc.device]) {
+        int rc = fp8::check_register_split(kern, kThreads, 256 * 216 + 128 * 72);
+        if (rc) return rc;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        configured[dc.device] = 1;
+    }
+    CUtensorMap mk, mv;
+    const int rows = std::min(w.a.page_size, kKT);
+    int rc = cache_map(&mk, w.a, w.a.k, rows);
+    if (rc == QG_OK) rc = cache_map(&mv, w.a, w.a.v, rows);
+    if (rc == QG_OK) rc = launch(kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
+    if (rc) return rc;
+    return launch_join<T, D, kRT, kKT, 32>(w, s);
+}
+
+template <class T, int D>
+int launch_gen(const DevCtx& dc, const Work& w, cudaStream_t s) {
+    return w.a.softcap > 0.f || !(w.scale_log2 > 0.f) ? launch_one<T, D, true>(dc, w, s)
+                                                      : launch_one<T, D, false>(dc, w, s);
+}
+
+}  // namespace
+
+int launch_chunk(const DevCtx& dc, const Work& w, cudaStream_t s) {
+    if (w.a.dtype == QG_F16)
+        return w.a.d == 64 ? launch_gen<__half, 64>(dc, w, s) : launch_gen<__half, 128>(dc, w, s);
+    return w.a.d == 64 ? launch_gen<__nv_bfloat16, 64>(dc, w, s) : launch_gen<__nv_bfloat16, 128>(dc, w, s);
+}
+
+}  // namespace attn
+}  // namespace qg

@@ -11,10 +11,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Parts of cut row tiles: two per CTA, RT rows of D outputs, a maximum and a sum.
 size_t part_bytes(const DevCtx& dc, int rt, int d) { return (size_t)dc.num_sms * 2 * rt * (d + 2) * 4; }
 
+// Rows per tile, by the most rows that a sequence can have: up to 64 the
+// streaming kernel, whose tile is the least that holds them, else the
+// tensor-core kernel for the whole batch (its single tokens too: a step with
+// one row costs it little more than the bytes of the keys and values).
+int row_tile(const AttnArgs& a) {
+    const long long rows = (long long)a.max_new * (a.hq / a.hkv);
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;
+}
+
 }  // namespace
 
 size_t attn_workspace_bytes(const DevCtx& dc, const AttnArgs& a) {
-    return part_bytes(dc, 64, a.d);
+    return part_bytes(dc, row_tile(a), a.d);
 }
 
 int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, size_t, cudaStream_t s) {
@@ -28,13 +37,10 @@ int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, size_t, cudaStrea
     }
     w.err = dc.err;
     w.ctas = dc.num_sms;
-    w.rows_min = 0;
-    w.rows_max = 0x7FFFFFFF;
-    const long long rows = (long long)a.max_new * w.group;
-    const int rb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    const int rt = row_tile(a);
     w.part = static_cast<float*>(ws);
-    w.ml = reinterpret_cast<float2*>(w.part + (size_t)w.ctas * 2 * 16 * rb * a.d);
-    return attn::launch_few(dc, w, rb, s);
+    w.ml = reinterpret_cast<float2*>(w.part + (size_t)w.ctas * 2 * rt * a.d);
+    return rt <= 64 ? attn::launch_few(dc, w, rt / 16, s) : attn::launch_chunk(dc, w, s);
 }
 
 }  // namespace qg

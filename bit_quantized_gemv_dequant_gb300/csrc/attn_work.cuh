@@ -26,7 +26,6 @@ using prefill::warp_wait_sleep;
 struct Work {
     AttnArgs a;
     int group;
-    int rows_min, rows_max;  // sequences with rows in (rows_min, rows_max]
     float scale_log2;        // scale * log2(e); without a cap scores go straight to base 2
     float cap_in, cap_out;   // 2 log2(e) scale / softcap, softcap * log2(e)
     float* part;             // [G][2][RT][D] unnormalised outputs of cut row tiles
@@ -36,7 +35,7 @@ struct Work {
 };
 
 struct Seq {
-    int first, n, rows, ctx;  // rows: 0 where this kernel has nothing to do
+    int first, n, rows, ctx;
 };
 
 __device__ __forceinline__ Seq seq_at(const Work& w, int b) {
@@ -55,7 +54,6 @@ __device__ __forceinline__ Seq seq_at(const Work& w, int b) {
     bad |= s.n > w.a.max_new;
     if (bad) report_error(w.err, DEVERR_INDEX);
     s.rows = min(s.n, w.a.max_new) * w.group;
-    if (s.rows <= w.rows_min || s.rows > w.rows_max) s.rows = 0;
     return s;
 }
 
@@ -227,8 +225,10 @@ __device__ __forceinline__ float score(const Work& w, float x) {
     return w.cap_out * (1.f - __fdividef(2.f, 1.f + ex2(fminf(x * w.cap_in, 126.f))));
 }
 
-// Largest grid and workspace; see attn_paged.cu.
+// Up to 16 * row_blocks rows per sequence and key head (row_blocks 1, 2, 4).
 int launch_few(const DevCtx& dc, const Work& w, int row_blocks, cudaStream_t s);
+// Any number of rows.
+int launch_chunk(const DevCtx& dc, const Work& w, cudaStream_t s);
 
 // A map of k or v: [num_pages][hkv * page_size][d], boxes of `rows` x 64 values.
 int cache_map(CUtensorMap* m, const AttnArgs& a, const void* p, int rows);

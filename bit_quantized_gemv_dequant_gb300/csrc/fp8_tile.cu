@@ -193,6 +193,8 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     static int configured[64] = {0};
     auto kern = tile_kernel<TY>;
     if (!configured[dc.device]) {
+        const int rc = check_register_split(kern, kThreads, 256 * 216 + 128 * 72);
+        if (rc) return rc;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dc.device] = 1;
