@@ -377,7 +377,7 @@ int token_logprobs_workspace_size(int64_t M, int64_t V, int top_k, size_t* bytes
     if (!bytes) return QG_ERR_INVALID_ARG;
     *bytes = 0;
     if (M < 0 || V <= 0 || top_k < 0 || top_k > V) return QG_ERR_INVALID_ARG;
-    if (M > kMaxInt || V > kMaxInt || top_k > 32) return QG_ERR_UNSUPPORTED;
+    if (M > kMaxInt || V > kMaxInt / 2 || top_k > 32) return QG_ERR_UNSUPPORTED;
     const DevCtx* dc = nullptr;
     int rc = device_ctx(&dc);
     if (rc) return rc;
@@ -390,7 +390,7 @@ int token_logprobs(const void* logits, int dtype, int64_t row_stride, const int6
                    float* top_values, int32_t* top_ids, void* workspace, size_t workspace_bytes,
                    qg_stream_t stream) {
     if (M < 0 || V <= 0 || top_k < 0 || top_k > V || !is_type(dtype)) return QG_ERR_INVALID_ARG;
-    if (M > kMaxInt || V > kMaxInt || top_k > 32) return QG_ERR_UNSUPPORTED;
+    if (M > kMaxInt || V > kMaxInt / 2 || top_k > 32) return QG_ERR_UNSUPPORTED;
     if (M > 0 && (!logits || !targets || !logprobs || !entropy || !ranks)) return QG_ERR_INVALID_ARG;
     if (M > 0 && top_k > 0 && (!top_values || !top_ids)) return QG_ERR_INVALID_ARG;
     int64_t xb = 0;
