@@ -17,7 +17,6 @@ on one stream are ordered by the stream.
 from __future__ import annotations
 
 import ctypes as C
-import math
 import os
 import threading
 
@@ -30,7 +29,6 @@ QG_OK, QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_MISALIGNED = 0, 1, 2, 3
 QG_ERR_CUDA, QG_ERR_WORKSPACE, QG_ERR_DEVICE = 4, 5, 6
 QG_OP_Q4_0, QG_OP_DUAL_Q4_0, QG_OP_Q4_K, QG_OP_AFFINE, QG_OP_AF4_G64 = 0, 1, 2, 3, 4
 QG_OP_DUAL_Q4_0_HOST = 5
-QG_OP_FP8_B128 = 6
 QG_F32, QG_F16, QG_BF16 = 0, 1, 2
 QG_OPT_PDL = 1
 QG_OPT_PREFILL_MIN_M = 2
@@ -50,8 +48,7 @@ EXPORTS = ("qgemv_q4_0", "qgemv_dual_q4_0", "qgemv_q4_k", "qmm_affine", "qkv_spl
            "qgemv_q4_k_noalloc", "qg_prepare_af4_g64", "qmm_af4_g64", "qgemv_dual_q4_0_host",
            "quantize_fp8_b128", "qmm_fp8_b128", "attn_paged", "attn_paged_workspace_size",
            "kv_append", "kv_copy_pages", "kv_fork", "kv_fork_workspace_size", "kv_free",
-           "kv_compact", "kv_compact_workspace_size", "token_logprobs",
-           "token_logprobs_workspace_size")
+           "kv_compact", "kv_compact_workspace_size", "token_logprobs")
 
 _LIB = None
 _LOCK = threading.Lock()
@@ -99,7 +96,7 @@ def lib():
             "qg_prepare_af4_g64": [P, P, P, P, P, I64, I64, P],
             "qmm_af4_g64": [P, P, P, P, I64, I64, I64, P, SZ, P],
             "quantize_fp8_b128": [P, I, I64, P, P, I64, I64, P],
-            "qmm_fp8_b128": [P, P, P, P, P, I, I64, I64, I64, P, SZ, P],
+            "qmm_fp8_b128": [P, P, P, P, P, I, I64, I64, I64, P],
             "attn_paged": [P, I64] + [P] * 7 + [I] + [I64] * 9 + [C.c_float] * 2 + [I64, P, SZ, P],
             "attn_paged_workspace_size": [I64] * 6 + [C.POINTER(SZ)],
             "kv_append": [P, P, I64, I64, I, P, P, I, P] + [I64] * 5 + [P],
@@ -109,8 +106,7 @@ def lib():
             "kv_free": [P] * 4 + [I64] * 3 + [P] * 4,
             "kv_compact": [P, I64, I64, I64, P, I64, I64] + [P] * 6 + [SZ, P],
             "kv_compact_workspace_size": [I64, C.POINTER(SZ)],
-            "token_logprobs": [P, I, I64, P, I64, I64, I] + [P] * 6 + [SZ, P],
-            "token_logprobs_workspace_size": [I64, I64, I, C.POINTER(SZ)],
+            "token_logprobs": [P, I, I64, P, I64, I64, I] + [P] * 6,
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -130,6 +126,8 @@ def _check(rc: int, what: str):
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
+    if type(t) is torch.Tensor and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -151,6 +149,8 @@ def _host(t: torch.Tensor, name: str, dtype) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
+        if torch.cuda.is_initialized():  # the current stream, without building an object for it
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -365,7 +365,7 @@ def _rows(t: torch.Tensor, name: str, dims: int):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    width = math.prod(t.shape[1:])
+    width = t.shape[1] if dims == 2 else t.shape[1] * t.shape[2]
     if t.is_contiguous():
         return t.data_ptr(), width
     step = 1
@@ -377,7 +377,7 @@ def _rows(t: torch.Tensor, name: str, dims: int):
 
 
 def _same(t: torch.Tensor, name: str, *shape) -> None:
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
 
 
@@ -386,7 +386,7 @@ _SIZES = {}
 
 def _size(what: str, *args) -> int:
     """The workspace bytes that the library asks for, asked once per shape and device."""
-    key = (what, torch.cuda.current_device(), *args)
+    key = (what, torch._C._cuda_getDevice(), *args)
     n = _SIZES.get(key)
     if n is None:
         v = C.c_size_t(0)
@@ -418,8 +418,7 @@ def quantize_fp8_b128(x, codes=None, scales=None, *, stream=None):
     return codes, scales
 
 
-def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, workspace=None,
-                 stream=None):
+def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, stream=None):
     """y[M, N] = (a * a_scales) . (w * w_scales)^T: e4m3 codes a [M, K] with a
     scale per row and 128 values of K, w [N, K] with one per 128 x 128 values;
     y is float32 or bfloat16."""
@@ -433,14 +432,11 @@ def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, w
         y = torch.empty((M, N), dtype=out_dtype, device=a.device)
     else:
         _same(y, "y", M, N)
-    st = _stream(stream)
-    need = _size("qg_workspace_size", QG_OP_FP8_B128, M, N, K, 0, 0)
-    ws, wsb = _scratch(need, a.device, workspace, st)
     _check(lib().qmm_fp8_b128(_dev(a, "a", torch.float8_e4m3fn),
                               _dev(a_scales, "a_scales", torch.float32),
                               _dev(w, "w", torch.float8_e4m3fn),
                               _dev(w_scales, "w_scales", torch.float32), _dev(y, "y"),
-                              _dtype(y, "y"), M, N, K, ws, wsb, st), "qmm_fp8_b128")
+                              _dtype(y, "y"), M, N, K, _stream(stream)), "qmm_fp8_b128")
     return y
 
 
@@ -588,7 +584,7 @@ def kv_compact(cache, page_table, ref_counts, *, workspace=None, stream=None):
     return table, refs, page_map, live
 
 
-def token_logprobs(logits, targets, top_k=0, *, workspace=None, stream=None):
+def token_logprobs(logits, targets, top_k=0, *, stream=None):
     """(logprobs, entropy, ranks, top_values, top_ids) of rows of logits [M, V]
     (rows may lie apart): the log probability of each row's target (int64;
     negative: none, 0 and rank -1), the row's entropy, how many logits are
@@ -599,17 +595,16 @@ def token_logprobs(logits, targets, top_k=0, *, workspace=None, stream=None):
     _same(targets, "targets", M)
     k = min(int(top_k), V)
     dev = logits.device
-    f = torch.empty((2, M), dtype=torch.float32, device=dev)
-    ranks = torch.empty(M, dtype=torch.int32, device=dev)
-    top = torch.empty((M, k), dtype=torch.float32, device=dev)
-    ids = torch.empty((M, k), dtype=torch.int32, device=dev)
-    st = _stream(stream)
-    ws, wsb = _scratch(_size("token_logprobs_workspace_size", M, V, k), dev, workspace, st)
+    f32, i32 = torch.float32, torch.int32
+    logprobs = torch.empty(M, dtype=f32, device=dev)
+    entropy, ranks = torch.empty_like(logprobs), torch.empty(M, dtype=i32, device=dev)
+    top = torch.empty((M, max(k, 0)), dtype=f32, device=dev)
+    ids = torch.empty((M, max(k, 0)), dtype=i32, device=dev)
     _check(lib().token_logprobs(at, _dtype(logits, "logits"), stride,
-                                _dev(targets, "targets", torch.int64), M, V, k, f.data_ptr(),
-                                f.data_ptr() + 4 * M, ranks.data_ptr(), top.data_ptr(),
-                                ids.data_ptr(), ws, wsb, st), "token_logprobs")
-    return f[0], f[1], ranks, top, ids
+                                _dev(targets, "targets", torch.int64), M, V, k,
+                                logprobs.data_ptr(), entropy.data_ptr(), ranks.data_ptr(),
+                                top.data_ptr(), ids.data_ptr(), _stream(stream)), "token_logprobs")
+    return logprobs, entropy, ranks, top, ids
 
 
 def device_error(clear: bool = True) -> int:

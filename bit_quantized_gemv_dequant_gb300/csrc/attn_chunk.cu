@@ -32,13 +32,15 @@ using fp8::tmem_wait32;
 // 2^8 cost nothing in f16 or bf16, and the quotient by the sum is the same).
 // Rows past the last one repeat it; their results are not stored.
 //
-//   warps 0-3, 4-7  softmax and output of block 0, 1
+//   warps 0-3, 4-7  softmax and output of block 0, 1; they also gather their
+//                   block's rows of Q, those of the next segment as soon as the
+//                   last scores of this one are there
 //   warp 8          TMA producer: ring of K and V tiles, taken alternately
 //   warp 9          MMA issuer
-//   warps 10-11     gather Q into shared memory
+// Ten warps leave 200 registers per thread: a row's 128 scores stay in them.
 constexpr int kKT = 128;
 constexpr int kRT = 256;
-constexpr int kThreads = 384;
+constexpr int kThreads = 320;
 constexpr float kLazy = 8.f;
 
 template <int D>
@@ -100,10 +102,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto empty = [&](int i) { return bars + 8u * (G::kStages + i); };
     const uint32_t more = bars + 16u * G::kStages;
     auto s_full = [&](int t) { return more + 8u * t; };
-    auto p_full = [&](int t) { return more + 16u + 8u * t; };
-    auto o_full = [&](int t) { return more + 32u + 8u * t; };
-    const uint32_t q_full = more + 48u, q_free = more + 56u, tail = more + 64u, done = more + 72u;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(smem + G::kBarOff + 16 * G::kStages + 80);
+    auto p_full = [&](int t, int half) { return more + 16u + 16u * t + 8u * half; };  // 64 keys each
+    auto o_full = [&](int t) { return more + 48u + 8u * t; };
+    auto q_full = [&](int t) { return more + 64u + 8u * t; };
+    const uint32_t tail = more + 80u, done = more + 88u;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(smem + G::kBarOff + 16 * G::kStages + 96);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -113,11 +116,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), 4);
+            mbar_init(p_full(t, 0), 4);
+            mbar_init(p_full(t, 1), 4);
             mbar_init(o_full(t), 1);
+            mbar_init(q_full(t), 4);
         }
-        mbar_init(q_full, 2);
-        mbar_init(q_free, 1);
         mbar_init(tail, 1);
         mbar_init(done, 1);
         fence_mbar_init();
@@ -141,7 +144,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         if (warp == 8) {
             // -------------------------------------------------------- producer
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
             const int rows = min(w.a.page_size, kKT);
             int i = 0, tails = 0;
             while (ok && walk.next()) {
@@ -194,11 +196,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     report_error(w.err, DEVERR_WAIT_DRAIN);
         } else if (warp == 9) {
             // ------------------------------------------------------------- MMA
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
             if (lane == 0) {
                 constexpr uint32_t kQK = idesc<T>(128, false), kPV = idesc<T>(D, true);
-                int i = 0, seg = 0;       // ring entries, segments
-                int steps[2] = {0, 0};    // steps of each block
+                int i = 0;                               // ring entries
+                int steps[2] = {0, 0}, segs[2] = {0, 0};  // of each block
                 auto wait = [&](uint32_t bar, uint32_t parity) {
                     if (ok && !mbar_wait(bar, parity)) {
                         report_error(w.err, DEVERR_TC_WAIT);
@@ -219,25 +220,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto out_mma = [&](int t, int st, bool acc) {
                     const uint64_t v = mn_desc(base + G::kRingOff + st * G::kTile, G::kHalf);
 #pragma unroll
-                    for (int c = 0; c < kKT / 16; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
-                        tc_mma_ts(tmem + G::kO + t * D, tmem + t * 128 + c * 8, v + c * 128, kPV, acc || c > 0);
+                    for (int half = 0; half < 2; ++half) {
+                        if (!wait(p_full(t, half), steps[t] & 1)) return;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = half * 4; c < half * 4 + 4; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
+                            tc_mma_ts(tmem + G::kO + t * D, tmem + t * 128 + c * 8, v + c * 128, kPV, acc || c > 0);
+                    }
+                    ++steps[t];
                 };
                 while (ok && walk.next()) {
                     const bool two = walk.s.rows - walk.p.tile * kRT > 128;
                     const int nt = walk.hi - walk.lo;
-                    if (!wait(q_full, seg & 1) || !wait(full(i % G::kStages), (i / G::kStages) & 1)) break;
-                    tc_fence_after();
-                    score_mma(0, i % G::kStages);
-                    if (two) score_mma(1, i % G::kStages);
-                    tc_commit(empty(i % G::kStages));
-                    if (nt == 1) tc_commit(q_free);
-                    ++i;
-                    for (int j = 0; j < nt; ++j) {
-                        const int vs = i % G::kStages, ks = (i + 1) % G::kStages;
-                        if (!wait(full(vs), (i / G::kStages) & 1) || !wait(p_full(0), steps[0]++ & 1)) break;
+                    if (!wait(full(i % G::kStages), (i / G::kStages) & 1)) break;
+                    for (int t = 0; t < 1 + two; ++t) {
+                        if (!wait(q_full(t), segs[t]++ & 1)) break;
                         tc_fence_after();
-                        out_mma(0, vs, j > 0);
+                        score_mma(t, i % G::kStages);
+                    }
+                    tc_commit(empty(i % G::kStages));
+                    ++i;
+                    for (int j = 0; ok && j < nt; ++j, i += 2) {
+                        const int vs = i % G::kStages, ks = (i + 1) % G::kStages;
                         const bool last = j + 1 == nt;
+                        if (!wait(full(vs), (i / G::kStages) & 1)) break;
+                        out_mma(0, vs, j > 0);
                         if (last) {
                             tc_commit(o_full(0));
                         } else {
@@ -246,61 +253,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                             score_mma(0, ks);
                         }
                         if (two) {
-                            if (!wait(p_full(1), steps[1]++ & 1)) break;
-                            tc_fence_after();
                             out_mma(1, vs, j > 0);
+                            if (last) tc_commit(o_full(1));
                         }
                         tc_commit(empty(vs));
-                        if (last) {
-                            if (two) tc_commit(o_full(1));
-                            ++i;
-                        } else {
+                        if (!last) {
                             if (two) score_mma(1, ks);
                             tc_commit(empty(ks));
-                            if (j + 2 == nt) tc_commit(q_free);
-                            i += 2;
                         }
                     }
-                    ++seg;
+                    --i;  // the last step took no further K
                 }
                 tc_commit(done);
                 if (!mbar_wait(done, 0)) report_error(w.err, DEVERR_WAIT_DRAIN);
             }
-        } else if (warp >= 10) {
-            // --------------------------------------------------------------- Q
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-            int seg = 0;
-            while (ok && walk.next()) {
-                if (seg && !warp_wait_sleep(q_free, (seg - 1) & 1)) {
-                    if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
-                    ok = false;
-                    break;
-                }
-                const int r0 = walk.p.tile * kRT;
-                const int n_rows = walk.s.rows - r0 > 128 ? 256 : 128;
-                constexpr int C = D / 8;  // 16-byte chunks per row
-                for (int e = (int)threadIdx.x - 320; e < n_rows * C; e += 64) {
-                    const int row = e / C, c = e % C, r = min(r0 + row, walk.s.rows - 1);
-                    const T* src = static_cast<const T*>(w.a.q) +
-                                   (long long)(walk.s.first + r / w.group) * w.a.q_stride +
-                                   (long long)(walk.p.head * w.group + r % w.group) * D + c * 8;
-                    const int rr = row % 128;
-                    cp_async16(base + (row / 128) * G::kTile + (c / 8) * G::kHalf + rr * 128 +
-                                   (((c & 7) ^ (rr & 7)) << 4), src);
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_async_proxy();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
-                ++seg;
-            }
         } else {
             // --------------------------------------------------------- softmax
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
             const int t = warp >> 2, row = (warp & 3) * 32 + lane;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + G::kO + t * D;
             int steps = 0, seg = 0;
+            // This thread's row of Q in the next segment that has this block;
+            // `ahead` is advanced to it.
+            auto gather = [&](Walk<kRT, kKT>& ahead) {
+                do {
+                    if (!ahead.next()) return;
+                } while (ahead.s.rows - ahead.p.tile * kRT <= t * 128);
+                const int r = min(ahead.p.tile * kRT + t * 128 + row, ahead.s.rows - 1);
+                const T* src = static_cast<const T*>(w.a.q) +
+                               (long long)(ahead.s.first + r / w.group) * w.a.q_stride +
+                               (long long)(ahead.p.head * w.group + r % w.group) * D;
+                const uint32_t dst = base + t * G::kTile + row * 128;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    cp_async16(dst + (c / 8) * G::kHalf + (((c & 7) ^ (row & 7)) << 4), src + c * 8);
+            };
+            auto gathered = [&] {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full(t));
+            };
+            {
+                Walk<kRT, kKT> ahead = walk;
+                gather(ahead);
+                gathered();
+            }
             while (walk.next()) {
                 const Seq s = walk.s;
                 const int r0 = walk.p.tile * kRT, nt = walk.hi - walk.lo;
@@ -316,35 +314,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;  // the results are lost; the barriers are still met
                     }
                     tc_fence_after();
+                    // All of this segment's scores of the block are there: its Q is free.
+                    if (j + 1 == nt) {
+                        Walk<kRT, kKT> ahead = walk;
+                        gather(ahead);
+                    }
                     uint32_t x[4][32];
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    const bool masked = j0 + kKT - 1 > pos_lo || (w.a.window && j0 <= pos_hi - w.a.window);
+                    tmem_ld32_async(s_at, x[0]);
+                    tmem_ld32_async(s_at + 32, x[1]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32_async(s_at + c * 32, x[c]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_wait32(x[c]);
-                    if constexpr (GEN) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        if (c % 2 == 0) {
+                            tmem_wait32(x[c]);
+                            tmem_wait32(x[c + 1]);
+                            if (c == 0) {
+                                tmem_ld32_async(s_at + 64, x[2]);
+                                tmem_ld32_async(s_at + 96, x[3]);
+                            }
+                        }
+                        if constexpr (GEN) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 const float v = __uint_as_float(x[c][e]);
                                 x[c][e] = __float_as_uint(w.a.softcap > 0.f ? score<true>(w, v) : score<false>(w, v));
                             }
-                    }
-                    if (j0 + kKT - 1 > pos_lo || (w.a.window && j0 <= pos_hi - w.a.window)) {
-                        const int hi = pos - j0;                                       // last key seen
-                        const int lo = w.a.window ? pos - w.a.window - j0 : -1;        // first key seen - 1
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                        }
+                        if (masked) {
+                            const int hi = pos - j0 - c * 32;                                // last key seen
+                            const int lo = w.a.window ? pos - w.a.window - j0 - c * 32 : -1;  // first key seen - 1
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (c * 32 + e > hi || c * 32 + e <= lo) x[c][e] = 0xFF800000u;
-                    }
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                                if (e > hi || e <= lo) x[c][e] = 0xFF800000u;
+                        }
 #pragma unroll
                         for (int e = 0; e < 32; e += 2)
-                            top = fmaxf(top, fmaxf(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
+                            tops[(e / 2) & 3] = fmaxf(fmaxf(tops[(e / 2) & 3], __uint_as_float(x[c][e])),
+                                                      __uint_as_float(x[c][e + 1]));
+                    }
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     if (!GEN) top *= w.scale_log2;
                     if (__any_sync(0xFFFFFFFFu, top > m + kLazy)) {
                         const float mn = fmaxf(m, top);
@@ -365,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float ref = m == -INFINITY ? 0.f : m;
                     const float2 sc = make_float2(GEN ? 1.f : w.scale_log2, GEN ? 1.f : w.scale_log2);
                     const float2 off = make_float2(-ref, -ref);
-                    float2 sum = make_float2(0.f, 0.f);
+                    float2 sum[4] = {};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t p[16];
@@ -374,17 +383,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float2 v = fma2(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc, off);
                             v.x = ex2(v.x);
                             v.y = ex2(v.y);
-                            sum = __fadd2_rn(sum, v);
+                            sum[(e / 2) & 3] = __fadd2_rn(sum[(e / 2) & 3], v);
                             p[e / 2] = pack2<T>(v.x, v.y);
                         }
                         tmem_st16(s_at + c * 16, p);
+                        if (c & 1) {
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(p_full(t, c / 2));
+                        }
                     }
-                    l += sum.x + sum.y;
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full(t));
+                    const float2 s01 = __fadd2_rn(sum[0], sum[1]), s23 = __fadd2_rn(sum[2], sum[3]);
+                    l += (s01.x + s23.x) + (s01.y + s23.y);
                 }
+                gathered();
                 // ------------------------------------------- end of a segment
                 if (ok && !warp_wait(o_full(t), seg & 1)) {
                     if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
@@ -437,8 +450,6 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     static int configured[64] = {0};
     auto kern = chunk_kernel<T, D, GEN>;
     if (!configured[dc.device]) {
-        int rc = fp8::check_register_split(kern, kThreads, 256 * 216 + 128 * 72);
-        if (rc) return rc;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dc.device] = 1;

@@ -26,7 +26,7 @@ size_t attn_workspace_bytes(const DevCtx& dc, const AttnArgs& a) {
     return part_bytes(dc, row_tile(a), a.d);
 }
 
-int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, size_t, cudaStream_t s) {
+int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, cudaStream_t s) {
     attn::Work w{};
     w.a = a;
     w.group = a.hq / a.hkv;

@@ -83,9 +83,7 @@ int general_launch(const Fp8Args& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t fp8_workspace_bytes(const DevCtx&, const Fp8Args&) { return 0; }
-
-int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, void*, size_t, cudaStream_t s) {
+int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     const bool tma = a.K % 16 == 0 && reinterpret_cast<uintptr_t>(a.a) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
     if (tma) return a.M <= 128 ? fp8::launch_swap(dc, a, s) : fp8::launch_tile(dc, a, s);

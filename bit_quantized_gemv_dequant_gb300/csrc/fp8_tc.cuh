@@ -76,17 +76,6 @@ __device__ __forceinline__ void st_global_256(void* p, const uint32_t (&r)[8]) {
                  : "memory");
 }
 
-// setmaxnreg moves registers between warps of a block that was launched with
-// `need` in all: were the kernel compiled to fewer, the increase would wait for
-// ever, so it is not launched.
-template <class K>
-int check_register_split(K kern, int threads, int need) {
-    cudaFuncAttributes at{};
-    const cudaError_t e = cudaFuncGetAttributes(&at, kern);
-    if (e != cudaSuccess) return cuda_fail(e);
-    return at.numRegs * threads >= need ? QG_OK : QG_ERR_UNSUPPORTED;
-}
-
 struct Params {
     const float* sa;   // [M, KB]
     const float* sw;   // [ceil(N / 128), KB]

@@ -14,10 +14,10 @@ namespace {
 // columns, which lie in one block of w's scales, so a k block enters the sum
 // as fma(d, a_scale * w_scale, acc) with one factor per thread.
 //
-//   warp 0      TMA producer (48 KB per k block, four stages)
-//   warp 1      MMA issuer
-//   warps 4-11  epilogue; 216 registers each, from the 72 of warps 0-3
-constexpr int kThreads = 384;
+//   warps 0-7  epilogue (ten warps leave 200 registers: 128 sums fit)
+//   warp 8     TMA producer (48 KB per k block, four stages)
+//   warp 9     MMA issuer
+constexpr int kThreads = 320;
 constexpr int kBM = 128, kBN = 256;
 constexpr int kStages = 4;
 constexpr int kStage = (kBM + kBN) * 128;
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&map_a);
         prefetch_tmap(&map_w);
     }
-    if (warp == 1) tmem_alloc(smem_addr(slot), 512);
+    if (warp == 9) tmem_alloc(smem_addr(slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -66,9 +66,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
     pdl_wait();
 
-    if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 0 && lane == 0) {
+    if (warp >= 8) {
+        if (warp == 8 && lane == 0) {
             int i = 0;
             bool ok = true;
             for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
@@ -88,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int j = max(0, i - kStages); j < i; ++j)
                 if (!mbar_wait(full(j % kStages), (j / kStages) & 1)) report_error(p.err, DEVERR_WAIT_DRAIN);
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 9 && lane == 0) {
             int i = 0;
             bool ok = true;
             for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
@@ -113,8 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!mbar_wait(done, 0)) report_error(p.err, DEVERR_WAIT_DRAIN);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int half = (warp - 4) / 4;
+        const int half = warp / 4;
         const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
         int i = 0;
         bool ok = true;
@@ -127,34 +125,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-            float s_next = __ldg(sa) * __ldg(sw);
+            // The scales of the next k block, loaded one k block ahead.
+            float sa_next = __ldg(sa), sw_next = __ldg(sw);
             for (int b = 0; b < p.KB; ++b, ++i) {
                 const int tb = i & 1;
-                const float2 s = make_float2(s_next, s_next);
-                if (b + 1 < p.KB) s_next = __ldg(sa + b + 1) * __ldg(sw + b + 1);
+                const float sc = sa_next * sw_next;
+                const float2 s = make_float2(sc, sc);
+                if (b + 1 < p.KB) {
+                    sa_next = __ldg(sa + b + 1);
+                    sw_next = __ldg(sw + b + 1);
+                }
                 if (!warp_wait(t_full(tb), (i / 2) & 1)) {
                     if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t r[2][32];
-                tmem_ld32_async(at + tb * kBN, r[0]);
+                uint32_t r[2][16];
+                tmem_ld16_async(at + tb * kBN, r[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_wait32(r[c & 1]);
-                    if (c < 3) {
-                        tmem_ld32_async(at + tb * kBN + (c + 1) * 32, r[(c + 1) & 1]);
+                for (int c = 0; c < 8; ++c) {
+                    tmem_wait16(r[c & 1]);
+                    if (c < 7) {
+                        tmem_ld16_async(at + tb * kBN + (c + 1) * 16, r[(c + 1) & 1]);
                     } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(t_empty(tb));
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[c * 16 + j] = fma2(make_float2(__uint_as_float(r[c & 1][2 * j]),
-                                                           __uint_as_float(r[c & 1][2 * j + 1])),
-                                               s, acc[c * 16 + j]);
+                    for (int j = 0; j < 8; ++j)
+                        acc[c * 8 + j] = fma2(make_float2(__uint_as_float(r[c & 1][2 * j]),
+                                                          __uint_as_float(r[c & 1][2 * j + 1])),
+                                              s, acc[c * 8 + j]);
                 }
             }
             if (!ok || !live) continue;
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -193,8 +196,6 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     static int configured[64] = {0};
     auto kern = tile_kernel<TY>;
     if (!configured[dc.device]) {
-        const int rc = check_register_split(kern, kThreads, 256 * 216 + 128 * 72);
-        if (rc) return rc;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dc.device] = 1;

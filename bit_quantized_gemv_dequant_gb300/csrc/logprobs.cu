@@ -448,9 +448,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) row_kernel(c
 
 }  // namespace
 
-size_t logprobs_workspace_bytes(const DevCtx&, long long, long long, int) { return 0; }
-
-int logprobs_launch(const DevCtx& dc, const LogprobArgs& a, void*, cudaStream_t s) {
+int logprobs_launch(const DevCtx& dc, const LogprobArgs& a, cudaStream_t s) {
     return by_type(a.dtype, [&](auto t) {
         using T = decltype(t);
         // Few rows are shared by clusters of up to 8 CTAs, so that all SMs load,

@@ -308,17 +308,6 @@ int workspace_size_impl(int op, int64_t M, int64_t N, int64_t K, int group_size,
         if (rc) return rc;
         return (M > 32 || N % 64 || K % 64) ? QG_ERR_INVALID_ARG : QG_OK;
     }
-    if (op == QG_OP_FP8_B128) {
-        int rc = check_dims(M, N, K);
-        if (rc) return rc;
-        const DevCtx* dc = nullptr;
-        rc = current_ctx(&dc);
-        if (rc) return rc;
-        Fp8Args f{};
-        f.M = M; f.N = N; f.K = K;
-        *bytes = fp8_workspace_bytes(*dc, f);
-        return QG_OK;
-    }
     GemvArgs a{};
     switch (op) {
         case QG_OP_Q4_0: a.fmt = FMT_Q4_0; a.nw = 1; break;

@@ -252,8 +252,7 @@ struct Fp8Args {
     int y_dtype;
     long long M, N, K;
 };
-size_t fp8_workspace_bytes(const DevCtx& dc, const Fp8Args& a);
-int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, void* ws, size_t ws_bytes, cudaStream_t s);
+int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s);
 
 // Attention over a paged cache (attn_paged.cu).
 struct AttnArgs {
@@ -273,7 +272,7 @@ struct AttnArgs {
     int window;  // 0: none
 };
 size_t attn_workspace_bytes(const DevCtx& dc, const AttnArgs& a);
-int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, size_t ws_bytes, cudaStream_t s);
+int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, cudaStream_t s);
 
 // Pages of a cache (kv_pages.cu).
 struct PagePlanes {
@@ -329,8 +328,7 @@ struct LogprobArgs {
     float *logprobs, *entropy, *top_values;
     int32_t *ranks, *top_ids;
 };
-size_t logprobs_workspace_bytes(const DevCtx& dc, long long M, long long V, int k);
-int logprobs_launch(const DevCtx& dc, const LogprobArgs& a, void* ws, cudaStream_t s);
+int logprobs_launch(const DevCtx& dc, const LogprobArgs& a, cudaStream_t s);
 
 // Record a CUDA error for qg_last_cuda_error() and return QG_ERR_CUDA.
 int cuda_fail(cudaError_t e);

@@ -117,8 +117,7 @@ int quantize_fp8_b128(const void* x, int x_dtype, int64_t x_stride, uint8_t* cod
 }
 
 int qmm_fp8_b128(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
-                 void* y, int y_dtype, int64_t M, int64_t N, int64_t K, void* workspace,
-                 size_t workspace_bytes, qg_stream_t stream) {
+                 void* y, int y_dtype, int64_t M, int64_t N, int64_t K, qg_stream_t stream) {
     if (!a || !a_scales || !w || !w_scales || !y || M <= 0 || N <= 0 || K <= 0)
         return QG_ERR_INVALID_ARG;
     if (y_dtype != QG_F32 && y_dtype != QG_BF16) return QG_ERR_INVALID_ARG;
@@ -134,10 +133,7 @@ int qmm_fp8_b128(const uint8_t* a, const float* a_scales, const uint8_t* w, cons
     const DevCtx* dc = nullptr;
     int rc = device_ctx(&dc);
     if (rc) return rc;
-    const Fp8Args f{a, a_scales, w, w_scales, y, y_dtype, M, N, K};
-    rc = check_workspace(workspace, workspace_bytes, fp8_workspace_bytes(*dc, f));
-    if (rc) return rc;
-    return fp8_mm_launch(*dc, f, workspace, workspace_bytes, cu(stream));
+    return fp8_mm_launch(*dc, Fp8Args{a, a_scales, w, w_scales, y, y_dtype, M, N, K}, cu(stream));
 }
 
 int attn_paged(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -188,7 +184,7 @@ int attn_paged(const void* q, int64_t q_stride, const void* k_cache, const void*
     rc = check_workspace(workspace, workspace_bytes, attn_workspace_bytes(*dc, a));
     if (rc) return rc;
     if (a.tokens == 0 || a.max_new == 0) return QG_OK;
-    return attn_launch(*dc, a, workspace, workspace_bytes, cu(stream));
+    return attn_launch(*dc, a, workspace, cu(stream));
 }
 
 int attn_paged_workspace_size(int64_t tokens, int64_t batch, int64_t max_new, int64_t q_heads,
@@ -373,22 +369,9 @@ int kv_compact(void* cache, int64_t planes, int64_t num_pages, int64_t page_byte
     return kv_compact_launch(*dc, a, cu(stream));
 }
 
-int token_logprobs_workspace_size(int64_t M, int64_t V, int top_k, size_t* bytes) {
-    if (!bytes) return QG_ERR_INVALID_ARG;
-    *bytes = 0;
-    if (M < 0 || V <= 0 || top_k < 0 || top_k > V) return QG_ERR_INVALID_ARG;
-    if (M > kMaxInt || V > kMaxInt / 2 || top_k > 32) return QG_ERR_UNSUPPORTED;
-    const DevCtx* dc = nullptr;
-    int rc = device_ctx(&dc);
-    if (rc) return rc;
-    *bytes = logprobs_workspace_bytes(*dc, M, V, top_k);
-    return QG_OK;
-}
-
 int token_logprobs(const void* logits, int dtype, int64_t row_stride, const int64_t* targets,
                    int64_t M, int64_t V, int top_k, float* logprobs, float* entropy, int32_t* ranks,
-                   float* top_values, int32_t* top_ids, void* workspace, size_t workspace_bytes,
-                   qg_stream_t stream) {
+                   float* top_values, int32_t* top_ids, qg_stream_t stream) {
     if (M < 0 || V <= 0 || top_k < 0 || top_k > V || !is_type(dtype)) return QG_ERR_INVALID_ARG;
     if (M > kMaxInt || V > kMaxInt / 2 || top_k > 32) return QG_ERR_UNSUPPORTED;
     if (M > 0 && (!logits || !targets || !logprobs || !entropy || !ranks)) return QG_ERR_INVALID_ARG;
@@ -405,12 +388,10 @@ int token_logprobs(const void* logits, int dtype, int64_t row_stride, const int6
     const DevCtx* dc = nullptr;
     int rc = device_ctx(&dc);
     if (rc) return rc;
-    rc = check_workspace(workspace, workspace_bytes, logprobs_workspace_bytes(*dc, M, V, top_k));
-    if (rc) return rc;
     if (M == 0) return QG_OK;
     const LogprobArgs a{logits, dtype, row_stride, targets, M, V, top_k, logprobs, entropy, top_values,
                         ranks, top_ids};
-    return logprobs_launch(*dc, a, workspace, cu(stream));
+    return logprobs_launch(*dc, a, cu(stream));
 }
 
 }  // extern "C"

@@ -88,9 +88,8 @@ enum {
     QG_OP_Q4_K = 2,
     QG_OP_AFFINE = 3,
     QG_OP_AF4_G64 = 4,
-    QG_OP_DUAL_Q4_0_HOST = 5, /* qgemv_dual_q4_0_host: the call's own workspace plus
+    QG_OP_DUAL_Q4_0_HOST = 5  /* qgemv_dual_q4_0_host: the call's own workspace plus
                                  device staging for x, y_a, y_b */
-    QG_OP_FP8_B128 = 6        /* qmm_fp8_b128 */
 };
 
 /* Single Q4_0 projection: y[M,N] = x[M,K] . dequant(w)[N,K]^T.
@@ -289,13 +288,12 @@ enum { QG_F32 = 0, QG_F16 = 1, QG_BF16 = 2 };
  * exact and summed in f32: |y - exact| <= 1e-5 * sum |terms| + one rounding
  * to y's type. Calls with K % 16 == 0 and 16-byte aligned a and w take the
  * tensor cores; others a CUDA-core kernel with the same result up to the
- * order of the sum. Workspace: qg_workspace_size(QG_OP_FP8_B128, M, N, K,
- * 0, 0). */
+ * order of the sum. */
 QG_API int quantize_fp8_b128(const void* x, int x_dtype, int64_t x_stride, uint8_t* codes,
                              float* scales, int64_t M, int64_t K, qg_stream_t stream);
 QG_API int qmm_fp8_b128(const uint8_t* a, const float* a_scales, const uint8_t* w,
                         const float* w_scales, void* y, int y_dtype, int64_t M, int64_t N,
-                        int64_t K, void* workspace, size_t workspace_bytes, qg_stream_t stream);
+                        int64_t K, qg_stream_t stream);
 
 /* The paged cache of one layer: k_cache and v_cache are [num_pages,
  * kv_heads, page_size, head_dim] of one 16-bit type, 16-byte aligned.
@@ -407,13 +405,11 @@ QG_API int kv_compact_workspace_size(int64_t num_pages, size_t* bytes);
  * has log probabilities -infinity and entropy 0. A NaN makes a row's log
  * probabilities and entropy NaN and counts as the largest logit.
  * top_k <= min(32, V); with top_k = 0, top_values and top_ids may be NULL.
- * Sums are f32. Workspace: token_logprobs_workspace_size(). */
+ * (+infinity makes them NaN too.) V <= 2^30. Sums are f32. */
 QG_API int token_logprobs(const void* logits, int dtype, int64_t row_stride,
                           const int64_t* targets, int64_t M, int64_t V, int top_k,
                           float* logprobs, float* entropy, int32_t* ranks, float* top_values,
-                          int32_t* top_ids, void* workspace, size_t workspace_bytes,
-                          qg_stream_t stream);
-QG_API int token_logprobs_workspace_size(int64_t M, int64_t V, int top_k, size_t* bytes);
+                          int32_t* top_ids, qg_stream_t stream);
 
 /* Workspace bytes op (QG_OP_*) needs for the given shape; *bytes = 0 when
  * none. group_size/packed matter only for QG_OP_AFFINE. Returns a status. */
