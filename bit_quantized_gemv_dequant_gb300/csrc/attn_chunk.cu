@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto q_full = [&](int t) { return more + 64u + 8u * t; };
     const uint32_t tail = more + 80u, done = more + 88u;
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem + G::kBarOff + 16 * G::kStages + 96);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < G::kStages; ++i) {
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     for (int kv = 0; kv < 2; ++kv, ++i) {
                         const int st = i % G::kStages;
-                        if (i >= G::kStages && !warp_wait_sleep(empty(st), ((i / G::kStages) & 1) ^ 1)) {
+                        if (i >= G::kStages && !warp_bar_wait(empty(st), ((i / G::kStages) & 1) ^ 1)) {
                             if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
                             ok = false;
                             break;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             page, bar);
                         }
                         if (part) {
-                            if (!warp_wait(tail, tails & 1)) {
+                            if (!warp_bar_wait(tail, tails & 1)) {
                                 if (lane == 0) report_error(w.err, DEVERR_WAIT_DRAIN);
                                 ok = false;
                             }
@@ -192,81 +192,100 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             for (int j = max(0, i - G::kStages); j < i; ++j)
-                if (!warp_wait(full(j % G::kStages), (j / G::kStages) & 1) && lane == 0)
+                if (!warp_bar_wait(full(j % G::kStages), (j / G::kStages) & 1) && lane == 0)
                     report_error(w.err, DEVERR_WAIT_DRAIN);
         } else if (warp == 9) {
             // ------------------------------------------------------------- MMA
-            if (lane == 0) {
-                constexpr uint32_t kQK = idesc<T>(128, false), kPV = idesc<T>(D, true);
-                int i = 0;                               // ring entries
-                int steps[2] = {0, 0}, segs[2] = {0, 0};  // of each block
-                auto wait = [&](uint32_t bar, uint32_t parity) {
-                    if (ok && !mbar_wait(bar, parity)) {
-                        report_error(w.err, DEVERR_TC_WAIT);
-                        ok = false;
-                    }
-                    return ok;
-                };
-                auto score_mma = [&](int t, int st) {
-                    const uint32_t q = base + t * G::kTile, k = base + G::kRingOff + st * G::kTile;
+            constexpr uint32_t kQK = idesc<T>(128, false), kPV = idesc<T>(D, true);
+            const uint64_t dq = sw128_desc(base), dk = sw128_desc(base + G::kRingOff);
+            const uint64_t dv = mn_desc(base + G::kRingOff, G::kHalf);
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            int st = 0;                               // place of the next ring entry
+            uint32_t ph = 0;                          // and its phase
+            int steps[2] = {0, 0}, segs[2] = {0, 0};  // of each block
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (ok && !warp_bar_wait(bar, parity)) {
+                    if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
+                    ok = false;
+                }
+                return ok;
+            };
+            auto score_mma = [&](int t, int stage) {
+                const uint64_t a = dq + (uint64_t)(t * (G::kTile >> 4)), b = dk + (uint64_t)(stage * (G::kTile >> 4));
+                if (elect_one()) {
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h)
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            mma_ss(tmem + t * 128, sw128_desc(q + h * G::kHalf) + 2 * c,
-                                   sw128_desc(k + h * G::kHalf) + 2 * c, kQK, h + c > 0);
+                            mma_ss(tm + t * 128, a + h * (G::kHalf >> 4) + 2 * c, b + h * (G::kHalf >> 4) + 2 * c, kQK,
+                                   h + c > 0);
                     tc_commit(s_full(t));
-                };
-                auto out_mma = [&](int t, int st, bool acc) {
-                    const uint64_t v = mn_desc(base + G::kRingOff + st * G::kTile, G::kHalf);
+                }
+                __syncwarp();
+            };
+            auto out_mma = [&](int t, int stage, bool acc) {
+                const uint64_t v = dv + (uint64_t)(stage * (G::kTile >> 4));
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (!wait(p_full(t, half), steps[t] & 1)) return;
-                        tc_fence_after();
+                for (int half = 0; half < 2; ++half) {
+                    if (!wait(p_full(t, half), steps[t] & 1)) return;
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
                         for (int c = half * 4; c < half * 4 + 4; ++c)  // 16 keys: 8 columns of P, 2048 bytes of V
-                            tc_mma_ts(tmem + G::kO + t * D, tmem + t * 128 + c * 8, v + c * 128, kPV, acc || c > 0);
+                            tc_mma_ts(tm + G::kO + t * D, tm + t * 128 + c * 8, v + c * 128, kPV, acc || c > 0);
                     }
-                    ++steps[t];
-                };
-                while (ok && walk.next()) {
-                    const bool two = walk.s.rows - walk.p.tile * kRT > 128;
-                    const int nt = walk.hi - walk.lo;
-                    if (!wait(full(i % G::kStages), (i / G::kStages) & 1)) break;
-                    for (int t = 0; t < 1 + two; ++t) {
-                        if (!wait(q_full(t), segs[t]++ & 1)) break;
-                        tc_fence_after();
-                        score_mma(t, i % G::kStages);
-                    }
-                    tc_commit(empty(i % G::kStages));
-                    ++i;
-                    for (int j = 0; ok && j < nt; ++j, i += 2) {
-                        const int vs = i % G::kStages, ks = (i + 1) % G::kStages;
-                        const bool last = j + 1 == nt;
-                        if (!wait(full(vs), (i / G::kStages) & 1)) break;
-                        out_mma(0, vs, j > 0);
-                        if (last) {
-                            tc_commit(o_full(0));
-                        } else {
-                            if (!wait(full(ks), ((i + 1) / G::kStages) & 1)) break;
-                            tc_fence_after();
-                            score_mma(0, ks);
-                        }
-                        if (two) {
-                            out_mma(1, vs, j > 0);
-                            if (last) tc_commit(o_full(1));
-                        }
-                        tc_commit(empty(vs));
-                        if (!last) {
-                            if (two) score_mma(1, ks);
-                            tc_commit(empty(ks));
-                        }
-                    }
-                    --i;  // the last step took no further K
+                    __syncwarp();
                 }
-                tc_commit(done);
-                if (!mbar_wait(done, 0)) report_error(w.err, DEVERR_WAIT_DRAIN);
+                ++steps[t];
+            };
+            auto commit = [&](uint32_t bar) {
+                if (elect_one()) tc_commit(bar);
+                __syncwarp();
+            };
+            auto advance = [&] {
+                if (++st == G::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            };
+            while (ok && walk.next()) {
+                const bool two = walk.s.rows - walk.p.tile * kRT > 128;
+                const int nt = walk.hi - walk.lo;
+                if (!wait(full(st), ph)) break;
+                for (int t = 0; t < 1 + two; ++t) {
+                    if (!wait(q_full(t), segs[t]++ & 1)) break;
+                    tc_fence_after();
+                    score_mma(t, st);
+                }
+                commit(empty(st));
+                advance();
+                for (int j = 0; ok && j < nt; ++j) {
+                    const int vs = st;
+                    const bool last = j + 1 == nt;
+                    if (!wait(full(vs), ph)) break;
+                    advance();
+                    out_mma(0, vs, j > 0);
+                    if (last) {
+                        commit(o_full(0));
+                    } else {
+                        if (!wait(full(st), ph)) break;
+                        tc_fence_after();
+                        score_mma(0, st);
+                    }
+                    if (two) {
+                        out_mma(1, vs, j > 0);
+                        if (last) commit(o_full(1));
+                    }
+                    commit(empty(vs));
+                    if (!last) {
+                        if (two) score_mma(1, st);
+                        commit(empty(st));
+                        advance();
+                    }
+                }
             }
+            commit(done);
+            if (!warp_bar_wait(done, 0) && lane == 0) report_error(w.err, DEVERR_WAIT_DRAIN);
         } else {
             // --------------------------------------------------------- softmax
             const int t = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -309,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float m = -INFINITY, l = 0.f;
                 for (int j = 0; j < nt; ++j, ++steps) {
                     const int j0 = (walk.lo + j) * kKT;
-                    if (ok && !warp_wait(s_full(t), steps & 1)) {
+                    if (ok && !warp_bar_wait(s_full(t), steps & 1)) {
                         if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
                         ok = false;  // the results are lost; the barriers are still met
                     }
@@ -399,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 gathered();
                 // ------------------------------------------- end of a segment
-                if (ok && !warp_wait(o_full(t), seg & 1)) {
+                if (ok && !warp_bar_wait(o_full(t), seg & 1)) {
                     if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
                     ok = false;
                 }

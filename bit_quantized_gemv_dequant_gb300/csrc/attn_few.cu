@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && walk.next()) {
             for (int t = walk.lo; t < walk.hi; ++t, ++i) {
                 const int st = i % G::kStages;
-                if (i >= G::kStages && !warp_wait_sleep(empty(st), ((i / G::kStages) & 1) ^ 1)) {
+                if (i >= G::kStages && !warp_bar_wait(empty(st), ((i / G::kStages) & 1) ^ 1)) {
                     if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
                     ok = false;
                     break;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         for (int j = max(0, i - G::kStages); j < i; ++j)
-            if (!warp_wait(full(j % G::kStages), (j / G::kStages) & 1) && lane == 0)
+            if (!warp_bar_wait(full(j % G::kStages), (j / G::kStages) & 1) && lane == 0)
                 report_error(w.err, DEVERR_WAIT_DRAIN);
         return;
     }
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st = i % G::kStages;
             // After a wait that gave up the error word is set and the results
             // are lost, but every barrier below is still met.
-            if (ok && !warp_wait(full(st), (i / G::kStages) & 1)) {
+            if (ok && !warp_bar_wait(full(st), (i / G::kStages) & 1)) {
                 if (lane == 0) report_error(w.err, DEVERR_TC_WAIT);
                 ok = false;
             }

@@ -20,8 +20,6 @@ namespace attn {
 using fp8::pdl_trigger;
 using fp8::pdl_wait;
 using prefill::prefetch_tmap;
-using prefill::warp_wait;
-using prefill::warp_wait_sleep;
 
 struct Work {
     AttnArgs a;

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t done = bars + 8u * (2 * G::kStages + 2 * G::kBufs);
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem + G::kBarOff + 8 * (2 * G::kStages + 2 * G::kBufs + 1));
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const int split = (int)gridDim.x, rank = (int)blockIdx.x;
     const int n0 = (int)blockIdx.y * 128, m0 = (int)blockIdx.z * BN;
     const int b0 = (int)((long long)p.KB * rank / split), b1 = (int)((long long)p.KB * (rank + 1) / split);
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int issued = 0;
             for (int i = 0; i < nb; ++i) {
                 const int st = i % G::kStages;
-                if (i >= G::kStages && !mbar_wait_sleep(empty(st), ((i / G::kStages) & 1) ^ 1)) {
+                if (i >= G::kStages && !bar_wait(empty(st), ((i / G::kStages) & 1) ^ 1)) {
                     report_error(p.err, DEVERR_TC_WAIT);
                     break;
                 }
@@ -121,29 +121,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issued = i + 1;
             }
             for (int i = max(0, issued - G::kStages); i < issued; ++i)
-                if (!mbar_wait(full(i % G::kStages), (i / G::kStages) & 1))
+                if (!bar_wait(full(i % G::kStages), (i / G::kStages) & 1))
                     report_error(p.err, DEVERR_WAIT_DRAIN);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            for (int i = 0; i < nb; ++i) {
-                const int st = i % G::kStages, tb = i % G::kBufs;
-                if (!mbar_wait(full(st), (i / G::kStages) & 1) ||
-                    (i >= G::kBufs && !mbar_wait(t_empty(tb), ((i / G::kBufs) & 1) ^ 1))) {
-                    report_error(p.err, DEVERR_TC_WAIT);
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t dw = sw128_desc(base + st * G::kStage);
-                const uint64_t da = sw128_desc(base + st * G::kStage + 16384);
+        const uint64_t dw = sw128_desc(base), da = sw128_desc(base + 16384);
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        int st = 0, tb = 0;
+        uint32_t ph = 0, tph = 0;
+        for (int i = 0; i < nb; ++i) {
+            if (!warp_bar_wait(full(st), ph) || !warp_bar_wait(t_empty(tb), tph ^ 1)) {
+                if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
+                break;
+            }
+            tc_fence_after();
+            const uint64_t w = dw + (uint64_t)(st * (G::kStage >> 4)), a = da + (uint64_t)(st * (G::kStage >> 4));
+            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_f8(tmem + tb * BN, dw + 2 * k, da + 2 * k, kDesc, k > 0);
+                for (int k = 0; k < 4; ++k) mma_f8(tm + tb * BN, w + 2 * k, a + 2 * k, kDesc, k > 0);
                 tc_commit(empty(st));
                 tc_commit(t_full(tb));
             }
-            tc_commit(done);
-            if (!mbar_wait(done, 0)) report_error(p.err, DEVERR_WAIT_DRAIN);
+            __syncwarp();
+            if (++st == G::kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+            if (++tb == G::kBufs) {
+                tb = 0;
+                tph ^= 1;
+            }
         }
+        if (elect_one()) tc_commit(done);
+        __syncwarp();
+        if (!warp_bar_wait(done, 0) && lane == 0) report_error(p.err, DEVERR_WAIT_DRAIN);
     } else if (warp >= 4) {
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float* sw = p.sw + (long long)blockIdx.y * p.KB + b0;
@@ -159,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar_sync(1, 128);
             for (int b = 0; b < nk; ++b) {
                 const int i = i0 + b, tb = i % G::kBufs;
-                if (!warp_wait(t_full(tb), (i / G::kBufs) & 1)) {
+                if (!warp_bar_wait(t_full(tb), (i / G::kBufs) & 1)) {
                     if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
                     i0 = nb;  // the sums are lost; the barriers below are still met
                     break;

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto t_empty = [&](int i) { return bars + 8u * (2 * kStages + 2 + i); };
     const uint32_t done = bars + 8u * (2 * kStages + 4);
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 8 * (2 * kStages + 5));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const int mt = (p.M + kBM - 1) / kBM, nt = (p.N + kBN - 1) / kBN;
     const long long tiles = (long long)mt * nt;
 
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int m0 = (int)(t % mt) * kBM, n0 = (int)(t / mt) * kBN;
                 for (int b = 0; b < p.KB; ++b, ++i) {
                     const int st = i % kStages;
-                    if (i >= kStages && !mbar_wait_sleep(empty(st), ((i / kStages) & 1) ^ 1)) {
+                    if (i >= kStages && !bar_wait(empty(st), ((i / kStages) & 1) ^ 1)) {
                         report_error(p.err, DEVERR_TC_WAIT);
                         ok = false;
                         break;
@@ -86,30 +86,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             for (int j = max(0, i - kStages); j < i; ++j)
-                if (!mbar_wait(full(j % kStages), (j / kStages) & 1)) report_error(p.err, DEVERR_WAIT_DRAIN);
-        } else if (warp == 9 && lane == 0) {
-            int i = 0;
+                if (!bar_wait(full(j % kStages), (j / kStages) & 1)) report_error(p.err, DEVERR_WAIT_DRAIN);
+        } else if (warp == 9) {
+            const uint64_t da = sw128_desc(base), dw = sw128_desc(base + kBM * 128);
+            const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            int st = 0, tb = 0;
+            uint32_t ph = 0, tph = 0;
             bool ok = true;
             for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                for (int b = 0; b < p.KB; ++b, ++i) {
-                    const int st = i % kStages, tb = i & 1;
-                    if (!mbar_wait(full(st), (i / kStages) & 1) ||
-                        (i >= 2 && !mbar_wait(t_empty(tb), ((i / 2) & 1) ^ 1))) {
-                        report_error(p.err, DEVERR_TC_WAIT);
+                for (int b = 0; b < p.KB; ++b) {
+                    if (!warp_bar_wait(full(st), ph) || !warp_bar_wait(t_empty(tb), tph ^ 1)) {
+                        if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t da = sw128_desc(base + st * kStage);
-                    const uint64_t dw = sw128_desc(base + st * kStage + kBM * 128);
+                    const uint64_t a = da + (uint64_t)(st * (kStage >> 4)), w = dw + (uint64_t)(st * (kStage >> 4));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_f8(tmem + tb * kBN, da + 2 * k, dw + 2 * k, kDesc, k > 0);
-                    tc_commit(empty(st));
-                    tc_commit(t_full(tb));
+                        for (int k = 0; k < 4; ++k) mma_f8(tm + tb * kBN, a + 2 * k, w + 2 * k, kDesc, k > 0);
+                        tc_commit(empty(st));
+                        tc_commit(t_full(tb));
+                    }
+                    __syncwarp();
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                    tb ^= 1;
+                    tph ^= tb == 0;
                 }
             }
-            tc_commit(done);
-            if (!mbar_wait(done, 0)) report_error(p.err, DEVERR_WAIT_DRAIN);
+            if (elect_one()) tc_commit(done);
+            __syncwarp();
+            if (!warp_bar_wait(done, 0) && lane == 0) report_error(p.err, DEVERR_WAIT_DRAIN);
         }
     } else {
         const int half = warp / 4;
@@ -135,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sa_next = __ldg(sa + b + 1);
                     sw_next = __ldg(sw + b + 1);
                 }
-                if (!warp_wait(t_full(tb), (i / 2) & 1)) {
+                if (!warp_bar_wait(t_full(tb), (i / 2) & 1)) {
                     if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
                     ok = false;
                     break;

@@ -56,6 +56,28 @@ int by_type(int dtype, F&& f) {
     }
 }
 
+// Bounded wait; the thread is suspended between polls, which would take issue
+// slots from the warps that it waits for.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) { return mbar_wait_sleep(bar, parity); }
+// The same for a whole warp.
+__device__ __forceinline__ bool warp_bar_wait(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity));
+}
+
+// True in one lane of a converged warp, the same one every time. The tensor-core
+// instructions take their operands from uniform registers: a warp that stays
+// together and issues them under this predicate has its addresses there, while
+// a loop that one lane runs alone moves every operand over for every instruction
+// (about 100 cycles each: more than the instruction itself takes).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// The warp's number in its block, known to be the same in all its lanes.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0); }
+
 inline int launched() {
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
