@@ -70,18 +70,12 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-__device__ __forceinline__ void st_global_256(void* p, const uint32_t (&r)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 struct Params {
     const float* sa;   // [M, KB]
     const float* sw;   // [ceil(N / 128), KB]
     void* y;           // [M, N]
     int M, N, KB;
-    bool vec;          // y rows start on 32-byte boundaries
+    bool vec;          // y's rows start on 16-byte boundaries (tile_kernel)
     unsigned* err;
 };
 

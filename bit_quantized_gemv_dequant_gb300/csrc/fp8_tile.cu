@@ -14,21 +14,43 @@ namespace {
 // columns, which lie in one block of w's scales, so a k block enters the sum
 // as fma(d, a_scale * w_scale, acc) with one factor per thread.
 //
-//   warps 0-7  epilogue (ten warps leave 200 registers: 128 sums fit)
-//   warp 8     TMA producer (48 KB per k block, four stages)
+// The scales of 32 k blocks at a time come into shared memory by 4-byte
+// asynchronous copies, the next 32 while these are used (read from global
+// memory as they are needed, a column of a row-major array, they cost 29 us of
+// 210 at M = 4096, N = 12288, K = 4096). Outputs leave through shared memory and
+// TMA stores, which go on while the next tile is summed (32-byte stores of 32
+// rows by each warp cost 33 us there).
+//
+//   warps 0-7  epilogue
+//   warp 8     TMA producer (48 KB per k block, three stages)
 //   warp 9     MMA issuer
 constexpr int kThreads = 320;
 constexpr int kBM = 128, kBN = 256;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kStage = (kBM + kBN) * 128;
-constexpr int kBarOff = kStages * kStage;
+constexpr int kScaleBlocks = 32;
+constexpr int kScaleRow = kBM + 4;                              // floats per k block: a's 128 rows, w's 2 blocks
+constexpr int kScaleSet = kScaleBlocks * kScaleRow * 4;
+constexpr int kOutOff = kStages * kStage;                       // 4 KB per epilogue warp: 32 rows x 128 bytes
+constexpr int kScaleOff = kOutOff + 8 * 4096;                   // two sets
+constexpr int kBarOff = kScaleOff + 2 * kScaleSet;
 constexpr int kSmem = 1024 + kBarOff + 256;
 constexpr uint32_t kDesc = f8_idesc(kBM, kBN);
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int c0, int c1, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
+}
 
 template <class TY>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-                const Params p) {
+                const __grid_constant__ CUtensorMap map_y, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -124,31 +146,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         const int half = warp / 4;
         const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
-        int i = 0;
+        const uint32_t out = base + kOutOff + warp * 4096;
+        const float* scales = reinterpret_cast<const float*>(smem + kScaleOff);
+        // Starts the copies of a tile's scales of the k blocks from b0 into a
+        // set: warp = 16 rows of a, lane = k block (a row's are consecutive).
+        auto fetch = [&](long long t, int b0, int set) {
+            if (t < tiles) {
+                const int m0 = (int)(t % mt) * kBM, n0 = (int)(t / mt) * kBN;
+                const uint32_t dst = base + kScaleOff + set * kScaleSet + lane * (kScaleRow * 4);
+                if (b0 + lane < p.KB) {
+#pragma unroll
+                    for (int i = 0; i < kBM / 8; ++i) {
+                        const int row = warp * (kBM / 8) + i;
+                        cp_async4(dst + row * 4, p.sa + (long long)min(m0 + row, p.M - 1) * p.KB + b0 + lane);
+                    }
+                    if (warp < 2)
+                        cp_async4(dst + (kBM + warp) * 4,
+                                  p.sw + (long long)min(n0 / 128 + warp, (p.N - 1) / 128) * p.KB + b0 + lane);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int i = 0, set = 0;
         bool ok = true;
+        fetch(blockIdx.x, 0, 0);
         for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const int m = (int)(t % mt) * kBM + (warp & 3) * 32 + lane;
+            const int row = (warp & 3) * 32 + lane;
+            const int m0 = (int)(t % mt) * kBM + (warp & 3) * 32, m = m0 + lane;
             const long long n0 = (t / mt) * kBN + half * 128;
-            const bool live = m < p.M && n0 < p.N;
-            const float* sa = p.sa + (long long)min(m, p.M - 1) * p.KB;
-            const float* sw = p.sw + min(n0, (long long)p.N - 1) / 128 * p.KB;
             float2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-            // The scales of the next k block, loaded one k block ahead.
-            float sa_next = __ldg(sa), sw_next = __ldg(sw);
             for (int b = 0; b < p.KB; ++b, ++i) {
-                const int tb = i & 1;
-                const float sc = sa_next * sw_next;
-                const float2 s = make_float2(sc, sc);
-                if (b + 1 < p.KB) {
-                    sa_next = __ldg(sa + b + 1);
-                    sw_next = __ldg(sw + b + 1);
+                if (b % kScaleBlocks == 0) {
+                    // The other set's last readers are past this barrier, this set's copies done.
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    named_bar_sync(1, 256);
+                    const bool more = b + kScaleBlocks < p.KB;
+                    fetch(more ? t : t + gridDim.x, more ? b + kScaleBlocks : 0, set ^ 1);
+                    set ^= 1;
                 }
-                if (!warp_bar_wait(t_full(tb), (i / 2) & 1)) {
+                const int tb = i & 1;
+                const float* sp = scales + (set ^ 1) * (kScaleSet / 4) + b % kScaleBlocks * kScaleRow;
+                const float sc = sp[row] * sp[kBM + half];
+                const float2 s = make_float2(sc, sc);
+                if (ok && !warp_bar_wait(t_full(tb), (i / 2) & 1)) {
                     if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
-                    ok = false;
-                    break;
+                    ok = false;  // the sums are lost; the barriers are still met
                 }
                 tc_fence_after();
                 uint32_t r[2][16];
@@ -170,28 +214,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               s, acc[c * 8 + j]);
                 }
             }
-            if (!ok || !live) continue;
-            TY* y = static_cast<TY*>(p.y) + (long long)m * p.N + n0;
-            if (p.vec && n0 + 128 <= p.N) {
-                constexpr int kPer = 32 / sizeof(TY);  // outputs per 32-byte store
+            if (p.vec) {
+                constexpr int kPer = 128 / sizeof(TY);  // columns of a 128-byte row
 #pragma unroll
                 for (int c = 0; c < 128; c += kPer) {
-                    uint32_t w[8];
+                    // the buffer's last store has been read
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if constexpr (sizeof(TY) == 4)
-                            w[j] = __float_as_uint(j & 1 ? acc[(c + j) / 2].y : acc[(c + j) / 2].x);
-                        else
-                            w[j] = pack2<TY>(acc[c / 2 + j].x, acc[c / 2 + j].y);
+                    for (int q = 0; q < 8; ++q) {  // 16-byte chunk q of the row, at q ^ (row % 8)
+                        uint4 v;
+                        if constexpr (sizeof(TY) == 4) {
+                            const float2 a0 = acc[(c + q * 4) / 2], a1 = acc[(c + q * 4) / 2 + 1];
+                            v = make_uint4(__float_as_uint(a0.x), __float_as_uint(a0.y), __float_as_uint(a1.x),
+                                           __float_as_uint(a1.y));
+                        } else {
+                            const float2* a = acc + (c + q * 8) / 2;
+                            v = make_uint4(pack2<TY>(a[0].x, a[0].y), pack2<TY>(a[1].x, a[1].y),
+                                           pack2<TY>(a[2].x, a[2].y), pack2<TY>(a[3].x, a[3].y));
+                        }
+                        *reinterpret_cast<uint4*>(smem + (out - base) + lane * 128 + ((q ^ (lane & 7)) << 4)) = v;
                     }
-                    st_global_256(y + c, w);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (m0 < p.M && n0 + c < p.N) tma_store_2d(&map_y, (int)n0 + c, m0, out);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
                 }
-            } else {
+            } else if (m < p.M) {
+                TY* y = static_cast<TY*>(p.y) + (long long)m * p.N + n0;
 #pragma unroll
                 for (int c = 0; c < 128; ++c)
                     if (n0 + c < p.N) y[c] = from_f32<TY>(c & 1 ? acc[c / 2].y : acc[c / 2].x);
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -199,6 +258,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// y in boxes of 32 rows x 128 bytes.
+template <class TY>
+int out_map(CUtensorMap* m, const Fp8Args& a) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    int rc = encoder(&encode);
+    if (rc) return rc;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.M};
+    const cuuint64_t strides[1] = {(cuuint64_t)a.N * sizeof(TY)};
+    const cuuint32_t box[2] = {128 / sizeof(TY), 32}, es[2] = {1, 1};
+    return encode(m, sizeof(TY) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.y, dims,
+                  strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QG_OK
+               : QG_ERR_UNSUPPORTED;
 }
 
 template <class TY>
@@ -210,11 +285,13 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dc.device] = 1;
     }
-    CUtensorMap ma, mw;
+    CUtensorMap ma, mw, my = {};
     int rc = code_map(&ma, a.a, a.M, a.K, kBM);
     if (rc == QG_OK) rc = code_map(&mw, a.w, a.N, a.K, kBN);
+    // TMA stores want rows of y on 16-byte boundaries
+    const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.N * sizeof(TY) % 16 == 0;
+    if (rc == QG_OK && vec) rc = out_map<TY>(&my, a);
     if (rc) return rc;
-    const bool vec = reinterpret_cast<uintptr_t>(a.y) % 32 == 0 && a.N * sizeof(TY) % 32 == 0;
     const Params p{a.sa, a.sw, a.y, (int)a.M, (int)a.N, (int)((a.K + 127) / 128), vec, dc.err};
     const long long tiles = ((a.M + kBM - 1) / kBM) * ((a.N + kBN - 1) / kBN);
     cudaLaunchConfig_t cfg{};
@@ -227,7 +304,7 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ma, mw, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ma, mw, my, p);
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }
 
