@@ -21,14 +21,28 @@ namespace {
 // At the end, with c, s, t of the whole row,
 //     log p(x) = ln2 (x log2(e) - c - log2 s),  entropy = ln2 (log2 s - t / s).
 //
-// The k largest come almost for free: every thread also keeps its best logit
-// as a key (value, then lower id). If T is the k-th largest of the threads'
-// keys, a logit below T has k larger ones; so only the k threads with keys of T
-// and more can hold any of the k largest, and their logits, a small part of
-// the row, are read again.
-constexpr int kThreads = 256;
+// A producer warp copies the row's aligned middle into a ring of 16 KB stages by
+// bulk copies, and on into the CTA's next row, so that the loads go on while a row
+// is being finished and cost the other warps no instructions (they issue almost
+// all the time: some 8 instructions per logit).
+//
+// The k largest come almost for free: every thread also keeps its largest logit
+// and the chunk that has it. If k of these (of equal ones the one in the earlier
+// chunk first) are at least T, a logit below T has k before it; so only the threads
+// with T and larger ones can hold any of the k largest, and their logits, a small
+// part of the row, are read again. That and the joining of the
+// statistics is the work of one more warp while the others read the next row
+// (done by all warps between two rows it took 55 us of 159 for 2048 rows of
+// 131072 bf16 logits with the 5 largest).
+constexpr int kThreads = 256;               // that read logits; a producer and a finishing warp more
 constexpr int kWarps = kThreads / 32;
 constexpr int kTop = 32;                    // most alternatives
+constexpr int kPer = 2;                     // chunks per thread and stage
+constexpr int kStageChunks = kPer * kThreads;
+constexpr int kStages = 6;
+constexpr int kRing = kStages * kStageChunks * 32;
+constexpr int kCtasPerSm = 2;
+constexpr float kLazy = 20.f;               // exponentials up to e^20 are left as they are
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 using Key = unsigned long long;
@@ -118,6 +132,17 @@ struct Row {
     int off, lo, hi;
     int c_lo, c_hi;  // its chunks
 
+    __device__ __forceinline__ void set(const LogprobArgs& a, long long r, int part, int parts) {
+        constexpr int N = Chunk<T>::kN;
+        x = static_cast<const T*>(a.x) + r * a.stride;
+        off = (int)(reinterpret_cast<uintptr_t>(x) % 32 / sizeof(T));
+        base = x - off;
+        const int chunks = (int)((a.V + off + N - 1) / N);
+        c_lo = (int)((long long)chunks * part / parts);
+        c_hi = (int)((long long)chunks * (part + 1) / parts);
+        lo = max(0, c_lo * N - off);
+        hi = (int)min((long long)a.V, (long long)c_hi * N - off);
+    }
     __device__ __forceinline__ bool inside(int c) const {
         return c * Chunk<T>::kN - off >= lo && (c + 1) * Chunk<T>::kN - off <= hi;
     }
@@ -150,7 +175,7 @@ __device__ __forceinline__ Stats join(const Stats& a, const Stats& b) {
 }
 
 struct Thread {
-    Stats st;       // NaN left out of the maximum
+    Stats st;
     float best;     // the largest logit, NaN above all, and the first chunk with it
     int best_chunk;
     int above;
@@ -167,32 +192,62 @@ struct Thread {
             best = cm;
             best_chunk = chunk;
         }
-        if (cm > st.c) {
-            const float g = fmaxf((st.c - cm) * kLog2e, -200.f);  // at first from -infinity, with s = t = 0
+        if (cm > st.c + kLazy) {  // always at first: st.c is -infinity
+            const float g = fmaxf((st.c - cm) * kLog2e, -200.f);  // with s = t = 0 then
             const float f = ex2(g);
             st.t = f * (st.t + g * st.s);
             st.s *= f;
             st.c = cm;
         }
-        const float ref = st.c == -INFINITY ? 0.f : st.c;
-        const float2 l2 = make_float2(kLog2e, kLog2e), mc = make_float2(-ref, -ref);
+        const float2 l2 = make_float2(kLog2e, kLog2e);
         float2 ss = make_float2(0.f, 0.f), tt = make_float2(0.f, 0.f);
+        {
+            const float2 mc = make_float2(-st.c * kLog2e, -st.c * kLog2e);
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            float2 d = __fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), mc), l2);
-            // 2^-200 is 0 in f32: masked logits add 0, not 0 times infinity; NaN stays
-            d.x = max_nan(d.x, -200.f);
-            d.y = max_nan(d.y, -200.f);
-            const float2 e = make_float2(ex2(d.x), ex2(d.y));
-            ss = __fadd2_rn(ss, e);
-            tt = __ffma2_rn(e, d, tt);
+            for (int i = 0; i < N; i += 2) {
+                const float2 d = __ffma2_rn(make_float2(v[i], v[i + 1]), l2, mc);
+                const float2 e = make_float2(ex2(d.x), ex2(d.y));
+                ss = __fadd2_rn(ss, e);
+                tt = __ffma2_rn(e, d, tt);
+            }
+        }
+        // Not finite: a masked logit (0 times infinity), a value whose multiple by
+        // log2(e) is out of range, or a NaN. Again, difference first and cut off.
+        if (!(fabsf(tt.x + tt.y) < 1e30f)) {
+            const float ref = st.c == -INFINITY ? 0.f : st.c;
+            const float2 mc = make_float2(-ref, -ref);
+            ss = tt = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                float2 d = __fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), mc), l2);
+                // 2^-200 is 0 in f32: a masked logit adds 0; NaN stays
+                d.x = max_nan(d.x, -200.f);
+                d.y = max_nan(d.y, -200.f);
+                const float2 e = make_float2(ex2(d.x), ex2(d.y));
+                ss = __fadd2_rn(ss, e);
+                tt = __ffma2_rn(e, d, tt);
+            }
         }
         st.s += ss.x + ss.y;
         st.t += tt.x + tt.y;
     }
 };
 
-// The warp's 32 keys in descending order over its lanes.
+// The larger 32 of the keys in two descending lists over the warp's lanes,
+// descending: lane i's larger one of a[i] and b[31 - i] is a bitonic sequence.
+__device__ __forceinline__ Key merge_top(Key a, Key b) {
+    const int lane = threadIdx.x & 31;
+    const Key r = __shfl_sync(0xFFFFFFFFu, b, 31 - lane);
+    Key k = a > r ? a : r;
+#pragma unroll
+    for (int step = 16; step; step /= 2) {
+        const Key o = __shfl_xor_sync(0xFFFFFFFFu, k, step);
+        k = ((lane & step) == 0) == (k > o) ? k : o;
+    }
+    return k;
+}
+
+// The warp's keys, descending over its lanes.
 __device__ __forceinline__ Key warp_sort(Key k) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -206,33 +261,19 @@ __device__ __forceinline__ Key warp_sort(Key k) {
     return k;
 }
 
-// Puts key k (lists: n descending lists of kTop keys; this thread's is number
-// `list`, place `lane`) to its place among all of them, if that is below `top`.
-// Equal keys occur only as 0, the absent one, which has no place.
-template <int NL>
-__device__ __forceinline__ int rank_of(Key k, int list, int lane, const Key (*lists)[kTop]) {
-    int rank = lane;
-    auto get = [&](int o, int i) { return lists[o][i]; };
-#pragma unroll
-    for (int j = 1; j < NL; ++j) {  // the searches are independent of one another
-        const int o = (list + j) % NL;
-        int at = 0;  // keys of list o above k
-#pragma unroll
-        for (int step = 16; step; step /= 2)
-            if (get(o, at + step - 1) > k) at += step;
-        at += at == 31 && get(o, 31) > k;
-        rank += at;
-    }
-    return rank;
+// Puts `in` to its place in a list over the warp's lanes, which lets its last go.
+__device__ __forceinline__ Key insert(Key list, Key in) {
+    const int lane = threadIdx.x & 31;
+    const int at = __popc(__ballot_sync(0xFFFFFFFFu, list > in));
+    const Key up = __shfl_up_sync(0xFFFFFFFFu, list, 1);
+    return lane == at ? in : lane > at ? up : list;
 }
 
-// The statistics of the first W lanes in lane 0 (W a power of two; lanes hold
-// theirs with period W). Both sides of an exchange join in the same order.
-template <int W>
+// The lanes' statistics in one. Both sides of an exchange join in the same order.
 __device__ __forceinline__ void join_lanes(Stats& st, int& above) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = W / 2; i; i >>= 1) {
+    for (int i = 16; i; i >>= 1) {
         const Stats o{__shfl_xor_sync(0xFFFFFFFFu, st.c, i), __shfl_xor_sync(0xFFFFFFFFu, st.s, i),
                       __shfl_xor_sync(0xFFFFFFFFu, st.t, i)};
         st = lane & i ? join(o, st) : join(st, o);
@@ -240,210 +281,285 @@ __device__ __forceinline__ void join_lanes(Stats& st, int& above) {
     }
 }
 
-// The best key of a chunk.
-template <class T>
-__device__ __forceinline__ Key best_of(const Row<T>& row, int c) {
-    constexpr int N = Chunk<T>::kN;
-    Chunk<T> ch;
-    row.load(c, ch);
-    float v[N];
-    ch.get(v);
-    Key best = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int id = c * N - row.off + i;
-        const Key k = id >= row.lo && id < row.hi ? key_of(v[i], id) : 0;
-        best = k > best ? k : best;
-    }
-    return best;
-}
+// What a row's readers leave to the finishing warp.
+struct Left {
+    float c[kThreads], s[kThreads], t[kThreads], best[kThreads];
+    int chunk[kThreads], above[kThreads];
+};
 
+// CTA x of a cluster (grid x) has share x of its rows: y, y + grid y, ...
 template <class T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) row_kernel(const LogprobArgs a, unsigned* err) {
+__global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) row_kernel(const LogprobArgs a, unsigned* err) {
     constexpr int N = Chunk<T>::kN;
-    __shared__ Key lists[kWarps][kTop];
-    __shared__ Key found[kTop];      // the share's largest
-    __shared__ int owner[kTop];      // the threads that can hold them
-    __shared__ Stats stats[kWarps];
-    __shared__ int aboves[kWarps];
-    __shared__ Stats all;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages];
+    __shared__ __align__(8) uint64_t more[4];  // left[i] written, taken
+    __shared__ Left left[2];
+    __shared__ int owner[kThreads];            // the threads that can hold the share's largest
+    __shared__ Key found[kTop];                // those
+    __shared__ Stats all;                      // and its statistics
     __shared__ int all_above;
-    __shared__ Key threshold;
-    fp8::pdl_trigger();
-    fp8::pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int parts = (int)gridDim.x, part = (int)blockIdx.x;
-    const long long r = blockIdx.y + (long long)gridDim.y * blockIdx.z;
-    if (r >= a.M) return;  // the whole cluster: it has one row
     const int V = (int)a.V;
-    Row<T> row;
-    row.x = static_cast<const T*>(a.x) + r * a.stride;
-    row.off = (int)(reinterpret_cast<uintptr_t>(row.x) % 32 / sizeof(T));
-    row.base = row.x - row.off;
-    const int chunks = (int)(((long long)V + row.off + N - 1) / N);
-    row.c_lo = (int)((long long)chunks * part / parts);
-    row.c_hi = (int)((long long)chunks * (part + 1) / parts);
-    row.lo = max(0, row.c_lo * N - row.off);
-    row.hi = (int)min((long long)V, (long long)row.c_hi * N - row.off);
-
-    const int64_t target = a.targets[r];
-    const bool given = target >= 0 && target < V;
-    const float xt = given ? to_f32(row.x[target]) : INFINITY;  // without a target no count is needed
-    if (target >= V && threadIdx.x == 0 && part == 0) report_error(err, DEVERR_INDEX);
-
-    uint32_t xt2 = 0;
-    if constexpr (sizeof(T) == 2) xt2 = pack2<T>(xt, xt);  // exact: xt is a logit (or infinity)
-    Thread th{{-INFINITY, 0.f, 0.f}, -INFINITY, row.c_lo + (int)threadIdx.x, 0};
     const bool top = a.k > 0;
-    // Chunk c_lo + threadIdx.x and every kThreads-th after it, four in flight.
-    constexpr int U = 4;
-    for (int c0 = row.c_lo + threadIdx.x; c0 < row.c_hi; c0 += U * kThreads) {
-        Chunk<T> ch[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = c0 + u * kThreads;
-            if (c < row.c_hi) row.load(c, ch[u]);
+    cg::cluster_group cl = cg::this_cluster();
+    auto full = [&](int i) { return smem_addr(bars + i); };
+    auto empty = [&](int i) { return smem_addr(bars + kStages + i); };
+    auto left_full = [&](int i) { return smem_addr(more + i); };
+    auto left_empty = [&](int i) { return smem_addr(more + 2 + i); };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(left_full(i), kWarps);
+            mbar_init(left_empty(i), 1);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = c0 + u * kThreads;
-            if (c >= row.c_hi) break;
-            float v[N];
-            ch[u].get(v);
-            th.take<T>(v, ch[u], c, xt, xt2);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), kWarps);
         }
-    }
-
-    // ------------------------------------------------- the share's statistics
-    Stats st = th.st;
-    int above = th.above;
-    join_lanes<32>(st, above);
-    if (lane == 0) {
-        stats[warp] = st;
-        aboves[warp] = above;
-    }
-    if (top) {
-        Key best = 0;
-        if (th.best_chunk < row.c_hi) best = best_of(row, th.best_chunk);
-        lists[warp][lane] = warp_sort(best);
-        if (threadIdx.x < kTop) {
-            owner[threadIdx.x] = -1;
-            found[threadIdx.x] = 0;
-        }
-        if (threadIdx.x == 0) threshold = 0;
+        fence_mbar_init();
     }
     __syncthreads();
-    if (warp == 0) {
-        st = stats[lane % kWarps];
-        above = aboves[lane % kWarps];
-        join_lanes<kWarps>(st, above);
-        if (lane == 0) {
-            all = st;
-            all_above = above;
+    fp8::pdl_trigger();
+    fp8::pdl_wait();
+    int st = 0;          // place of the next stage in the ring
+    uint32_t ph = 0;     // and its phase
+
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ producer
+        int i = 0;
+        bool ok = true;
+        for (long long r = blockIdx.y; r < a.M; r += gridDim.y) {
+            Row<T> row;
+            row.set(a, r, part, parts);
+            const int in_lo = row.inside(row.c_lo) ? row.c_lo : row.c_lo + 1;
+            const int in_hi = row.c_hi > row.c_lo && row.inside(row.c_hi - 1) ? row.c_hi : row.c_hi - 1;
+            for (int c = row.c_lo; c < row.c_hi; c += kStageChunks, ++i) {
+                if (i >= kStages && ok && !warp_bar_wait(empty(st), ph ^ 1)) {
+                    if (lane == 0) report_error(err, DEVERR_WAIT_EMPTY);
+                    ok = false;
+                }
+                if (lane == 0 && ok) {
+                    const int lo = max(c, in_lo), hi = min(c + kStageChunks, in_hi);
+                    const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 32u : 0u;
+                    mbar_arrive_expect_tx(full(st), bytes);
+                    if (bytes)
+                        prefill::bulk_g2s_nohint(smem_addr(ring) + (st * kStageChunks + lo - c) * 32,
+                                                 row.base + (long long)lo * N, bytes, full(st));
+                }
+                __syncwarp();
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (parts > 1) {  // the others' two meetings of this row
+                cl.sync();
+                cl.sync();
+            }
         }
+        // Every copy is waited for by the threads that read it, unless they gave up.
+        for (int j = max(0, i - kStages); ok && j < i; ++j)
+            if (!warp_bar_wait(full(j % kStages), (j / kStages) & 1) && lane == 0)
+                report_error(err, DEVERR_WAIT_DRAIN);
+        return;
     }
 
-    // --------------------------------------------------- the share's largest
-    if (top) {
-        const Key k = lists[warp][lane];
-        const int rank = k ? rank_of<kWarps>(k, warp, lane, lists) : kTop;
-        if (rank < a.k) {
-            // the thread whose chunk holds that logit
-            owner[rank] = ((id_of(k) + row.off) / N - row.c_lo) % kThreads;
-            if (rank == a.k - 1) threshold = k;
-        }
-        __syncthreads();
-        const Key least = threshold;
-        __syncthreads();  // the lists are written again
-        Key mine = 0, worst = 0;  // this warp's largest, lane i the i-th; the k-th of them
-        for (int o = warp; o < a.k; o += kWarps) {
-            const int t = owner[o];
-            if (t < 0) break;
-            const int n = (row.c_hi - row.c_lo - t + kThreads - 1) / kThreads;  // that thread's chunks
-            for (int i0 = 0; i0 < n; i0 += 32) {
-                const int c = row.c_lo + t + (i0 + lane) * kThreads;
-                float v[N];
-                const bool has = i0 + lane < n;
-                if (has) {
-                    Chunk<T> ch;
-                    row.load(c, ch);
-                    ch.get(v);
+    if (warp < kWarps) {
+        // ------------------------------------------------------------- readers
+        int64_t target = blockIdx.y < a.M ? a.targets[blockIdx.y] : -1;
+        float xt = target >= 0 && target < V ? to_f32(static_cast<const T*>(a.x)[blockIdx.y * a.stride + target])
+                                             : INFINITY;  // without a target nothing is counted
+        bool ok = true;
+        int rows = 0;
+        for (long long r = blockIdx.y; r < a.M; r += gridDim.y, ++rows) {
+            Row<T> row;
+            row.set(a, r, part, parts);
+            const long long rn = r + gridDim.y;
+            const int64_t target_n = rn < a.M ? a.targets[rn] : -1;
+            uint32_t xt2 = 0;
+            if constexpr (sizeof(T) == 2) xt2 = pack2<T>(xt, xt);  // exact: xt is a logit (or infinity)
+            Thread th{{-INFINITY, 0.f, 0.f}, -INFINITY, row.c_lo + (int)threadIdx.x, 0};
+#pragma unroll 1
+            for (int c0 = row.c_lo; c0 < row.c_hi; c0 += kStageChunks) {
+                if (ok && !warp_bar_wait(full(st), ph)) {
+                    if (lane == 0) report_error(err, DEVERR_WAIT_FULL);
+                    ok = false;  // the results are lost; the barriers are still met
                 }
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    const int c = c0 + u * kThreads + threadIdx.x;
+                    if (c < row.c_hi) {
+                        Chunk<T> ch;
+                        if (row.inside(c)) {
+                            const uint4* p = reinterpret_cast<const uint4*>(
+                                ring + (st * kStageChunks + u * kThreads + threadIdx.x) * 32);
+                            const uint4 lo = p[0], hi = p[1];
+                            ch.w[0] = lo.x; ch.w[1] = lo.y; ch.w[2] = lo.z; ch.w[3] = lo.w;
+                            ch.w[4] = hi.x; ch.w[5] = hi.y; ch.w[6] = hi.z; ch.w[7] = hi.w;
+                        } else {
+                            row.load(c, ch);
+                        }
+                        float v[N];
+                        ch.get(v);
+                        th.take<T>(v, ch, c, xt, xt2);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty(st));
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            xt = target_n >= 0 && target_n < V ? to_f32(static_cast<const T*>(a.x)[rn * a.stride + target_n])
+                                               : INFINITY;
+            if (rows >= 2 && ok && !warp_bar_wait(left_empty(rows & 1), ((rows >> 1) & 1) ^ 1)) {
+                if (lane == 0) report_error(err, DEVERR_WAIT_EMPTY);
+                ok = false;
+            }
+            Left& l = left[rows & 1];
+            l.c[threadIdx.x] = th.st.c;
+            l.s[threadIdx.x] = th.st.s;
+            l.t[threadIdx.x] = th.st.t;
+            l.best[threadIdx.x] = th.best;
+            l.chunk[threadIdx.x] = th.best_chunk;
+            l.above[threadIdx.x] = th.above;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(left_full(rows & 1));
+            if (parts > 1) {
+                cl.sync();
+                cl.sync();
+            }
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------- finishing warp
+    int rows = 0;
+    bool ok = true;
+    for (long long r = blockIdx.y; r < a.M; r += gridDim.y, ++rows) {
+        Row<T> row;
+        row.set(a, r, part, parts);
+        const int64_t target = a.targets[r];
+        const bool given = target >= 0 && target < V;
+        if (target >= V && lane == 0 && part == 0) report_error(err, DEVERR_INDEX);
+        const float xt = given ? to_f32(row.x[target]) : 0.f;
+        if (ok && !warp_bar_wait(left_full(rows & 1), (rows >> 1) & 1)) {
+            if (lane == 0) report_error(err, DEVERR_WAIT_FULL);
+            ok = false;
+        }
+        const Left& l = left[rows & 1];
+        Stats st{-INFINITY, 0.f, 0.f};
+        int above = 0;
+        Key own[kWarps];  // of threads lane, 32 + lane, ...: best logit, earlier chunk first
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const int t = i * 32 + lane;
+            st = join(st, Stats{l.c[t], l.s[t], l.t[t]});
+            above += l.above[t];
+            const int c = l.chunk[t];
+            own[i] = c < row.c_hi ? (Key)value_key(l.best[t]) << 32 | (0xFFFFFFFFu - (uint32_t)c) : 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(left_empty(rows & 1));
+        join_lanes(st, above);
+
+        Key mine = 0;  // the share's largest, lane i the i-th
+        if (top) {
+            // T here is the k-th largest of the lanes' largest keys: as good a bound,
+            // one sort away, which a few threads more than k reach (all, if there
+            // are not k lanes with keys).
+            Key m = own[0];
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) m = own[i] > m ? own[i] : m;
+            const Key t = __shfl_sync(0xFFFFFFFFu, warp_sort(m), a.k - 1);
+            const float least = t ? value_of(t) : -INFINITY;
+            int owners = 0;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const bool in = own[i] && own[i] >= t;
+                const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
+                if (in) owner[owners + __popc(who & ((1u << lane) - 1))] = i * 32 + lane;
+                owners += __popc(who);
+            }
+            __syncwarp();
+            Key worst = 0;  // the k-th of `mine`
+            // The owners' chunks, all in a line, 32 at a time; the next ones on the way.
+            const int per = (row.c_hi - row.c_lo + kThreads - 1) / kThreads, n = owners * per;
+            auto at = [&](int q) { return q < n ? row.c_lo + owner[q / per] + q % per * kThreads : row.c_hi; };
+            int c = at(lane);
+            Chunk<T> ch;
+            if (c < row.c_hi) row.load(c, ch);
+            for (int q = 0; q < n; q += 32) {
+                const int cn = at(q + 32 + lane);
+                Chunk<T> next;
+                if (cn < row.c_hi) row.load(cn, next);
+                float v[N];
+                ch.get(v);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     const int id = c * N - row.off + i;
-                    const Key key = has && id >= row.lo && id < row.hi ? key_of(v[i], id) : 0;
-                    unsigned who = __ballot_sync(0xFFFFFFFFu, key && key >= least && key > worst);
+                    const bool may = c < row.c_hi && id >= row.lo && id < row.hi && !(v[i] < least);
+                    if (!__any_sync(0xFFFFFFFFu, may)) continue;
+                    const Key key = may ? key_of(v[i], id) : 0;
+                    unsigned who = __ballot_sync(0xFFFFFFFFu, key > worst);
                     while (who) {
-                        const int src = __ffs(who) - 1;
-                        const Key in = __shfl_sync(0xFFFFFFFFu, key, src);
-                        const int at = __popc(__ballot_sync(0xFFFFFFFFu, mine > in));
-                        const Key up = __shfl_up_sync(0xFFFFFFFFu, mine, 1);
-                        mine = lane == at ? in : lane > at ? up : mine;
+                        mine = insert(mine, __shfl_sync(0xFFFFFFFFu, key, __ffs(who) - 1));
                         worst = __shfl_sync(0xFFFFFFFFu, mine, a.k - 1);
                         who &= who - 1;
                         who &= __ballot_sync(0xFFFFFFFFu, key > worst);
                     }
                 }
+                c = cn;
+                ch = next;
             }
         }
-        lists[warp][lane] = mine;
-        __syncthreads();
-        const int place = mine ? rank_of<kWarps>(mine, warp, lane, lists) : kTop;
-        if (place < a.k) found[place] = mine;
-    }
 
-    // --------------------------------------------------------- the whole row
-    cg::cluster_group cl = cg::this_cluster();
-    if (parts > 1) cl.sync();
-    else __syncthreads();
-    if (part == 0) {
-        if (parts > 1) {  // the shares' results into this CTA's shared memory
-            if (warp < parts) {
-                if (top) lists[warp][lane] = *cl.map_shared_rank(&found[lane], warp);
-                if (lane == 0) {
-                    stats[warp] = *cl.map_shared_rank(&all, warp);
-                    aboves[warp] = *cl.map_shared_rank(&all_above, warp);
+        if (parts > 1) {  // the shares' results meet in the first CTA
+            found[lane] = mine;
+            if (lane == 0) {
+                all = st;
+                all_above = above;
+            }
+            cl.sync();
+            if (part == 0) {
+                const int p = lane % parts;
+                st = *cl.map_shared_rank(&all, p);
+                above = *cl.map_shared_rank(&all_above, p);
+                if (lane >= parts) {
+                    st = Stats{-INFINITY, 0.f, 0.f};
+                    above = 0;
                 }
-            } else {
-                if (top) lists[warp][lane] = 0;
-                if (lane == 0) {
-                    stats[warp] = Stats{-INFINITY, 0.f, 0.f};
-                    aboves[warp] = 0;
+                join_lanes(st, above);
+                if (top) {
+                    Key others[7];
+#pragma unroll
+                    for (int o = 0; o < 7; ++o) others[o] = o + 1 < parts ? *cl.map_shared_rank(&found[lane], o + 1) : 0;
+#pragma unroll
+                    for (int o = 0; o < 7; ++o)
+                        if (o + 1 < parts) mine = merge_top(mine, others[o]);
                 }
             }
-            __syncthreads();
         }
-        Stats s = all;
-        int n = all_above;
-        if (parts > 1) {
-            s = stats[lane % kWarps];
-            n = aboves[lane % kWarps];
-            join_lanes<kWarps>(s, n);
-            s.c = __shfl_sync(0xFFFFFFFFu, s.c, 0);
-            s.s = __shfl_sync(0xFFFFFFFFu, s.s, 0);
-            s.t = __shfl_sync(0xFFFFFFFFu, s.t, 0);
-        }
-        const float ls = log2f(s.s);
-        const bool nan = s.s != s.s, none = s.c == -INFINITY && !nan;
-        auto logp = [&](float x) {
-            return nan ? NAN : x == -INFINITY ? -INFINITY : (x - s.c) - kLn2 * ls;
-        };
-        if (threadIdx.x == 0) {
-            a.logprobs[r] = given ? logp(xt) : 0.f;
-            a.entropy[r] = nan ? NAN : none ? 0.f : kLn2 * (ls - s.t / s.s);
-            a.ranks[r] = !given ? -1 : xt != xt ? 0 : n;
-        }
-        if (top && warp < parts) {
-            const Key k = parts > 1 ? lists[warp][lane] : found[lane];
-            const int rank = !k ? kTop : parts > 1 ? rank_of<kWarps>(k, warp, lane, lists) : lane;
-            if (rank < a.k) {
-                a.top_ids[r * a.k + rank] = id_of(k);
-                a.top_values[r * a.k + rank] = logp(value_of(k));
+        if (part == 0) {
+            st.c = __shfl_sync(0xFFFFFFFFu, st.c, 0);
+            st.s = __shfl_sync(0xFFFFFFFFu, st.s, 0);
+            const float ls = log2f(st.s);
+            const bool nan = st.s != st.s, none = st.c == -INFINITY && !nan;
+            auto logp = [&](float x) { return nan ? NAN : x == -INFINITY ? -INFINITY : (x - st.c) - kLn2 * ls; };
+            if (lane == 0) {
+                a.logprobs[r] = given ? logp(xt) : 0.f;
+                a.entropy[r] = nan ? NAN : none ? 0.f : kLn2 * (ls - st.t / st.s);
+                a.ranks[r] = !given ? -1 : xt != xt ? 0 : above;
+            }
+            if (lane < a.k) {
+                a.top_ids[r * a.k + lane] = id_of(mine);
+                a.top_values[r * a.k + lane] = logp(value_of(mine));
             }
         }
+        if (parts > 1) cl.sync();  // the shares' results have been read
     }
-    if (parts > 1) cl.sync();  // shared memory is read until here
 }
 
 }  // namespace
@@ -457,10 +573,18 @@ int logprobs_launch(const DevCtx& dc, const LogprobArgs& a, cudaStream_t s) {
         while (parts < 8 && a.M * parts * 2 <= 2 * dc.num_sms &&
                a.V >= (long long)parts * 2 * 2 * kThreads * Chunk<T>::kN)
             parts *= 2;
+        static int configured[64] = {0};
+        if (!configured[dc.device]) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(row_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+            if (e != cudaSuccess) return cuda_fail(e);
+            configured[dc.device] = 1;
+        }
         cudaLaunchConfig_t cfg{};
-        const long long y = std::min<long long>(a.M, 65535);
-        cfg.gridDim = dim3((unsigned)parts, (unsigned)y, (unsigned)((a.M + y - 1) / y));
-        cfg.blockDim = dim3(kThreads);
+        const long long most = std::max(1, dc.num_sms * kCtasPerSm / parts);
+        cfg.gridDim = dim3((unsigned)parts, (unsigned)std::min<long long>(a.M, most));
+        cfg.dynamicSmemBytes = kRing;
+        cfg.blockDim = dim3(kThreads + 64);
         cfg.stream = s;
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
