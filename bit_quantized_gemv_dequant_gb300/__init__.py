@@ -178,12 +178,13 @@ def _scratch(need, device, workspace, stream):
         return None, 0
     # One buffer per (device, stream): two calls on different streams may run
     # at the same time and must not share split-K scratch.
-    key = (torch.device(device).index, stream)
-    with _LOCK:
-        buf = _WS.get(key)
-        if buf is None or buf.numel() < need:
-            buf = torch.empty(need, dtype=torch.uint8, device=device)
-            _WS[key] = buf
+    key = (device.index, stream)
+    buf = _WS.get(key)
+    if buf is None or buf.numel() < need:
+        with _LOCK:
+            buf = _WS.get(key)
+            if buf is None or buf.numel() < need:
+                buf = _WS[key] = torch.empty(need, dtype=torch.uint8, device=device)
     return buf.data_ptr(), buf.numel()
 
 
@@ -349,6 +350,7 @@ def dequant_affine(q, scales, biases, N, K, group_size, packed, out=None, *, str
 
 # ------------------------------------------------------- serving operators
 _DTYPES = {torch.float32: QG_F32, torch.float16: QG_F16, torch.bfloat16: QG_BF16}
+_E4M3 = torch.float8_e4m3fn
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -363,17 +365,18 @@ def _rows(t: torch.Tensor, name: str, dims: int):
     rows may lie apart (a part of a fused projection, a padded vocabulary)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    width = t.shape[1] if dims == 2 else t.shape[1] * t.shape[2]
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
+    width = shape[1] if dims == 2 else shape[1] * shape[2]
     if t.is_contiguous():
         return t.data_ptr(), width
-    step = 1
+    strides, step = t.stride(), 1
     for i in range(dims - 1, 0, -1):
-        if t.shape[i] > 1 and t.stride(i) != step:
+        if shape[i] > 1 and strides[i] != step:
             raise ValueError(f"{name} must have dense rows")
-        step *= t.shape[i]
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+        step *= shape[i]
+    return t.data_ptr(), strides[0] if shape[0] > 1 else width
 
 
 def _same(t: torch.Tensor, name: str, *shape) -> None:
@@ -403,18 +406,22 @@ def quantize_fp8_b128(x, codes=None, scales=None, *, stream=None):
     row, [M, ceil(K / 128)]."""
     at, stride = _rows(x, "x", 2)
     M, K = x.shape
-    KB = (K + 127) // 128
+    dev = x.device
     if codes is None:
-        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+        codes = torch.empty((M, K), dtype=_E4M3, device=dev)
+        codes_at = codes.data_ptr()
     else:
         _same(codes, "codes", M, K)
+        codes_at = _dev(codes, "codes", _E4M3)
     if scales is None:
-        scales = torch.empty((M, KB), dtype=torch.float32, device=x.device)
+        scales = torch.empty((M, (K + 127) // 128), dtype=torch.float32, device=dev)
+        scales_at = scales.data_ptr()
     else:
-        _same(scales, "scales", M, KB)
-    _check(lib().quantize_fp8_b128(at, _dtype(x, "x"), stride, _dev(codes, "codes", torch.float8_e4m3fn),
-                                   _dev(scales, "scales", torch.float32), M, K, _stream(stream)),
-           "quantize_fp8_b128")
+        _same(scales, "scales", M, (K + 127) // 128)
+        scales_at = _dev(scales, "scales", torch.float32)
+    rc = lib().quantize_fp8_b128(at, _dtype(x, "x"), stride, codes_at, scales_at, M, K, _stream(stream))
+    if rc:
+        raise QGError("quantize_fp8_b128", rc)
     return codes, scales
 
 
@@ -428,15 +435,17 @@ def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, s
     _same(w, "w", N, K)
     _same(a_scales, "a_scales", M, KB)
     _same(w_scales, "w_scales", (N + 127) // 128, KB)
+    at, scales_at = _dev(a, "a", _E4M3), _dev(a_scales, "a_scales", torch.float32)
     if y is None:
         y = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        y_at = y.data_ptr()
     else:
         _same(y, "y", M, N)
-    _check(lib().qmm_fp8_b128(_dev(a, "a", torch.float8_e4m3fn),
-                              _dev(a_scales, "a_scales", torch.float32),
-                              _dev(w, "w", torch.float8_e4m3fn),
-                              _dev(w_scales, "w_scales", torch.float32), _dev(y, "y"),
-                              _dtype(y, "y"), M, N, K, _stream(stream)), "qmm_fp8_b128")
+        y_at = _dev(y, "y")
+    rc = lib().qmm_fp8_b128(at, scales_at, _dev(w, "w", _E4M3), _dev(w_scales, "w_scales", torch.float32),
+                            y_at, _dtype(y, "y"), M, N, K, _stream(stream))
+    if rc:
+        raise QGError("qmm_fp8_b128", rc)
     return y
 
 
@@ -456,33 +465,37 @@ def attn_paged(q, k_cache, v_cache, page_table, q_offsets, context_lens, out=Non
     softcap > 0 caps the scores, window > 0 limits how far back a row sees."""
     at, stride = _rows(q, "q", 3)
     T, Hq, D = q.shape
-    NP, Hkv, page, _ = k_cache.shape
+    NP, Hkv, page, _ = cache = k_cache.shape
     B, width = page_table.shape
-    _same(k_cache, "k_cache", NP, Hkv, page, D)
-    _same(v_cache, "v_cache", NP, Hkv, page, D)
+    i32 = torch.int32
+    if cache[3] != D or v_cache.shape != cache:
+        raise ValueError(f"k_cache and v_cache must have the shape [pages, kv_heads, page_size, {D}]")
     _same(q_offsets, "q_offsets", B + 1)
     _same(context_lens, "context_lens", B)
-    dt = q.dtype
+    dt, dev = q.dtype, q.device
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        out = torch.empty((T, Hq, D), dtype=dt, device=dev)
+        out_at = out.data_ptr()
     else:
         _same(out, "out", T, Hq, D)
+        out_at = _dev(out, "out", dt)
+    lse_at = None
     if lse is not None:
         _same(lse, "lse", T, Hq)
+        lse_at = _dev(lse, "lse", torch.float32)
     elif return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse_at = lse.data_ptr()
     st = _stream(stream)
     max_new = T if max_new is None else int(max_new)
-    need = _size("attn_paged_workspace_size", T, B, max_new, Hq, Hkv, D)
-    ws, wsb = _scratch(need, q.device, workspace, st)
-    _check(lib().attn_paged(at, stride, _dev(k_cache, "k_cache", dt), _dev(v_cache, "v_cache", dt),
-                            _dev(page_table, "page_table", torch.int32),
-                            _dev(q_offsets, "q_offsets", torch.int32),
-                            _dev(context_lens, "context_lens", torch.int32), _dev(out, "out", dt),
-                            None if lse is None else _dev(lse, "lse", torch.float32),
-                            _dtype(q, "q"), T, B, max_new, Hq, Hkv, D, NP, page, width,
-                            D ** -0.5 if scale is None else scale, softcap, window, ws, wsb, st),
-           "attn_paged")
+    ws, wsb = _scratch(_size("attn_paged_workspace_size", T, B, max_new, Hq, Hkv, D), dev, workspace, st)
+    rc = lib().attn_paged(at, stride, _dev(k_cache, "k_cache", dt), _dev(v_cache, "v_cache", dt),
+                          _dev(page_table, "page_table", i32), _dev(q_offsets, "q_offsets", i32),
+                          _dev(context_lens, "context_lens", i32), out_at, lse_at, _dtype(q, "q"),
+                          T, B, max_new, Hq, Hkv, D, NP, page, width,
+                          D ** -0.5 if scale is None else scale, softcap, window, ws, wsb, st)
+    if rc:
+        raise QGError("attn_paged", rc)
     return (out, lse) if lse is not None else out
 
 
@@ -493,18 +506,20 @@ def kv_append(k, v, k_cache, v_cache, slots, *, stream=None):
     int64 [tokens]: page * page_size + place of each row; negative: skipped."""
     ka, ks = _rows(k, "k", 3)
     va, vs = _rows(v, "v", 3)
-    T, H, D = k.shape
-    NP, _, page, _ = k_cache.shape
-    _same(v, "v", T, H, D)
-    _same(k_cache, "k_cache", NP, H, page, D)
-    _same(v_cache, "v_cache", NP, H, page, D)
+    T, H, D = shape = k.shape
+    NP, _, page, _ = cache = k_cache.shape
+    if v.shape != shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be alike")
+    if v_cache.shape != cache or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be alike")
+    if cache[1] != H or cache[3] != D:
+        raise ValueError(f"k_cache and v_cache must have the shape [pages, {H}, page_size, {D}]")
     _same(slots, "slots", T)
-    if v.dtype != k.dtype or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k and v, and their caches, must be of one type")
-    _check(lib().kv_append(ka, va, ks, vs, _dtype(k, "k"), _dev(k_cache, "k_cache"),
-                           _dev(v_cache, "v_cache"), _dtype(k_cache, "k_cache"),
-                           _dev(slots, "slots", torch.int64), T, H, D, NP, page, _stream(stream)),
-           "kv_append")
+    rc = lib().kv_append(ka, va, ks, vs, _dtype(k, "k"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+                         _dtype(k_cache, "k_cache"), _dev(slots, "slots", torch.int64), T, H, D, NP, page,
+                         _stream(stream))
+    if rc:
+        raise QGError("kv_append", rc)
 
 
 def _planes(cache):
@@ -593,17 +608,19 @@ def token_logprobs(logits, targets, top_k=0, *, stream=None):
     at, stride = _rows(logits, "logits", 2)
     M, V = logits.shape
     _same(targets, "targets", M)
+    targets_at = _dev(targets, "targets", torch.int64)
     k = min(int(top_k), V)
-    dev = logits.device
-    f32, i32 = torch.float32, torch.int32
+    dev, f32, i32 = logits.device, torch.float32, torch.int32
     logprobs = torch.empty(M, dtype=f32, device=dev)
-    entropy, ranks = torch.empty_like(logprobs), torch.empty(M, dtype=i32, device=dev)
+    entropy = torch.empty_like(logprobs)
+    ranks = torch.empty(M, dtype=i32, device=dev)
     top = torch.empty((M, max(k, 0)), dtype=f32, device=dev)
     ids = torch.empty((M, max(k, 0)), dtype=i32, device=dev)
-    _check(lib().token_logprobs(at, _dtype(logits, "logits"), stride,
-                                _dev(targets, "targets", torch.int64), M, V, k,
-                                logprobs.data_ptr(), entropy.data_ptr(), ranks.data_ptr(),
-                                top.data_ptr(), ids.data_ptr(), _stream(stream)), "token_logprobs")
+    rc = lib().token_logprobs(at, _dtype(logits, "logits"), stride, targets_at, M, V, k, logprobs.data_ptr(),
+                              entropy.data_ptr(), ranks.data_ptr(), top.data_ptr(), ids.data_ptr(),
+                              _stream(stream))
+    if rc:
+        raise QGError("token_logprobs", rc)
     return logprobs, entropy, ranks, top, ids
 
 
