@@ -137,8 +137,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long total;
     long long* scratch = reinterpret_cast<long long*>(smem + G::kScratchOff);
     locate<kRT, kKT, kThreads>(w, -1, &total, scratch);
-    const long long begin = cut(total, blockIdx.x, w.ctas), n = cut(total, blockIdx.x + 1, w.ctas) - begin;
-    if (n > 0) {
+    const Cuts cuts(total, w.ctas);
+    if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1;
+    if ((int)blockIdx.x < cuts.n) {
+        const long long begin = cuts(blockIdx.x), n = cuts(blockIdx.x + 1) - begin;
         const Place place = locate<kRT, kKT, kThreads>(w, begin, &total, scratch);
         Walk<kRT, kKT> walk(w, place, n);
         bool ok = true;
@@ -449,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_fence_before();
+                if (threadIdx.x == 0) walk.note(cuts, kRT, blockIdx.x);
                 if (live) {
                     if (!walk.whole) w.ml[pt] = make_float2(m, l);
                     else if (w.a.lse) w.a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
@@ -479,7 +482,7 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     if (rc == QG_OK) rc = cache_map(&mv, w.a, w.a.v, rows);
     if (rc == QG_OK) rc = launch(kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
     if (rc) return rc;
-    return launch_join<T, D, kRT, kKT, 32>(w, s);
+    return launch_join<T, D, kRT, 32>(w, s);
 }
 
 template <class T, int D>

@@ -93,8 +93,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long* scratch = reinterpret_cast<long long*>(smem + G::kScratchOff);
     // The first locate only sums up; the second finds this CTA's first step.
     locate<RT, kKT, kThreads>(w, -1, &total, scratch);
-    const long long begin = cut(total, blockIdx.x, w.ctas), n = cut(total, blockIdx.x + 1, w.ctas) - begin;
-    if (n <= 0) return;
+    const Cuts cuts(total, w.ctas);
+    if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1;
+    if ((int)blockIdx.x >= cuts.n) return;
+    const long long begin = cuts(blockIdx.x), n = cuts(blockIdx.x + 1) - begin;
     const Place place = locate<RT, kKT, kThreads>(w, begin, &total, scratch);
     Walk<RT, kKT> walk(w, place, n);
 
@@ -330,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (nt == 0) w.ml[at] = make_float2(mm, ll);
             }
         }
+        if (threadIdx.x == 0) walk.note(cuts, RT, blockIdx.x);
         named_bar_sync(1, kWarps * 32);  // the buffers are free again
     }
 }
@@ -349,7 +352,7 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     if (rc == QG_OK) rc = cache_map(&mv, w.a, w.a.v, rows);
     if (rc == QG_OK) rc = launch(kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
     if (rc) return rc;
-    return launch_join<T, D, 16 * RB, kKT, 4>(w, s);
+    return launch_join<T, D, 16 * RB, 4>(w, s);
 }
 
 template <class T, int D, int RB>

@@ -8,8 +8,11 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Parts of cut row tiles: two per CTA, RT rows of D outputs, a maximum and a sum.
-size_t part_bytes(const DevCtx& dc, int rt, int d) { return (size_t)dc.num_sms * 2 * rt * (d + 2) * 4; }
+// Parts of cut row tiles: two per CTA, RT rows of D outputs, a maximum and a
+// sum; and a note per CTA.
+size_t part_bytes(const DevCtx& dc, int rt, int d) {
+    return (size_t)dc.num_sms * (2 * rt * (d + 2) * 4 + sizeof(attn::Note));
+}
 
 // Rows per tile, by the most rows that a sequence can have: up to 64 the
 // streaming kernel, whose tile is the least that holds them, else the
@@ -40,6 +43,7 @@ int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, cudaStream_t s) {
     const int rt = row_tile(a);
     w.part = static_cast<float*>(ws);
     w.ml = reinterpret_cast<float2*>(w.part + (size_t)w.ctas * 2 * rt * a.d);
+    w.notes = reinterpret_cast<attn::Note*>(w.ml + (size_t)w.ctas * 2 * rt);
     return rt <= 64 ? attn::launch_few(dc, w, rt / 16, s) : attn::launch_chunk(dc, w, s);
 }
 

@@ -5,11 +5,12 @@
 // tile meets the keys that any of its rows sees in tiles of KT keys. All
 // (row tile, key tile) pairs of the batch, in the order sequence, key head,
 // row tile, key tile, are one line of W steps; CTA c of G takes the steps
-// W c / G .. W (c + 1) / G - 1, so every CTA has the same work to within one
-// step whatever the lengths. Where a cut falls inside a row tile its parts
-// leave (m, l, O) in the workspace and combine_kernel joins them, in the order
-// of the keys. A CTA has at most two such parts: its first segment (slot 0)
-// and its last (slot 1).
+// W c / G .. W (c + 1) / G - 1 (G at most W), so every CTA has the same work to
+// within one step whatever the lengths. Where a cut falls inside a row tile its
+// parts leave (m, l, O) in the workspace and join_kernel joins them, in the
+// order of the keys. A CTA has at most two such parts: its first segment (slot
+// 0) and its last (slot 1). The CTA with a row tile's last part notes down
+// which one that is and where the parts begin.
 #pragma once
 
 #include "fp8_tc.cuh"
@@ -28,8 +29,17 @@ struct Work {
     float cap_in, cap_out;   // 2 log2(e) scale / softcap, softcap * log2(e)
     float* part;             // [G][2][RT][D] unnormalised outputs of cut row tiles
     float2* ml;              // [G][2][RT] their maximum (base 2) and sum
+    struct Note* notes;      // [G]
     int ctas;
     unsigned* err;
+};
+
+// A row tile that ends in a CTA and was begun in another: CTA `from`, slot `slot`.
+struct Note {
+    int from, slot;  // from = -1: none
+    int out_row;     // row of q and out of the tile's first token's first head
+    int rows, r0;    // rows of the sequence, first of the tile
+    int head;
 };
 
 struct Seq {
@@ -143,7 +153,23 @@ __device__ Place locate(const Work& w, long long t, long long* total, long long*
     return at;
 }
 
-__device__ __forceinline__ long long cut(long long total, int c, int ctas) { return total * c / ctas; }
+// The first step of CTA c: total c / n.
+struct Cuts {
+    long long each;  // total / n
+    int rest, n;
+    __device__ Cuts(long long total, int ctas) {
+        n = (int)min((long long)ctas, total);
+        each = n ? total / n : 0;
+        rest = n ? (int)(total - each * n) : 0;
+    }
+    __device__ __forceinline__ long long operator()(int c) const { return each * c + (long long)rest * c / n; }
+    // The CTA whose steps hold step t.
+    __device__ __forceinline__ int holder(long long t) const {
+        int c = (int)min((long long)n - 1, t / each);  // at most a little too far
+        while ((*this)(c) > t) --c;
+        return c;
+    }
+};
 
 // Walks the segments of a CTA's steps: for each, a row tile and the key tiles
 // lo .. hi - 1 of it that are this CTA's.
@@ -164,6 +190,19 @@ struct Walk {
             s = seq_at(w, p.b);
             span = span_of<RT, KT>(w, s, p.tile);
         }
+    }
+    // Leaves this segment's note, when it ends a row tile that another CTA began.
+    __device__ void note(const Cuts& cuts, int rt, int cta) const {
+        if (hi != span.hi || lo == span.lo) return;
+        const long long start = cuts(cta) - (lo - span.lo);
+        const int from = cuts.holder(start);
+        Note& n = w.notes[cta];
+        n.slot = cuts(from) < start ? 1 : 0;
+        n.out_row = s.first * w.a.hq;
+        n.rows = s.rows;
+        n.r0 = p.tile * rt;
+        n.head = p.head * w.group;
+        n.from = from;
     }
     __device__ bool next() {
         if (left <= 0) return false;

@@ -45,11 +45,12 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
     uint32_t at;
-    float v;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
     return v;
 }
 
@@ -226,11 +227,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         cluster_arrive();
         cluster_wait();
-        for (int e = rank * kThreads + threadIdx.x; e < rows * 128; e += split * kThreads) {
-            float v = 0.f;
-            for (int r = 0; r < split; ++r) v += ld_cluster(base + e * 4, r);
-            const long long m = m0 + e / 128, col = n0 + e % 128;
-            if (col < p.N) y[m * p.N + col] = from_f32<TY>(v);
+        for (int e = rank * kThreads + threadIdx.x; e < rows * 32; e += split * kThreads) {
+            float4 v[8];  // all parts under way at once
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                v[r] = r < split ? ld_cluster(base + e * 16, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 1; r < 8; ++r) {
+                v[0].x += v[r].x; v[0].y += v[r].y; v[0].z += v[r].z; v[0].w += v[r].w;
+            }
+            const float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+            const long long m = m0 + e / 32, col = n0 + e % 32 * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col + i < p.N) y[m * p.N + col + i] = from_f32<TY>(o[i]);
         }
         cluster_arrive();
         cluster_wait();
