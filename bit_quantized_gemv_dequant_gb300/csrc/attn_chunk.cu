@@ -86,9 +86,12 @@ __device__ __forceinline__ void fence_async_proxy() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// GEN: scores are formed one by one first (a cap, or a scale that is not
-// positive, under which the largest dot product need not be the largest score).
-template <class T, int D, bool GEN>
+// How scores come from dot products: times a positive scale, which is left to the
+// exponential; capped; or times any scale, under which the largest product need
+// not be the largest score. The latter two are formed before anything else.
+enum Mode : int { kPositive, kCapped, kAnyScale };
+
+template <class T, int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const Work w) {
@@ -355,11 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_ld32_async(s_at + 96, x[3]);
                             }
                         }
-                        if constexpr (GEN) {
+                        if constexpr (MODE != kPositive) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float v = __uint_as_float(x[c][e]);
-                                x[c][e] = __float_as_uint(w.a.softcap > 0.f ? score<true>(w, v) : score<false>(w, v));
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 v = score2<MODE == kCapped>(
+                                    w, make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
+                                x[c][e] = __float_as_uint(v.x);
+                                x[c][e + 1] = __float_as_uint(v.y);
                             }
                         }
                         if (masked) {
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                       __uint_as_float(x[c][e + 1]));
                     }
                     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    if (!GEN) top *= w.scale_log2;
+                    if (MODE == kPositive) top *= w.scale_log2;
                     if (__any_sync(0xFFFFFFFFu, top > m + kLazy)) {
                         const float mn = fmaxf(m, top);
                         const float f = ex2(m - (mn == -INFINITY ? 0.f : mn));
@@ -393,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;
-                    const float2 sc = make_float2(GEN ? 1.f : w.scale_log2, GEN ? 1.f : w.scale_log2);
+                    const float2 sc = make_float2(MODE == kPositive ? w.scale_log2 : 1.f, MODE == kPositive ? w.scale_log2 : 1.f);
                     const float2 off = make_float2(-ref, -ref);
                     float2 sum[4] = {};
 #pragma unroll
@@ -467,10 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <class T, int D, bool GEN>
+template <class T, int D, int MODE>
 int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     static int configured[64] = {0};
-    auto kern = chunk_kernel<T, D, GEN>;
+    auto kern = chunk_kernel<T, D, MODE>;
     if (!configured[dc.device]) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
         if (e != cudaSuccess) return cuda_fail(e);
@@ -486,17 +491,17 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
 }
 
 template <class T, int D>
-int launch_gen(const DevCtx& dc, const Work& w, cudaStream_t s) {
-    return w.a.softcap > 0.f || !(w.scale_log2 > 0.f) ? launch_one<T, D, true>(dc, w, s)
-                                                      : launch_one<T, D, false>(dc, w, s);
+int launch_mode(const DevCtx& dc, const Work& w, cudaStream_t s) {
+    if (w.a.softcap > 0.f) return launch_one<T, D, kCapped>(dc, w, s);
+    return w.scale_log2 > 0.f ? launch_one<T, D, kPositive>(dc, w, s) : launch_one<T, D, kAnyScale>(dc, w, s);
 }
 
 }  // namespace
 
 int launch_chunk(const DevCtx& dc, const Work& w, cudaStream_t s) {
     if (w.a.dtype == QG_F16)
-        return w.a.d == 64 ? launch_gen<__half, 64>(dc, w, s) : launch_gen<__half, 128>(dc, w, s);
-    return w.a.d == 64 ? launch_gen<__nv_bfloat16, 64>(dc, w, s) : launch_gen<__nv_bfloat16, 128>(dc, w, s);
+        return w.a.d == 64 ? launch_mode<__half, 64>(dc, w, s) : launch_mode<__half, 128>(dc, w, s);
+    return w.a.d == 64 ? launch_mode<__nv_bfloat16, 64>(dc, w, s) : launch_mode<__nv_bfloat16, 128>(dc, w, s);
 }
 
 }  // namespace attn

@@ -254,12 +254,17 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Score of a dot product, in base 2: softcap * tanh(scale x / softcap) with
-// tanh(z) = 1 - 2 / (1 + e^2z), whose absolute error is a few 2^-24.
+// Scores of two dot products, in base 2. With a cap, softcap * tanh(scale x /
+// softcap) where tanh(z) = 1 - 2 / (1 + e^2z), whose absolute error is a few
+// 2^-24; an infinite e^2z gives the cap.
 template <bool CAP>
-__device__ __forceinline__ float score(const Work& w, float x) {
-    if (!CAP) return x * w.scale_log2;
-    return w.cap_out * (1.f - __fdividef(2.f, 1.f + ex2(fminf(x * w.cap_in, 126.f))));
+__device__ __forceinline__ float2 score2(const Work& w, float2 x) {
+    if (!CAP) return __fmul2_rn(x, make_float2(w.scale_log2, w.scale_log2));
+    float2 e = __fmul2_rn(x, make_float2(w.cap_in, w.cap_in));
+    e = __fadd2_rn(make_float2(ex2(e.x), ex2(e.y)), make_float2(1.f, 1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+    return __ffma2_rn(e, make_float2(-2.f * w.cap_out, -2.f * w.cap_out), make_float2(w.cap_out, w.cap_out));
 }
 
 // Up to 16 * row_blocks rows per sequence and key head (row_blocks 1, 2, 4).

@@ -86,7 +86,7 @@ int general_launch(const Fp8Args& a, cudaStream_t s) {
 int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     const bool tma = a.K % 16 == 0 && reinterpret_cast<uintptr_t>(a.a) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
-    if (tma) return a.M <= 128 ? fp8::launch_swap(dc, a, s) : fp8::launch_tile(dc, a, s);
+    if (tma) return fp8::swap_is_shorter(dc, a) ? fp8::launch_swap(dc, a, s) : fp8::launch_tile(dc, a, s);
     return a.y_dtype == QG_F32 ? general_launch<float>(a, s) : general_launch<__nv_bfloat16>(a, s);
 }
 

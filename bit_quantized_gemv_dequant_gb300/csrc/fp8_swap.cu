@@ -1,6 +1,7 @@
 // qmm_fp8_b128 for few rows of a: 128 rows of w on the tensor cores' M side, the
 // rows of a on the N side, K split over a thread-block cluster.
 #include <algorithm>
+#include <mutex>
 
 #include "fp8_tc.cuh"
 
@@ -16,21 +17,29 @@ namespace {
 //   warp 0    TMA producer: w tile and a tile of each k block.
 //   warp 1    issues the four MMAs of a k block into an accumulator of its own
 //             (kBufs of them in tensor memory).
-//   warps 4-7 take the accumulators into registers, times
+//   warps 4-7 (and 8-11 from BN = 64 on, for the second half of the rows of a)
+//             take the accumulators into registers, times
 //             a_scale[m, b] * w_scale[n / 128, b] (f32): thread = row of w.
+//
+// The ring takes all of an SM, so a split is limited by how many clusters of its
+// size the GPU can place at once (18 clusters of 8 took two rounds: 12.0 us
+// instead of 7.0 at M = 37, N = 2200, K = 5200).
 //
 // The split's partial sums meet in shared memory over the cluster, each CTA
 // adding up its share of the rows of a in the order of the split: the result
 // does not depend on timing. Threads of a warp hold consecutive n, so stores
 // of y are coalesced.
-constexpr int kThreads = 256;
 constexpr int kScaleBlocks = 16;  // k blocks whose scales are staged at a time
 
 template <int BN>
 struct Geo {
     static constexpr int kStage = 16384 + BN * 128;
     static constexpr int kStages = BN == 128 ? 6 : BN == 64 ? 8 : 10;
-    static constexpr int kBufs = BN == 128 ? 4 : 8;       // accumulators of BN columns
+    static constexpr int kBufs = BN == 16 ? 8 : 256 / BN;  // accumulators of BN columns
+    static constexpr int kGroups = BN >= 64 ? 2 : 1;       // epilogue warpgroups
+    static constexpr int kThreads = 128 + 128 * kGroups;
+    static constexpr int kEpi = 128 * kGroups;             // epilogue threads
+    static constexpr int kOwn = BN / kGroups;              // rows of a per epilogue thread
     static constexpr int kCols = kBufs * BN < 32 ? 32 : kBufs * BN;
     static constexpr int kScaleOff = kStages * kStage;
     static constexpr int kBarOff = kScaleOff + kScaleBlocks * BN * 4;
@@ -55,7 +64,7 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 }
 
 template <int BN, class TY>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Geo<BN>::kThreads, 1)
     swap_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
                 const Params p) {
     using G = Geo<BN>;
@@ -86,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < G::kBufs; ++i) {
             mbar_init(t_full(i), 1);
-            mbar_init(t_empty(i), 4);
+            mbar_init(t_empty(i), 4 * G::kGroups);
         }
         mbar_init(done, 1);
         fence_mbar_init();
@@ -101,10 +110,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
     pdl_wait();
 
-    float2 acc[BN / 2];
+    float2 acc[G::kOwn / 2];
 #pragma unroll
-    for (int i = 0; i < BN / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+    for (int i = 0; i < G::kOwn / 2; ++i) acc[i] = make_float2(0.f, 0.f);
     const int row = (warp & 3) * 32 + lane;
+    const int own0 = (warp >> 2) > 1 ? ((warp >> 2) - 1) * G::kOwn : 0;  // first row of a of this thread
 
     if (warp == 0) {
         if (lane == 0) {
@@ -162,13 +172,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i0 = 0; i0 < nb; i0 += kScaleBlocks) {
             // The scales of the next blocks: [block][row of a], both factors in one.
             const int nk = min(kScaleBlocks, nb - i0);
-            if (i0) named_bar_sync(1, 128);
-            for (int j = threadIdx.x - 128; j < nk * BN; j += 128) {
+            if (i0) named_bar_sync(1, G::kEpi);
+            for (int j = threadIdx.x - 128; j < nk * BN; j += G::kEpi) {
                 const int m = j / nk, b = j % nk;  // consecutive threads, consecutive blocks of a row
                 scales[b * BN + m] = m0 + m < p.M
                     ? __ldg(p.sa + (long long)(m0 + m) * p.KB + b0 + i0 + b) * __ldg(sw + i0 + b) : 0.f;
             }
-            named_bar_sync(1, 128);
+            named_bar_sync(1, G::kEpi);
             for (int b = 0; b < nk; ++b) {
                 const int i = i0 + b, tb = i % G::kBufs;
                 if (!warp_bar_wait(t_full(tb), (i / G::kBufs) & 1)) {
@@ -177,18 +187,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const float4* sc = reinterpret_cast<const float4*>(scales + b * BN);
-                constexpr int kChunk = BN < 32 ? 16 : 32;
+                const float4* sc = reinterpret_cast<const float4*>(scales + b * BN + own0);
+                const uint32_t from = tmem + lanes + tb * BN + own0;
+                constexpr int kChunk = 16, kChunks = G::kOwn / kChunk;
+                uint32_t r2[2][kChunk];
+                tmem_ld16_async(from, r2[0]);
 #pragma unroll
-                for (int c = 0; c < BN; c += kChunk) {
-                    uint32_t r[kChunk];
-                    if constexpr (kChunk == 16) {
-                        tmem_ld16(tmem + lanes + tb * BN + c, r);
+                for (int c = 0; c < G::kOwn; c += kChunk) {
+                    uint32_t(&r)[kChunk] = r2[(c / kChunk) & 1];
+                    tmem_wait16(r);
+                    if (c / kChunk + 1 < kChunks) {
+                        tmem_ld16_async(from + c + kChunk, r2[(c / kChunk + 1) & 1]);
                     } else {
-                        tmem_ld32_async(tmem + lanes + tb * BN + c, r);
-                        tmem_wait32(r);
-                    }
-                    if (c + kChunk == BN) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(t_empty(tb));
@@ -214,20 +224,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (split == 1) {
         if (warp >= 4 && n < p.N) {
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-                if (m0 + c < p.M) y[(m0 + c) * (long long)p.N + n] = from_f32<TY>(c & 1 ? acc[c / 2].y : acc[c / 2].x);
+            for (int c = 0; c < G::kOwn; ++c)
+                if (m0 + own0 + c < p.M)
+                    y[(m0 + own0 + c) * (long long)p.N + n] = from_f32<TY>(c & 1 ? acc[c / 2].y : acc[c / 2].x);
         }
     } else {
         float* part = reinterpret_cast<float*>(smem);  // [row of a][row of w]; the ring is idle
         const int rows = min(BN, p.M - m0);
         if (warp >= 4) {
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-                if (c < rows) part[c * 128 + row] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
+            for (int c = 0; c < G::kOwn; ++c)
+                if (own0 + c < rows) part[(own0 + c) * 128 + row] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
         }
         cluster_arrive();
         cluster_wait();
-        for (int e = rank * kThreads + threadIdx.x; e < rows * 32; e += split * kThreads) {
+        for (int e = rank * G::kThreads + threadIdx.x; e < rows * 32; e += split * G::kThreads) {
             float4 v[8];  // all parts under way at once
 #pragma unroll
             for (int r = 0; r < 8; ++r)
@@ -251,54 +262,105 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// How many clusters of 1 << i CTAs the GPU holds at once, asked once per kernel
+// and device.
 template <int BN, class TY>
-int launch(const DevCtx& dc, const Fp8Args& a, int split, cudaStream_t s) {
+int cluster_room(const DevCtx& dc, const int** room) {
     using G = Geo<BN>;
-    static int configured[64] = {0};
-    auto kern = swap_kernel<BN, TY>;
-    if (!configured[dc.device]) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
-        if (e != cudaSuccess) return cuda_fail(e);
-        configured[dc.device] = 1;
-    }
+    static std::once_flag once[64];
+    static cudaError_t error[64];
+    static int held[64][4];
+    std::call_once(once[dc.device], [&] {
+        auto kern = swap_kernel<BN, TY>;
+        cudaError_t& e = error[dc.device];
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+        for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(1u << i);
+            cfg.blockDim = dim3(G::kThreads);
+            cfg.dynamicSmemBytes = G::kSmem;
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 1u << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&held[dc.device][i], kern, &cfg);
+        }
+    });
+    *room = held[dc.device];
+    return error[dc.device] == cudaSuccess ? QG_OK : cuda_fail(error[dc.device]);
+}
+
+// The tiles, and the largest split (its logarithm) whose clusters all run at
+// once with two k blocks per CTA at least.
+struct Plan {
+    long long nt, mt, kb;
+    int log_split;
+};
+template <int BN, class TY>
+int plan(const DevCtx& dc, const Fp8Args& a, Plan* p) {
+    const int* room = nullptr;
+    const int rc = cluster_room<BN, TY>(dc, &room);
+    if (rc) return rc;
+    *p = Plan{(a.N + 127) / 128, (a.M + BN - 1) / BN, (a.K + 127) / 128, 0};
+    while (p->log_split < 3 && p->nt * p->mt <= room[p->log_split + 1] && p->kb >= (4 << p->log_split)) ++p->log_split;
+    return QG_OK;
+}
+
+template <int BN, class TY>
+int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
+    using G = Geo<BN>;
+    Plan pl;
+    int rc = plan<BN, TY>(dc, a, &pl);
     CUtensorMap mw, ma;
-    int rc = code_map(&mw, a.w, a.N, a.K, 128);
+    if (rc == QG_OK) rc = code_map(&mw, a.w, a.N, a.K, 128);
     if (rc == QG_OK) rc = code_map(&ma, a.a, a.M, a.K, BN);
     if (rc) return rc;
-    const Params p{a.sa, a.sw, a.y, (int)a.M, (int)a.N, (int)((a.K + 127) / 128), false, dc.err};
+    if (pl.nt > 65535 || pl.mt > 65535) return QG_ERR_UNSUPPORTED;
+    const Params p{a.sa, a.sw, a.y, (int)a.M, (int)a.N, (int)pl.kb, false, dc.err};
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)split, (unsigned)((a.N + 127) / 128), (unsigned)((a.M + BN - 1) / BN));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(1u << pl.log_split, (unsigned)pl.nt, (unsigned)pl.mt);
+    cfg.blockDim = dim3(G::kThreads);
     cfg.dynamicSmemBytes = G::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.x = 1u << pl.log_split;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, ma, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, swap_kernel<BN, TY>, mw, ma, p);
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }
 
-template <int BN>
-int launch_bn(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
-    // About one CTA per SM, at least two k blocks each.
-    const long long tiles = ((a.N + 127) / 128) * ((a.M + BN - 1) / BN), kb = (a.K + 127) / 128;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= dc.num_sms && kb >= split * 4) split *= 2;
-    return a.y_dtype == QG_F32 ? launch<BN, float>(dc, a, split, s) : launch<BN, __nv_bfloat16>(dc, a, split, s);
+template <class TY>
+int launch_type(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
+    if (a.M <= 16) return launch<16, TY>(dc, a, s);
+    if (a.M <= 32) return launch<32, TY>(dc, a, s);
+    if (a.M <= 64) return launch<64, TY>(dc, a, s);
+    return launch<128, TY>(dc, a, s);
 }
 
 }  // namespace
 
 int launch_swap(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
-    if (a.M <= 16) return launch_bn<16>(dc, a, s);
-    if (a.M <= 32) return launch_bn<32>(dc, a, s);
-    if (a.M <= 64) return launch_bn<64>(dc, a, s);
-    return launch_bn<128>(dc, a, s);
+    return a.y_dtype == QG_F32 ? launch_type<float>(dc, a, s) : launch_type<__nv_bfloat16>(dc, a, s);
+}
+
+// Both kernels take about 0.5 us per k block and CTA, so the one with fewer k
+// blocks one after the other is taken. M = 256, N = K = 4096: 11.7 us with the
+// split, 18.1 in 256-wide tiles; M = 256, N = 12288, K = 4096: 32.9 and 19.3.
+bool swap_is_shorter(const DevCtx& dc, const Fp8Args& a) {
+    if (a.M <= 64) return true;
+    Plan p;
+    if (plan<128, float>(dc, a, &p) != QG_OK) return false;
+    const long long ctas = (p.nt * p.mt) << p.log_split, split = 1ll << p.log_split;
+    const long long swap = (ctas + dc.num_sms - 1) / dc.num_sms * ((p.kb + split - 1) / split);
+    const long long tiles = ((a.M + 127) / 128) * ((a.N + 255) / 256);
+    return swap <= (tiles + dc.num_sms - 1) / dc.num_sms * p.kb;
 }
 
 int code_map(CUtensorMap* m, const uint8_t* ptr, long long rows, long long cols, int box_rows) {

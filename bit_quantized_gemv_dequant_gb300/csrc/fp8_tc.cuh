@@ -80,6 +80,7 @@ struct Params {
 };
 
 int launch_swap(const DevCtx& dc, const Fp8Args& a, cudaStream_t s);
+bool swap_is_shorter(const DevCtx& dc, const Fp8Args& a);
 int launch_tile(const DevCtx& dc, const Fp8Args& a, cudaStream_t s);
 
 // A 2-D map of rows x cols e4m3 codes, boxes of box_rows x 128, 128-byte swizzle.

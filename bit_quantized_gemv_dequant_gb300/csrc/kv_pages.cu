@@ -6,7 +6,7 @@
 
 #include <algorithm>
 
-#include "serve_common.cuh"
+#include "fp8_tc.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -90,6 +90,8 @@ struct Remap {
 
 __global__ void __launch_bounds__(kCopyThreads)
     copy_kernel(const PagePlanes p, const CopyList l, const Remap r, unsigned* err) {
+    fp8::pdl_trigger();
+    fp8::pdl_wait();
     for (long long i = (long long)blockIdx.x * kCopyThreads + threadIdx.x; r.table && i < r.n;
          i += (long long)gridDim.x * kCopyThreads) {
         const int32_t page = r.table[i];
@@ -123,9 +125,18 @@ __global__ void __launch_bounds__(kCopyThreads)
 int copy_launch(const DevCtx& dc, const PagePlanes& p, const CopyList& l, const Remap& r,
                 long long most, cudaStream_t s) {
     const long long work = std::max(most * p.planes, (r.n + kCopyThreads - 1) / kCopyThreads);
-    const long long grid = std::min<long long>(work, (long long)dc.num_sms * 8);
-    copy_kernel<<<(unsigned)std::max(1LL, grid), kCopyThreads, 0, s>>>(p, l, r, dc.err);
-    return launched();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)std::max(1LL, std::min<long long>(work, (long long)dc.num_sms * 8)));
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = s;
+    // starts while the kernel with the tables ends, and waits for it
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, copy_kernel, p, l, r, dc.err);
+    return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }
 
 // --------------------------------------------------------- tables and counts
@@ -180,6 +191,7 @@ __device__ __forceinline__ void cluster_scan(int mine, int* before, int* total) 
 // kv_fork's tables. Every block ranks its share of the free pages and, after
 // the barrier, writes the rows of its share of the children.
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a, unsigned* err) {
+    fp8::pdl_trigger();
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), np = (int)a.p.num_pages;
     int32_t* ws_src = a.ws;
@@ -293,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const FreeArgs a, unsign
 // sources; source number i counted from the last one has n - 1 - live(p) = i,
 // which needs no second count. There are as many of the one as of the other.
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
+    fp8::pdl_trigger();
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), np = (int)a.p.num_pages;
     int32_t* ws_src = a.ws + 4;
