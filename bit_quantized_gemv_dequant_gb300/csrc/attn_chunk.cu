@@ -137,14 +137,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *slot;
     pdl_trigger();
     pdl_wait();
-    long long total;
-    long long* scratch = reinterpret_cast<long long*>(smem + G::kScratchOff);
-    locate<kRT, kKT, kThreads>(w, -1, &total, scratch);
-    const Cuts cuts(total, w.ctas);
+    Cuts cuts;
+    Place place;
     if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1;
-    if ((int)blockIdx.x < cuts.n) {
-        const long long begin = cuts(blockIdx.x), n = cuts(blockIdx.x + 1) - begin;
-        const Place place = locate<kRT, kKT, kThreads>(w, begin, &total, scratch);
+    if (locate<kRT, kKT, kThreads>(w, blockIdx.x, &cuts, &place, reinterpret_cast<long long*>(smem + G::kScratchOff))) {
+        const long long n = cuts(blockIdx.x + 1) - cuts(blockIdx.x);
         Walk<kRT, kKT> walk(w, place, n);
         bool ok = true;
         if (warp == 8) {

@@ -89,15 +89,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     pdl_trigger();
     pdl_wait();
-    long long total;
-    long long* scratch = reinterpret_cast<long long*>(smem + G::kScratchOff);
-    // The first locate only sums up; the second finds this CTA's first step.
-    locate<RT, kKT, kThreads>(w, -1, &total, scratch);
-    const Cuts cuts(total, w.ctas);
+    Cuts cuts;
+    Place place;
     if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1;
-    if ((int)blockIdx.x >= cuts.n) return;
-    const long long begin = cuts(blockIdx.x), n = cuts(blockIdx.x + 1) - begin;
-    const Place place = locate<RT, kKT, kThreads>(w, begin, &total, scratch);
+    if (!locate<RT, kKT, kThreads>(w, blockIdx.x, &cuts, &place, reinterpret_cast<long long*>(smem + G::kScratchOff)))
+        return;
+    const long long n = cuts(blockIdx.x + 1) - cuts(blockIdx.x);
     Walk<RT, kKT> walk(w, place, n);
 
     if (warp == kWarps) {

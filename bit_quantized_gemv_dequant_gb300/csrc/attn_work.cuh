@@ -99,21 +99,39 @@ struct Place {
     int at;
 };
 
-// Places of step `t` (t < W gives a sequence), found by the whole block of NT
-// threads: a scan over the sequences, then the head and the tile in it.
-// scratch: NT / 32 + 4 long longs of shared memory.
+// The first step of CTA c: total c / n.
+struct Cuts {
+    long long each;  // total / n
+    int rest, n;
+    __device__ Cuts() {}
+    __device__ Cuts(long long total, int ctas) {
+        n = (int)min((long long)ctas, total);
+        each = n == 0 ? 0 : total < 0x7FFFFFFF ? (int)total / n : total / n;
+        rest = (int)(total - each * n);
+    }
+    __device__ __forceinline__ long long operator()(int c) const { return each * c + rest * c / n; }
+    // The CTA whose steps hold step t.
+    __device__ __forceinline__ int holder(long long t) const {
+        int c = (int)min((long long)n - 1, t / each);  // at most a little too far
+        while ((*this)(c) > t) --c;
+        return c;
+    }
+};
+
+// The cuts, and the place of CTA `cta`'s first step, found by the whole block of
+// NT threads: a scan over the sequences, whose counts stay in registers if there
+// are no more than threads, then the head and the tile in the sequence. False
+// if the CTA has no steps. scratch: NT / 32 + 2 long longs of shared memory.
 template <int RT, int KT, int NT>
-__device__ Place locate(const Work& w, long long t, long long* total, long long* scratch) {
+__device__ bool locate(const Work& w, int cta, Cuts* cuts, Place* at, long long* scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long before = 0;
-    Place at{w.a.batch, 0, 0, 0};
     long long* found = scratch + NT / 32;
-    if (threadIdx.x == 0) found[0] = -1;
-    for (int b0 = 0; b0 < w.a.batch; b0 += NT) {
+    // Steps of sequence b0 + thread, those of the block's sequences before it,
+    // and of all of them.
+    auto scan = [&](int b0, long long* v, long long* begin) {
         const int b = b0 + threadIdx.x;
-        long long v = 0;
-        if (b < w.a.batch) v = steps_of<RT, KT>(w, seq_at(w, b)) * w.a.hkv;
-        long long x = v;
+        *v = b < w.a.batch ? steps_of<RT, KT>(w, seq_at(w, b)) * w.a.hkv : 0;
+        long long x = *v;
 #pragma unroll
         for (int i = 1; i < 32; i *= 2) {
             const long long o = __shfl_up_sync(0xFFFFFFFFu, x, i);
@@ -122,54 +140,47 @@ __device__ Place locate(const Work& w, long long t, long long* total, long long*
         __syncthreads();
         if (lane == 31) scratch[warp] = x;
         __syncthreads();
-        long long base = before, all = 0;
+        long long base = 0, all = 0;
+#pragma unroll
         for (int i = 0; i < NT / 32; ++i) {
             if (i < warp) base += scratch[i];
             all += scratch[i];
         }
-        const long long begin = base + x - v;
-        if (t >= begin && t < begin + v) {
-            found[0] = b;
-            found[1] = t - begin;
+        *begin = base + x - *v;
+        return all;
+    };
+    long long v = 0, begin = 0, total = 0;
+    for (int b0 = 0; b0 < w.a.batch; b0 += NT) total += scan(b0, &v, &begin);
+    *cuts = Cuts(total, w.ctas);
+    if (cta >= cuts->n) return false;
+    const long long t = (*cuts)(cta);
+    long long before = 0;
+    for (int b0 = 0; b0 < w.a.batch; b0 += NT) {
+        const long long all = w.a.batch > NT ? scan(b0, &v, &begin) : total;
+        if (t >= before + begin && t < before + begin + v) {
+            found[0] = b0 + threadIdx.x;
+            found[1] = t - before - begin;
         }
         before += all;
     }
     __syncthreads();
-    *total = before;
-    const long long b = found[0], rest = found[1];
-    __syncthreads();
-    if (b < 0) return at;
-    const Seq s = seq_at(w, (int)b);
+    at->b = (int)found[0];
+    long long left = found[1];
+    const Seq s = seq_at(w, at->b);
     const long long per = steps_of<RT, KT>(w, s);
-    at.b = (int)b;
-    at.head = (int)(rest / per);
-    long long left = rest % per;
-    for (;; ++at.tile) {
-        const Span p = span_of<RT, KT>(w, s, at.tile);
+    at->head = 0;
+    while (left >= per) {  // few heads; a division of 64 bits takes longer
+        left -= per;
+        ++at->head;
+    }
+    for (at->tile = 0;; ++at->tile) {
+        const Span p = span_of<RT, KT>(w, s, at->tile);
         if (left < p.hi - p.lo) break;
         left -= p.hi - p.lo;
     }
-    at.at = (int)left;
-    return at;
+    at->at = (int)left;
+    return true;
 }
-
-// The first step of CTA c: total c / n.
-struct Cuts {
-    long long each;  // total / n
-    int rest, n;
-    __device__ Cuts(long long total, int ctas) {
-        n = (int)min((long long)ctas, total);
-        each = n ? total / n : 0;
-        rest = n ? (int)(total - each * n) : 0;
-    }
-    __device__ __forceinline__ long long operator()(int c) const { return each * c + (long long)rest * c / n; }
-    // The CTA whose steps hold step t.
-    __device__ __forceinline__ int holder(long long t) const {
-        int c = (int)min((long long)n - 1, t / each);  // at most a little too far
-        while ((*this)(c) > t) --c;
-        return c;
-    }
-};
 
 // Walks the segments of a CTA's steps: for each, a row tile and the key tiles
 // lo .. hi - 1 of it that are this CTA's.
