@@ -373,7 +373,7 @@ int token_logprobs(const void* logits, int dtype, int64_t row_stride, const int6
                    int64_t M, int64_t V, int top_k, float* logprobs, float* entropy, int32_t* ranks,
                    float* top_values, int32_t* top_ids, qg_stream_t stream) {
     if (M < 0 || V <= 0 || top_k < 0 || top_k > V || !is_type(dtype)) return QG_ERR_INVALID_ARG;
-    if (M > kMaxInt || V > kMaxInt / 2 || top_k > 32) return QG_ERR_UNSUPPORTED;
+    if (M > kMaxInt || V > kMaxInt / 2 + 1 || top_k > 32) return QG_ERR_UNSUPPORTED;
     if (M > 0 && (!logits || !targets || !logprobs || !entropy || !ranks)) return QG_ERR_INVALID_ARG;
     if (M > 0 && top_k > 0 && (!top_values || !top_ids)) return QG_ERR_INVALID_ARG;
     int64_t xb = 0;
