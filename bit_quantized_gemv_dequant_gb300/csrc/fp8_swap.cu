@@ -359,7 +359,7 @@ bool swap_is_shorter(const DevCtx& dc, const Fp8Args& a) {
     if (plan<128, float>(dc, a, &p) != QG_OK) return false;
     const long long ctas = (p.nt * p.mt) << p.log_split, split = 1ll << p.log_split;
     const long long swap = (ctas + dc.num_sms - 1) / dc.num_sms * ((p.kb + split - 1) / split);
-    const long long tiles = ((a.M + 127) / 128) * ((a.N + 255) / 256);
+    const long long tiles = 2 * ((a.M + 255) / 256) * ((a.N + 255) / 256);  // per SM
     return swap <= (tiles + dc.num_sms - 1) / dc.num_sms * p.kb;
 }
 

@@ -1,5 +1,5 @@
-// qmm_fp8_b128 for many rows of a: persistent CTAs over tiles of 128 rows of a
-// times 256 rows of w.
+// qmm_fp8_b128 for many rows of a: persistent pairs of CTAs over tiles of 256
+// rows of a times 256 rows of w.
 #include <algorithm>
 
 #include "fp8_tc.cuh"
@@ -8,11 +8,17 @@ namespace qg {
 namespace fp8 {
 namespace {
 
-// Bound by the tensor cores: 128 x 256 x 128 products of a k block take them
-// 512 cycles, while the two epilogue warpgroups bring its accumulator, which
-// has two places in tensor memory, into registers: thread = row of a and 128
-// columns, which lie in one block of w's scales, so a k block enters the sum
-// as fma(d, a_scale * w_scale, acc) with one factor per thread.
+// A tile's two SMs issue their MMAs as one (cta_group::2): each holds 128 rows of
+// a, the sums of those rows, and half of the rows of w, which the other one
+// reads from it. A k block is then 32 KB of shared memory written and read per
+// SM; one SM alone would need 48 KB for the same products, and the 96 KB that
+// pass through its shared memory took 850 of 1040 cycles per k block.
+//
+// The tensor cores take 512 cycles for a k block's 128 x 256 x 128 products, in
+// which the two epilogue warpgroups bring the accumulator of the one before,
+// which has two places in tensor memory, into registers: thread = row of a and
+// 128 columns, which lie in one block of w's scales, so a k block enters the
+// sum as fma(d, a_scale * w_scale, acc) with one factor per thread.
 //
 // The scales of 32 k blocks at a time come into shared memory by 4-byte
 // asynchronous copies, the next 32 while these are used (read from global
@@ -22,12 +28,13 @@ namespace {
 // rows by each warp cost 33 us there).
 //
 //   warps 0-7  epilogue
-//   warp 8     TMA producer (48 KB per k block, three stages)
-//   warp 9     MMA issuer
+//   warp 8     TMA producer (32 KB per k block, five stages), whose copies
+//              complete on the first CTA's barrier
+//   warp 9     of the first CTA: MMA issuer for both
 constexpr int kThreads = 320;
 constexpr int kBM = 128, kBN = 256;
-constexpr int kStages = 3;
-constexpr int kStage = (kBM + kBN) * 128;
+constexpr int kStages = 5;
+constexpr int kStage = (kBM + kBN / 2) * 128;                   // per CTA
 constexpr int kScaleBlocks = 32;
 constexpr int kScaleRow = kBM + 4;                              // floats per k block: a's 128 rows, w's 2 blocks
 constexpr int kScaleSet = kScaleBlocks * kScaleRow * 4;
@@ -35,10 +42,49 @@ constexpr int kOutOff = kStages * kStage;                       // 4 KB per epil
 constexpr int kScaleOff = kOutOff + 8 * 4096;                   // two sets
 constexpr int kBarOff = kScaleOff + 2 * kScaleSet;
 constexpr int kSmem = 1024 + kBarOff + 256;
-constexpr uint32_t kDesc = f8_idesc(kBM, kBN);
+constexpr uint32_t kDesc = f8_idesc(2 * kBM, kBN);
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// The address of shared memory `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+// A load into this CTA's shared memory that completes on a barrier of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kDesc), "r"(acc)
+        : "memory");
+}
+// Arrives on the barrier at this place in both CTAs when the MMAs so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// Arrives on a barrier of the pair. What the arrival orders is reads of tensor
+// memory, complete and behind a tcgen05 fence: no release over the cluster is
+// needed (one costs 1000 cycles here).
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int c0, int c1, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
@@ -63,8 +109,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t done = bars + 8u * (2 * kStages + 4);
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 8 * (2 * kStages + 5));
     const int warp = warp_number(), lane = threadIdx.x & 31;
-    const int mt = (p.M + kBM - 1) / kBM, nt = (p.N + kBN - 1) / kBN;
+    const int mt = (p.M + 2 * kBM - 1) / (2 * kBM), nt = (p.N + kBN - 1) / kBN;
     const long long tiles = (long long)mt * nt;
+    const int rank = (int)(blockIdx.x & 1);
+    const long long first = blockIdx.x >> 1, step = gridDim.x >> 1;  // this pair's tiles
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -73,16 +121,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(t_full(i), 1);
-            mbar_init(t_empty(i), 8);
+            mbar_init(t_empty(i), 16);  // of the first CTA: both CTAs' epilogue warps
         }
         mbar_init(done, 1);
         fence_mbar_init();
         prefetch_tmap(&map_a);
         prefetch_tmap(&map_w);
     }
-    if (warp == 9) tmem_alloc(smem_addr(slot), 512);
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // the other CTA's barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *slot;
     pdl_trigger();
@@ -92,8 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 8 && lane == 0) {
             int i = 0;
             bool ok = true;
-            for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const int m0 = (int)(t % mt) * kBM, n0 = (int)(t / mt) * kBN;
+            for (long long t = first; t < tiles && ok; t += step) {
+                const int m0 = ((int)(t % mt) * 2 + rank) * kBM, n0 = (int)(t / mt) * kBN + rank * (kBN / 2);
                 for (int b = 0; b < p.KB; ++b, ++i) {
                     const int st = i % kStages;
                     if (i >= kStages && !bar_wait(empty(st), ((i / kStages) & 1) ^ 1)) {
@@ -101,21 +154,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t sb = base + st * kStage;
-                    mbar_arrive_expect_tx(full(st), kStage);
-                    tma_load_2d(sb, &map_a, b * 128, m0, full(st));
-                    tma_load_2d(sb + kBM * 128, &map_w, b * 128, n0, full(st));
+                    const uint32_t sb = base + st * kStage, bar = in_cta(full(st), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * kStage);  // both CTAs' bytes
+                    tma_load_pair(sb, &map_a, b * 128, m0, bar);
+                    tma_load_pair(sb + kBM * 128, &map_w, b * 128, n0, bar);
                 }
             }
-            for (int j = max(0, i - kStages); j < i; ++j)
+            // Both CTAs' copies are done when the first one's barrier says so; the
+            // other CTA waits for that at the end, behind the cluster's barrier.
+            for (int j = max(0, i - kStages); rank == 0 && j < i; ++j)
                 if (!bar_wait(full(j % kStages), (j / kStages) & 1)) report_error(p.err, DEVERR_WAIT_DRAIN);
-        } else if (warp == 9) {
+        } else if (warp == 9 && rank == 0) {
             const uint64_t da = sw128_desc(base), dw = sw128_desc(base + kBM * 128);
             const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             int st = 0, tb = 0;
             uint32_t ph = 0, tph = 0;
             bool ok = true;
-            for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (long long t = first; t < tiles && ok; t += step) {
                 for (int b = 0; b < p.KB; ++b) {
                     if (!warp_bar_wait(full(st), ph) || !warp_bar_wait(t_empty(tb), tph ^ 1)) {
                         if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
@@ -126,9 +181,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t a = da + (uint64_t)(st * (kStage >> 4)), w = dw + (uint64_t)(st * (kStage >> 4));
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_f8(tm + tb * kBN, a + 2 * k, w + 2 * k, kDesc, k > 0);
-                        tc_commit(empty(st));
-                        tc_commit(t_full(tb));
+                        for (int k = 0; k < 4; ++k) mma_pair(tm + tb * kBN, a + 2 * k, w + 2 * k, k > 0);
+                        commit_pair(empty(st));
+                        commit_pair(t_full(tb));
                     }
                     __syncwarp();
                     if (++st == kStages) {
@@ -139,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tph ^= tb == 0;
                 }
             }
-            if (elect_one()) tc_commit(done);
+            if (elect_one()) commit_pair(done);
             __syncwarp();
             if (!warp_bar_wait(done, 0) && lane == 0) report_error(p.err, DEVERR_WAIT_DRAIN);
         }
@@ -152,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // set: warp = 16 rows of a, lane = k block (a row's are consecutive).
         auto fetch = [&](long long t, int b0, int set) {
             if (t < tiles) {
-                const int m0 = (int)(t % mt) * kBM, n0 = (int)(t / mt) * kBN;
+                const int m0 = ((int)(t % mt) * 2 + rank) * kBM, n0 = (int)(t / mt) * kBN;
                 const uint32_t dst = base + kScaleOff + set * kScaleSet + lane * (kScaleRow * 4);
                 if (b0 + lane < p.KB) {
 #pragma unroll
@@ -169,10 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int i = 0, set = 0;
         bool ok = true;
-        fetch(blockIdx.x, 0, 0);
-        for (long long t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const uint32_t empty0 = in_cta(t_empty(0), 0);
+        fetch(first, 0, 0);
+        for (long long t = first; t < tiles; t += step) {
             const int row = (warp & 3) * 32 + lane;
-            const int m0 = (int)(t % mt) * kBM + (warp & 3) * 32, m = m0 + lane;
+            const int m0 = ((int)(t % mt) * 2 + rank) * kBM + (warp & 3) * 32, m = m0 + lane;
             const long long n0 = (t / mt) * kBN + half * 128;
             float2 acc[64];
 #pragma unroll
@@ -183,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     named_bar_sync(1, 256);
                     const bool more = b + kScaleBlocks < p.KB;
-                    fetch(more ? t : t + gridDim.x, more ? b + kScaleBlocks : 0, set ^ 1);
+                    fetch(more ? t : t + step, more ? b + kScaleBlocks : 0, set ^ 1);
                     set ^= 1;
                 }
                 const int tb = i & 1;
@@ -205,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(t_empty(tb));
+                        if (lane == 0) arrive_cluster(empty0 + 8u * tb);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -254,9 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // neither CTA's memory is in use any more
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
@@ -287,23 +344,26 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     }
     CUtensorMap ma, mw, my = {};
     int rc = code_map(&ma, a.a, a.M, a.K, kBM);
-    if (rc == QG_OK) rc = code_map(&mw, a.w, a.N, a.K, kBN);
+    if (rc == QG_OK) rc = code_map(&mw, a.w, a.N, a.K, kBN / 2);
     // TMA stores want rows of y on 16-byte boundaries
     const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.N * sizeof(TY) % 16 == 0;
     if (rc == QG_OK && vec) rc = out_map<TY>(&my, a);
     if (rc) return rc;
     const Params p{a.sa, a.sw, a.y, (int)a.M, (int)a.N, (int)((a.K + 127) / 128), vec, dc.err};
-    const long long tiles = ((a.M + kBM - 1) / kBM) * ((a.N + kBN - 1) / kBN);
+    const long long tiles = ((a.M + 2 * kBM - 1) / (2 * kBM)) * ((a.N + kBN - 1) / kBN);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, dc.num_sms));
+    cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(tiles, dc.num_sms / 2));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ma, mw, my, p);
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }
