@@ -27,11 +27,13 @@ namespace {
 // TMA stores, which go on while the next tile is summed (32-byte stores of 32
 // rows by each warp cost 33 us there).
 //
-//   warps 0-7  epilogue
+//   warps 0-7  epilogue; 216 registers each (128 sums and two loads of 32
+//              columns under way), which warps 8-11 give up
 //   warp 8     TMA producer (32 KB per k block, five stages), whose copies
 //              complete on the first CTA's barrier
 //   warp 9     of the first CTA: MMA issuer for both
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+constexpr int kRegisters = 256 * 216 + 128 * 72;                 // what setmaxnreg hands out
 constexpr int kBM = 128, kBN = 256;
 constexpr int kStages = 5;
 constexpr int kStage = (kBM + kBN / 2) * 128;                   // per CTA
@@ -142,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
 
     if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8 && lane == 0) {
             int i = 0;
             bool ok = true;
@@ -199,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_bar_wait(done, 0) && lane == 0) report_error(p.err, DEVERR_WAIT_DRAIN);
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int half = warp / 4;
         const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
         const uint32_t out = base + kOutOff + warp * 4096;
@@ -222,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        int i = 0, set = 0;
+        int set = 0, tb = 0;
+        uint32_t tph = 0;
         bool ok = true;
         const uint32_t empty0 = in_cta(t_empty(0), 0);
         fetch(first, 0, 0);
@@ -233,41 +238,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-            for (int b = 0; b < p.KB; ++b, ++i) {
-                if (b % kScaleBlocks == 0) {
-                    // The other set's last readers are past this barrier, this set's copies done.
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    named_bar_sync(1, 256);
-                    const bool more = b + kScaleBlocks < p.KB;
-                    fetch(more ? t : t + step, more ? b + kScaleBlocks : 0, set ^ 1);
-                    set ^= 1;
-                }
-                const int tb = i & 1;
-                const float* sp = scales + (set ^ 1) * (kScaleSet / 4) + b % kScaleBlocks * kScaleRow;
-                const float sc = sp[row] * sp[kBM + half];
-                const float2 s = make_float2(sc, sc);
-                if (ok && !warp_bar_wait(t_full(tb), (i / 2) & 1)) {
-                    if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
-                    ok = false;  // the sums are lost; the barriers are still met
-                }
-                tc_fence_after();
-                uint32_t r[2][16];
-                tmem_ld16_async(at + tb * kBN, r[0]);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_wait16(r[c & 1]);
-                    if (c < 7) {
-                        tmem_ld16_async(at + tb * kBN + (c + 1) * 16, r[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_cluster(empty0 + 8u * tb);
+            for (int b0 = 0; b0 < p.KB; b0 += kScaleBlocks) {
+                // The other set's last readers are past this barrier, this set's copies done.
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                named_bar_sync(1, 256);
+                const int nb = min(kScaleBlocks, p.KB - b0);
+                const bool more = b0 + nb < p.KB;
+                fetch(more ? t : t + step, more ? b0 + nb : 0, set ^ 1);
+                const float* sp = scales + set * (kScaleSet / 4);
+                set ^= 1;
+                float sc = sp[row] * sp[kBM + half];
+#pragma unroll 1
+                for (int b = 0; b < nb; ++b) {
+                    const float2 s = make_float2(sc, sc);
+                    sp += b + 1 < nb ? kScaleRow : 0;
+                    if (!mbar_try_wait(t_full(tb), tph) && ok && !bar_wait(t_full(tb), tph)) {
+                        report_error(p.err, DEVERR_TC_WAIT);
+                        ok = false;  // the sums are lost; the barriers are still met
                     }
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint32_t from = at + tb * kBN;
+                    uint32_t r[2][32];
+                    tmem_ld32_async(from, r[0]);
+                    sc = sp[row] * sp[kBM + half];  // of the next block
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        acc[c * 8 + j] = fma2(make_float2(__uint_as_float(r[c & 1][2 * j]),
-                                                          __uint_as_float(r[c & 1][2 * j + 1])),
-                                              s, acc[c * 8 + j]);
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait32(r[c & 1]);
+                        if (c < 3) {
+                            tmem_ld32_async(from + (c + 1) * 32, r[(c + 1) & 1]);
+                        } else {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_cluster(empty0 + 8u * tb);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            acc[c * 16 + j] = fma2(make_float2(__uint_as_float(r[c & 1][2 * j]),
+                                                              __uint_as_float(r[c & 1][2 * j + 1])),
+                                                  s, acc[c * 16 + j]);
+                    }
+                    tb ^= 1;
+                    tph ^= tb == 0;
                 }
             }
             if (p.vec) {
@@ -338,7 +350,13 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     static int configured[64] = {0};
     auto kern = tile_kernel<TY>;
     if (!configured[dc.device]) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        // Were the kernel launched with fewer registers than it hands out, the
+        // increase would wait for ever.
+        cudaFuncAttributes at{};
+        cudaError_t e = cudaFuncGetAttributes(&at, kern);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (at.numRegs * kThreads < kRegisters) return QG_ERR_UNSUPPORTED;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dc.device] = 1;
     }

@@ -109,6 +109,24 @@ def test_quantize_every_tie_and_range():
     assert np.array_equal(codes.view(torch.uint8).cpu().numpy(), quantize_ref(x)[0])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_of_any_magnitude(dtype):
+    """Blocks from the smallest subnormal to the largest value, and scales whose significand is all ones or nearly:
+    the quotient is the correctly rounded one, so the codes are those of a division."""
+    g = torch.Generator().manual_seed(3)
+    e = torch.randint(-149, 128, (3000,), generator=g).double()
+    amax = torch.exp2(e) * (1 + torch.rand(3000, generator=g).double() * 0.999)
+    amax[::3] = 448.0 * torch.exp2(e[::3].clamp(-140, 110)) * (2 - torch.randint(1, 5, (1000,), generator=g) * 2.0**-23)
+    x = (torch.rand(3000, 128, generator=g).double() * 2 - 1) * amax[:, None]
+    x[:, 5] = amax
+    x[:, 64:] *= torch.exp2(-torch.rand(3000, 64, generator=g).double() * 12)
+    x = x.clamp(-3.0e38, 3.0e38).to(torch.float32).cuda().to(DTYPES[dtype])
+    codes, scales = qg.quantize_fp8_b128(x)
+    rc, rs = quantize_ref(x)
+    assert np.array_equal(scales.cpu().numpy(), rs)
+    assert np.array_equal(codes.view(torch.uint8).cpu().numpy(), rc)
+
+
 def test_quantize_strided_odd_and_nonfinite():
     base = torch.randn(6, 700, generator=rng(5), device="cuda")
     x = base[:, 3:3 + 261]
