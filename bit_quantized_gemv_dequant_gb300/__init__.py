@@ -46,7 +46,7 @@ EXPORTS = ("qgemv_q4_0", "qgemv_dual_q4_0", "qgemv_q4_k", "qmm_affine", "qkv_spl
            "qg_status_string", "qg_last_cuda_error", "qg_device_error",
            "qg_selftest_wait_timeout", "qg_set_option", "qg_get_option",
            "qgemv_q4_k_noalloc", "qg_prepare_af4_g64", "qmm_af4_g64", "qgemv_dual_q4_0_host",
-           "quantize_fp8_b128", "qmm_fp8_b128", "attn_paged", "attn_paged_workspace_size",
+           "quantize_fp8_b128", "qmm_fp8_b128", "qmm_fp8_b128_workspace_size", "attn_paged", "attn_paged_workspace_size",
            "kv_append", "kv_copy_pages", "kv_fork", "kv_fork_workspace_size", "kv_free",
            "kv_compact", "kv_compact_workspace_size", "token_logprobs")
 
@@ -96,7 +96,8 @@ def lib():
             "qg_prepare_af4_g64": [P, P, P, P, P, I64, I64, P],
             "qmm_af4_g64": [P, P, P, P, I64, I64, I64, P, SZ, P],
             "quantize_fp8_b128": [P, I, I64, P, P, I64, I64, P],
-            "qmm_fp8_b128": [P, P, P, P, P, I, I64, I64, I64, P],
+            "qmm_fp8_b128": [P, P, P, P, P, I, I64, I64, I64, P, SZ, P],
+            "qmm_fp8_b128_workspace_size": [I64, I64, I64, C.POINTER(SZ)],
             "attn_paged": [P, I64] + [P] * 7 + [I] + [I64] * 9 + [C.c_float] * 2 + [I64, P, SZ, P],
             "attn_paged_workspace_size": [I64] * 6 + [C.POINTER(SZ)],
             "kv_append": [P, P, I64, I64, I, P, P, I, P] + [I64] * 5 + [P],
@@ -425,7 +426,8 @@ def quantize_fp8_b128(x, codes=None, scales=None, *, stream=None):
     return codes, scales
 
 
-def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, stream=None):
+def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, workspace=None,
+                 stream=None):
     """y[M, N] = (a * a_scales) . (w * w_scales)^T: e4m3 codes a [M, K] with a
     scale per row and 128 values of K, w [N, K] with one per 128 x 128 values;
     y is float32 or bfloat16."""
@@ -442,8 +444,11 @@ def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, s
     else:
         _same(y, "y", M, N)
         y_at = _dev(y, "y")
-    rc = lib().qmm_fp8_b128(at, scales_at, _dev(w, "w", _E4M3), _dev(w_scales, "w_scales", torch.float32),
-                            y_at, _dtype(y, "y"), M, N, K, _stream(stream))
+    w_at, st = _dev(w, "w", _E4M3), _stream(stream)
+    need = _size("qmm_fp8_b128_workspace_size", M, N, K) if (K | at | w_at) & 15 else 0
+    ws, wsb = _scratch(need, a.device, workspace, st)
+    rc = lib().qmm_fp8_b128(at, scales_at, w_at, _dev(w_scales, "w_scales", torch.float32), y_at,
+                            _dtype(y, "y"), M, N, K, ws, wsb, st)
     if rc:
         raise QGError("qmm_fp8_b128", rc)
     return y

@@ -71,6 +71,52 @@ __global__ void __launch_bounds__(kGThreads)
         }
 }
 
+// dst[r][c] = src[r][c] for c < K, 0 up to the pitch (a multiple of 16); src's
+// rows start at any byte. 16 bytes per thread, from the five aligned words that
+// hold them; where those are not all inside src, byte by byte.
+constexpr int kPadThreads = 256;
+__global__ void __launch_bounds__(kPadThreads)
+    pad_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, long long rows, int K, int pitch) {
+    const int per = pitch / 16;
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(src), end = begin + rows * K;
+    for (long long i = (long long)blockIdx.x * kPadThreads + threadIdx.x; i < rows * per;
+         i += (long long)gridDim.x * kPadThreads) {
+        const long long r = i < 0x7FFFFFFF ? (int)i / per : i / per;
+        const int c = (int)(i - r * per) * 16, n = min(16, K - c);
+        const uintptr_t at = begin + r * K + c, word = at & ~(uintptr_t)3;
+        const int shift = (int)(at - word) * 8;
+        uint32_t v[5];
+        if (word >= begin && word + 20 <= end) {
+#pragma unroll
+            for (int j = 0; j < 5; ++j) v[j] = __ldg(reinterpret_cast<const uint32_t*>(word) + j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = __funnelshift_r(v[j], v[j + 1], shift);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (4 * j + b < n) v[j] |= (uint32_t)reinterpret_cast<const uint8_t*>(at)[4 * j + b] << (8 * b);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int left = n - 4 * j;  // bytes of this word that belong to the row
+            if (left < 4) v[j] &= left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+        }
+        *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+int pad_launch(const DevCtx& dc, const uint8_t* src, uint8_t* dst, long long rows, long long K, long long pitch,
+               cudaStream_t s) {
+    const long long ctas = (rows * (pitch / 16) + kPadThreads - 1) / kPadThreads;
+    pad_kernel<<<(unsigned)(ctas < dc.num_sms * 16LL ? ctas : dc.num_sms * 16LL), kPadThreads, 0, s>>>(
+        src, dst, rows, (int)K, (int)pitch);
+    return launched();
+}
+
 template <class TY>
 int general_launch(const Fp8Args& a, cudaStream_t s) {
     const long long gx = (a.N + kGTile - 1) / kGTile, gy = (a.M + kGTile - 1) / kGTile;
@@ -83,9 +129,29 @@ int general_launch(const Fp8Args& a, cudaStream_t s) {
 
 }  // namespace
 
-int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
-    const bool tma = a.K % 16 == 0 && reinterpret_cast<uintptr_t>(a.a) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
+int fp8_mm_launch(const DevCtx& dc, const Fp8Args& args, void* ws, size_t ws_bytes, cudaStream_t s) {
+    Fp8Args a = args;
+    const long long pitch = (a.K + 15) / 16 * 16;
+    auto fits = [&](const uint8_t* p) { return a.K == pitch && reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    bool tma = fits(a.a) && fits(a.w);
+    if (!tma && pitch <= 0x7FFFFFFF && ws_bytes >= (size_t)((a.M + a.N) * pitch)) {
+        // Zeros after the end of a row add nothing, and the blocks of 128 are the
+        // same. (M = 37, N = 2200, K = 5201: 13 us, and 553 on the CUDA cores.)
+        uint8_t* p = static_cast<uint8_t*>(ws);
+        int rc = QG_OK;
+        if (!fits(a.w)) {
+            rc = pad_launch(dc, a.w, p, a.N, a.K, pitch, s);
+            a.w = p;
+            p += a.N * pitch;
+        }
+        if (rc == QG_OK && !fits(args.a)) {
+            rc = pad_launch(dc, a.a, p, a.M, a.K, pitch, s);
+            a.a = p;
+        }
+        if (rc) return rc;
+        a.K = pitch;
+        tma = true;
+    }
     if (tma) return fp8::swap_is_shorter(dc, a) ? fp8::launch_swap(dc, a, s) : fp8::launch_tile(dc, a, s);
     return a.y_dtype == QG_F32 ? general_launch<float>(a, s) : general_launch<__nv_bfloat16>(a, s);
 }

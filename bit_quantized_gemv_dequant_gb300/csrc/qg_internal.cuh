@@ -252,7 +252,7 @@ struct Fp8Args {
     int y_dtype;
     long long M, N, K;
 };
-int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s);
+int fp8_mm_launch(const DevCtx& dc, const Fp8Args& a, void* ws, size_t ws_bytes, cudaStream_t s);
 
 // Attention over a paged cache (attn_paged.cu).
 struct AttnArgs {

@@ -117,7 +117,8 @@ int quantize_fp8_b128(const void* x, int x_dtype, int64_t x_stride, uint8_t* cod
 }
 
 int qmm_fp8_b128(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
-                 void* y, int y_dtype, int64_t M, int64_t N, int64_t K, qg_stream_t stream) {
+                 void* y, int y_dtype, int64_t M, int64_t N, int64_t K, void* workspace,
+                 size_t workspace_bytes, qg_stream_t stream) {
     if (!a || !a_scales || !w || !w_scales || !y || M <= 0 || N <= 0 || K <= 0)
         return QG_ERR_INVALID_ARG;
     if (y_dtype != QG_F32 && y_dtype != QG_BF16) return QG_ERR_INVALID_ARG;
@@ -133,7 +134,18 @@ int qmm_fp8_b128(const uint8_t* a, const float* a_scales, const uint8_t* w, cons
     const DevCtx* dc = nullptr;
     int rc = device_ctx(&dc);
     if (rc) return rc;
-    return fp8_mm_launch(*dc, Fp8Args{a, a_scales, w, w_scales, y, y_dtype, M, N, K}, cu(stream));
+    if (workspace && !aligned(workspace, 16)) return QG_ERR_MISALIGNED;
+    return fp8_mm_launch(*dc, Fp8Args{a, a_scales, w, w_scales, y, y_dtype, M, N, K}, workspace,
+                         workspace ? workspace_bytes : 0, cu(stream));
+}
+
+int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    if (!bytes) return QG_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (M <= 0 || N <= 0 || K <= 0) return QG_ERR_INVALID_ARG;
+    if (M > kMaxInt || N > kMaxInt || K > kMaxInt) return QG_ERR_UNSUPPORTED;
+    *bytes = (size_t)(M + N) * (size_t)((K + 15) / 16 * 16);
+    return QG_OK;
 }
 
 int attn_paged(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,

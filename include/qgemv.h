@@ -287,13 +287,16 @@ enum { QG_F32 = 0, QG_F16 = 1, QG_BF16 = 2 };
  * number (its last block may be short) and so are M and N. The products are
  * exact and summed in f32: |y - exact| <= 1e-5 * sum |terms| + one rounding
  * to y's type. Calls with K % 16 == 0 and 16-byte aligned a and w take the
- * tensor cores; others a CUDA-core kernel with the same result up to the
- * order of the sum. */
+ * tensor cores as they are. Others are copied into the workspace first, with
+ * rows of a multiple of 16 bytes, if it has
+ * qmm_fp8_b128_workspace_size() bytes; with a smaller one (or NULL) they take
+ * a CUDA-core kernel with the same result up to the order of the sum. */
 QG_API int quantize_fp8_b128(const void* x, int x_dtype, int64_t x_stride, uint8_t* codes,
                              float* scales, int64_t M, int64_t K, qg_stream_t stream);
 QG_API int qmm_fp8_b128(const uint8_t* a, const float* a_scales, const uint8_t* w,
                         const float* w_scales, void* y, int y_dtype, int64_t M, int64_t N,
-                        int64_t K, qg_stream_t stream);
+                        int64_t K, void* workspace, size_t workspace_bytes, qg_stream_t stream);
+QG_API int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
 
 /* The paged cache of one layer: k_cache and v_cache are [num_pages,
  * kv_heads, page_size, head_dim] of one 16-bit type, 16-byte aligned.

@@ -161,6 +161,20 @@ def test_product(M, N, K, out):
     assert qg.device_error() == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (3, 130, 257), (40, 200, 515), (130, 300, 1000), (5, 70, 333)])
+def test_product_of_odd_rows_with_and_without_workspace(M, N, K):
+    """Rows of any number of bytes, through the workspace on the tensor cores and, without one, on the CUDA cores."""
+    g = rng(M * N + K)
+    a, w = codes_like(g, M, K), codes_like(g, N, K)
+    sa, sw = scales_like(g, M, -(-K // 128)), scales_like(g, -(-N // 128), -(-K // 128))
+    need = qg._size("qmm_fp8_b128_workspace_size", M, N, K)
+    guarded = torch.full((need + 64,), 0x7F, dtype=torch.uint8, device="cuda")  # NaN codes around and in it
+    check_product(qg.qmm_fp8_b128(a, sa, w, sw, workspace=guarded[:need]), a, sa, w, sw)
+    assert (guarded[need:] == 0x7F).all()
+    check_product(qg.qmm_fp8_b128(a, sa, w, sw, workspace=guarded[: need - 1]), a, sa, w, sw)
+    assert qg.device_error() == 0
+
+
 def test_product_unaligned_operands():
     g = rng(9)
     M, N, K = 37, 200, 512

@@ -41,11 +41,15 @@ def test_quantize():
 
 
 def test_product():
-    good = dict(a=at(0), sa=at(1), w=at(2), sw=at(3), y=at(4), dtype=BF16, M=4, N=300, K=256, stream=None)
+    good = dict(a=at(0), sa=at(1), w=at(2), sw=at(3), y=at(4), dtype=BF16, M=4, N=300, K=256, ws=None, wsb=0,
+                stream=None)
     refused("qmm_fp8_b128", good, a=(None, INVALID), sa=(None, INVALID), w=(None, INVALID), sw=(None, INVALID),
             y=(None, INVALID), dtype=(F16, INVALID), M=(0, INVALID), N=(0, INVALID), K=(0, INVALID),
             N_2=(1 << 31, UNSUPPORTED), sa_2=(at(1) + 2, MISALIGNED), y_2=(at(4) + 1, MISALIGNED), y_3=(at(0), INVALID),
             y_4=(at(2) + 256, INVALID))
+    n = C.c_size_t(1)
+    assert qg.lib().qmm_fp8_b128_workspace_size(0, 300, 250, C.byref(n)) == INVALID
+    assert qg.lib().qmm_fp8_b128_workspace_size(4, 300, 250, C.byref(n)) == OK and n.value == 304 * 256
     big = dict(good, M=(1 << 31) - 1, N=(1 << 31) - 1)
     refused("qmm_fp8_b128", big, K=(16, UNSUPPORTED))
 
