@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++seg;
                 tc_fence_after();
                 const bool live = r0 + t * 128 + row < s.rows;
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
                 const long long at = (long long)(s.first + r / w.group) * w.a.hq + walk.p.head * w.group + r % w.group;
                 const long long pt = ((long long)blockIdx.x * 2 + walk.slot) * kRT + t * 128 + row;
 #pragma unroll 1
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (threadIdx.x == 0) walk.note(cuts, kRT, blockIdx.x);
                 if (live) {
                     if (!walk.whole) w.ml[pt] = make_float2(m, l);
-                    else if (w.a.lse) w.a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                    else if (w.a.lse) w.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                 }
             }
         }

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v[4] += b.x * f; v[5] += b.y * f; v[6] += b.z * f; v[7] += b.w * f;
             }
             if (walk.whole) {
-                const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                const float inv = ll == 0.f ? 0.f : 1.f / ll;  // NaN stays NaN
                 const int tok = s.first + (r0 + r) / w.group, head = walk.p.head * w.group + (r0 + r) % w.group;
                 const long long at = (long long)tok * w.a.hq + head;
                 uint4 u;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 u.w = pack2<T>(v[6] * inv, v[7] * inv);
                 *reinterpret_cast<uint4*>(static_cast<T*>(w.a.out) + at * D + nt * 8) = u;
                 if (w.a.lse && nt == 0)
-                    w.a.lse[at] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+                    w.a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
             } else {
                 const long long at = ((long long)blockIdx.x * 2 + walk.slot) * RT + r;
                 float4* dst = reinterpret_cast<float4*>(w.part + at * D + nt * 8);

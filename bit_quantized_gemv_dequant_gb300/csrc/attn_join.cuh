@@ -48,13 +48,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Work w) {
                 for (int j = 0; j < E; ++j) v[j] += e[j] * f;
             }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const int row = n.r0 + r;
         const long long at = n.out_row + (long long)(row / w.group) * w.a.hq + n.head + row % w.group;
         uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(w.a.out) + at * D + lane * E);
 #pragma unroll
         for (int e = 0; e < E; e += 2) out[e / 2] = pack2<T>(v[e] * inv, v[e + 1] * inv);
-        if (w.a.lse && lane == 0) w.a.lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (w.a.lse && lane == 0) w.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
 }
 

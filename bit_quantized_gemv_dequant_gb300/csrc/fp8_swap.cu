@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(Geo<BN>::kThreads, 1)
     } else if (warp >= 4) {
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float* sw = p.sw + (long long)blockIdx.y * p.KB + b0;
+        bool ok = true;
         for (int i0 = 0; i0 < nb; i0 += kScaleBlocks) {
             // The scales of the next blocks: [block][row of a], both factors in one.
             const int nk = min(kScaleBlocks, nb - i0);
@@ -181,10 +182,9 @@ __global__ void __launch_bounds__(Geo<BN>::kThreads, 1)
             named_bar_sync(1, G::kEpi);
             for (int b = 0; b < nk; ++b) {
                 const int i = i0 + b, tb = i % G::kBufs;
-                if (!warp_bar_wait(t_full(tb), (i / G::kBufs) & 1)) {
+                if (ok && !warp_bar_wait(t_full(tb), (i / G::kBufs) & 1)) {
                     if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
-                    i0 = nb;  // the sums are lost; the barriers below are still met
-                    break;
+                    ok = false;  // the sums are lost; the barriers are still met
                 }
                 tc_fence_after();
                 const float4* sc = reinterpret_cast<const float4*>(scales + b * BN + own0);
@@ -354,6 +354,7 @@ int launch_swap(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
 // blocks one after the other is taken. M = 256, N = K = 4096: 11.7 us with the
 // split, 18.1 in 256-wide tiles; M = 256, N = 12288, K = 4096: 32.9 and 19.3.
 bool swap_is_shorter(const DevCtx& dc, const Fp8Args& a) {
+    if (a.N > 65535 * 128LL) return false;  // more tiles than a grid's y has room for
     if (a.M <= 64) return true;
     Plan p;
     if (plan<128, float>(dc, a, &p) != QG_OK) return false;

@@ -220,6 +220,20 @@ def test_bad_indexes_are_recorded_and_not_followed():
     assert qg.device_error() == 32
 
 
+@pytest.mark.parametrize("new", [[1, 1], [150, 2]])
+def test_a_nan_reaches_its_rows_and_no_others(new):
+    """A NaN in a visible key, value or query: NaN in the rows that see it (out and lse), the others unchanged."""
+    args = make(15, new, [300, 300], 4, 2, 64, 16, torch.bfloat16)
+    q, k, v, table, off, ctx = args
+    good, glse = qg.attn_paged(*args, return_lse=True)
+    k[int(table[0, 2]), 1, 3] = float("nan")  # key 35 of sequence 0, key head 1
+    out, lse = qg.attn_paged(*args, return_lse=True)
+    assert torch.isnan(out[:new[0], 2:].float()).all() and torch.isnan(lse[:new[0], 2:]).all()
+    assert torch.equal(out[:new[0], :2], good[:new[0], :2]) and torch.equal(lse[:new[0], :2], glse[:new[0], :2])
+    assert torch.equal(out[new[0]:], good[new[0]:])
+    assert qg.device_error() == 0
+
+
 def test_nothing_to_do_and_refusals():
     q, k, v, table, off, ctx = make(14, [2, 3], [20, 30], 8, 2, 64, 16, torch.bfloat16)
     none = torch.zeros(3, dtype=torch.int32, device="cuda")
