@@ -3,11 +3,12 @@ operators around it in a serving step: the block-scaled fp8 product, attention
 over a paged cache, the upkeep of its pages and token log probabilities.
 
 The compute lives in the CUDA library libqgemv.so (C ABI in include/qgemv.h);
-this module is a thin ctypes binding over it with the same names. It only
-marshals arguments: torch supplies device memory and the current stream,
-every step of the computation runs in the library's kernels. The library is
-loaded on first use, and every call raises if it has not been built or no
-CUDA device is present: there is no CPU fallback.
+this module is a thin binding over it with the same names, by ctypes and, for
+the serving operators, by the compiled module _serving. It only marshals
+arguments: torch supplies device memory and the current stream, every step of
+the computation runs in the library's kernels. The library is loaded on first
+use, and every call raises if it has not been built or no CUDA device is
+present: there is no CPU fallback.
 
 Workspace: calls that need device scratch (split-K partial sums) get it from
 a torch buffer per (device, stream) that grows on demand, unless the caller
@@ -17,6 +18,7 @@ on one stream are ordered by the stream.
 from __future__ import annotations
 
 import ctypes as C
+import importlib
 import os
 import threading
 
@@ -350,80 +352,29 @@ def dequant_affine(q, scales, biases, N, K, group_size, packed, out=None, *, str
 
 
 # ------------------------------------------------------- serving operators
-_DTYPES = {torch.float32: QG_F32, torch.float16: QG_F16, torch.bfloat16: QG_BF16}
-_E4M3 = torch.float8_e4m3fn
+# Through the module _serving (csrc/serving.cpp), which does for these calls what
+# the functions above do, in less time: tensors are checked (ValueError), new
+# outputs allocated, and a status that is not QG_OK raises QGError.
+_SERVING = None
 
 
-def _dtype(t: torch.Tensor, name: str) -> int:
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return d
-
-
-def _rows(t: torch.Tensor, name: str, dims: int):
-    """(address, row stride) of a CUDA tensor whose rows t[i] are dense; the
-    rows may lie apart (a part of a fused projection, a padded vocabulary)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    shape = t.shape
-    if len(shape) != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
-    width = shape[1] if dims == 2 else shape[1] * shape[2]
-    if t.is_contiguous():
-        return t.data_ptr(), width
-    strides, step = t.stride(), 1
-    for i in range(dims - 1, 0, -1):
-        if shape[i] > 1 and strides[i] != step:
-            raise ValueError(f"{name} must have dense rows")
-        step *= shape[i]
-    return t.data_ptr(), strides[0] if shape[0] > 1 else width
-
-
-def _same(t: torch.Tensor, name: str, *shape) -> None:
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
-
-
-_SIZES = {}
-
-
-def _size(what: str, *args) -> int:
-    """The workspace bytes that the library asks for, asked once per shape and device."""
-    key = (what, torch._C._cuda_getDevice(), *args)
-    n = _SIZES.get(key)
-    if n is None:
-        v = C.c_size_t(0)
-        _check(getattr(lib(), what)(*args, C.byref(v)), what)
-        if len(_SIZES) > 4096:
-            _SIZES.clear()
-        n = _SIZES[key] = int(v.value)
-    return n
+def _calls():
+    global _SERVING
+    if _SERVING is None:
+        lib()
+        if not os.path.exists(os.path.join(_HERE, "_serving.so")):
+            raise RuntimeError("_serving.so is missing: build it with __graft_entry__.build()")
+        module = importlib.import_module(__name__ + "._serving")
+        module.set_error(QGError)
+        _SERVING = module
+    return _SERVING
 
 
 def quantize_fp8_b128(x, codes=None, scales=None, *, stream=None):
     """(codes, scales) of x [M, K] (float32, float16 or bfloat16; its rows may
     lie apart): e4m3 codes [M, K] and one float32 scale per 128 values of a
     row, [M, ceil(K / 128)]."""
-    at, stride = _rows(x, "x", 2)
-    M, K = x.shape
-    dev = x.device
-    if codes is None:
-        codes = torch.empty((M, K), dtype=_E4M3, device=dev)
-        codes_at = codes.data_ptr()
-    else:
-        _same(codes, "codes", M, K)
-        codes_at = _dev(codes, "codes", _E4M3)
-    if scales is None:
-        scales = torch.empty((M, (K + 127) // 128), dtype=torch.float32, device=dev)
-        scales_at = scales.data_ptr()
-    else:
-        _same(scales, "scales", M, (K + 127) // 128)
-        scales_at = _dev(scales, "scales", torch.float32)
-    rc = lib().quantize_fp8_b128(at, _dtype(x, "x"), stride, codes_at, scales_at, M, K, _stream(stream))
-    if rc:
-        raise QGError("quantize_fp8_b128", rc)
-    return codes, scales
+    return (_SERVING or _calls()).quantize_fp8_b128(x, codes, scales, stream)
 
 
 def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, workspace=None,
@@ -431,27 +382,7 @@ def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, w
     """y[M, N] = (a * a_scales) . (w * w_scales)^T: e4m3 codes a [M, K] with a
     scale per row and 128 values of K, w [N, K] with one per 128 x 128 values;
     y is float32 or bfloat16."""
-    M, K = a.shape
-    N = w.shape[0]
-    KB = (K + 127) // 128
-    _same(w, "w", N, K)
-    _same(a_scales, "a_scales", M, KB)
-    _same(w_scales, "w_scales", (N + 127) // 128, KB)
-    at, scales_at = _dev(a, "a", _E4M3), _dev(a_scales, "a_scales", torch.float32)
-    if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=a.device)
-        y_at = y.data_ptr()
-    else:
-        _same(y, "y", M, N)
-        y_at = _dev(y, "y")
-    w_at, st = _dev(w, "w", _E4M3), _stream(stream)
-    need = _size("qmm_fp8_b128_workspace_size", M, N, K) if (K | at | w_at) & 15 else 0
-    ws, wsb = _scratch(need, a.device, workspace, st)
-    rc = lib().qmm_fp8_b128(at, scales_at, w_at, _dev(w_scales, "w_scales", torch.float32), y_at,
-                            _dtype(y, "y"), M, N, K, ws, wsb, st)
-    if rc:
-        raise QGError("qmm_fp8_b128", rc)
-    return y
+    return (_SERVING or _calls()).qmm_fp8_b128(a, a_scales, w, w_scales, y, out_dtype, workspace, stream)
 
 
 def attn_paged(q, k_cache, v_cache, page_table, q_offsets, context_lens, out=None, lse=None, *,
@@ -468,40 +399,8 @@ def attn_paged(q, k_cache, v_cache, page_table, q_offsets, context_lens, out=Non
     its keys, the new ones included. max_new: the most new tokens that any
     sequence has (default: all of q's rows). scale: default head_dim ** -0.5.
     softcap > 0 caps the scores, window > 0 limits how far back a row sees."""
-    at, stride = _rows(q, "q", 3)
-    T, Hq, D = q.shape
-    NP, Hkv, page, _ = cache = k_cache.shape
-    B, width = page_table.shape
-    i32 = torch.int32
-    if cache[3] != D or v_cache.shape != cache:
-        raise ValueError(f"k_cache and v_cache must have the shape [pages, kv_heads, page_size, {D}]")
-    _same(q_offsets, "q_offsets", B + 1)
-    _same(context_lens, "context_lens", B)
-    dt, dev = q.dtype, q.device
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-        out_at = out.data_ptr()
-    else:
-        _same(out, "out", T, Hq, D)
-        out_at = _dev(out, "out", dt)
-    lse_at = None
-    if lse is not None:
-        _same(lse, "lse", T, Hq)
-        lse_at = _dev(lse, "lse", torch.float32)
-    elif return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        lse_at = lse.data_ptr()
-    st = _stream(stream)
-    max_new = T if max_new is None else int(max_new)
-    ws, wsb = _scratch(_size("attn_paged_workspace_size", T, B, max_new, Hq, Hkv, D), dev, workspace, st)
-    rc = lib().attn_paged(at, stride, _dev(k_cache, "k_cache", dt), _dev(v_cache, "v_cache", dt),
-                          _dev(page_table, "page_table", i32), _dev(q_offsets, "q_offsets", i32),
-                          _dev(context_lens, "context_lens", i32), out_at, lse_at, _dtype(q, "q"),
-                          T, B, max_new, Hq, Hkv, D, NP, page, width,
-                          D ** -0.5 if scale is None else scale, softcap, window, ws, wsb, st)
-    if rc:
-        raise QGError("attn_paged", rc)
-    return (out, lse) if lse is not None else out
+    return (_SERVING or _calls()).attn_paged(q, k_cache, v_cache, page_table, q_offsets, context_lens, out, lse,
+                                                max_new, scale, softcap, window, return_lse, workspace, stream)
 
 
 def kv_append(k, v, k_cache, v_cache, slots, *, stream=None):
@@ -509,40 +408,13 @@ def kv_append(k, v, k_cache, v_cache, slots, *, stream=None):
     parts of one fused projection) into a layer's k_cache and v_cache
     [num_pages, kv_heads, page_size, head_dim], rounded to their type. slots
     int64 [tokens]: page * page_size + place of each row; negative: skipped."""
-    ka, ks = _rows(k, "k", 3)
-    va, vs = _rows(v, "v", 3)
-    T, H, D = shape = k.shape
-    NP, _, page, _ = cache = k_cache.shape
-    if v.shape != shape or v.dtype != k.dtype:
-        raise ValueError("k and v must be alike")
-    if v_cache.shape != cache or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must be alike")
-    if cache[1] != H or cache[3] != D:
-        raise ValueError(f"k_cache and v_cache must have the shape [pages, {H}, page_size, {D}]")
-    _same(slots, "slots", T)
-    rc = lib().kv_append(ka, va, ks, vs, _dtype(k, "k"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-                         _dtype(k_cache, "k_cache"), _dev(slots, "slots", torch.int64), T, H, D, NP, page,
-                         _stream(stream))
-    if rc:
-        raise QGError("kv_append", rc)
-
-
-def _planes(cache):
-    """(address, planes, pages, bytes per page) of a cache [planes, num_pages, ...]."""
-    at = _dev(cache, "cache")
-    if cache.dim() < 3 or cache.numel() == 0:
-        raise ValueError("cache must be [planes, num_pages, ...] with at least one value")
-    planes, pages = cache.shape[:2]
-    return at, planes, pages, cache.numel() // (planes * pages) * cache.element_size()
+    return (_SERVING or _calls()).kv_append(k, v, k_cache, v_cache, slots, stream)
 
 
 def kv_copy_pages(cache, src, dst, *, stream=None):
     """In every plane of cache [planes, num_pages, ...]: page dst[i] = page
     src[i] (int32). Pairs with a negative member are skipped."""
-    _same(dst, "dst", *src.shape)
-    _check(lib().kv_copy_pages(*_planes(cache), _dev(src, "src", torch.int32),
-                               _dev(dst, "dst", torch.int32), src.numel(), _stream(stream)),
-           "kv_copy_pages")
+    return (_SERVING or _calls()).kv_copy_pages(cache, src, dst, stream)
 
 
 def kv_fork(cache, page_table, lens, ref_counts, parents, page_size, *, workspace=None, stream=None):
@@ -550,58 +422,22 @@ def kv_fork(cache, page_table, lens, ref_counts, parents, page_size, *, workspac
     parents[c] of page_table and gets a copy of its partly filled last page, in
     the lowest free pages. Returns (child_table [children, width], child_lens,
     new ref_counts); cache [planes, num_pages, ...] is changed in place."""
-    planes = _planes(cache)
-    rows, width = page_table.shape
-    n = parents.numel()
-    _same(lens, "lens", rows)
-    _same(ref_counts, "ref_counts", planes[2])
-    dev = page_table.device
-    table = torch.empty((n, width), dtype=torch.int32, device=dev)
-    child_lens = torch.empty(n, dtype=torch.int32, device=dev)
-    refs = torch.empty_like(ref_counts)
-    st = _stream(stream)
-    ws, wsb = _scratch(_size("kv_fork_workspace_size", n), dev, workspace, st)
-    _check(lib().kv_fork(*planes, int(page_size), _dev(page_table, "page_table", torch.int32),
-                         _dev(lens, "lens", torch.int32), _dev(ref_counts, "ref_counts", torch.int32),
-                         rows, width, _dev(parents, "parents", torch.int32), n, table.data_ptr(),
-                         child_lens.data_ptr(), refs.data_ptr(), ws, wsb, st), "kv_fork")
-    return table, child_lens, refs
+    return (_SERVING or _calls()).kv_fork(cache, page_table, lens, ref_counts, parents, page_size, workspace,
+                                             stream)
 
 
 def kv_free(page_table, lens, ref_counts, drop, *, stream=None):
     """New (page_table, lens, ref_counts) without the rows where drop (uint8
     [rows]) is not 0: their entries are -1, their length 0, and each page that
     they held counts one holder less."""
-    rows, width = page_table.shape
-    _same(lens, "lens", rows)
-    _same(drop, "drop", rows)
-    table, new_lens = torch.empty_like(page_table), torch.empty_like(lens)
-    refs = torch.empty_like(ref_counts)
-    _check(lib().kv_free(_dev(page_table, "page_table", torch.int32), _dev(lens, "lens", torch.int32),
-                         _dev(ref_counts, "ref_counts", torch.int32), _dev(drop, "drop", torch.uint8),
-                         rows, width, ref_counts.numel(), table.data_ptr(), new_lens.data_ptr(),
-                         refs.data_ptr(), _stream(stream)), "kv_free")
-    return table, new_lens, refs
+    return (_SERVING or _calls()).kv_free(page_table, lens, ref_counts, drop, stream)
 
 
 def kv_compact(cache, page_table, ref_counts, *, workspace=None, stream=None):
     """Moves the pages of cache [planes, num_pages, ...] so that those in use
     are 0 .. live - 1. Returns (page_table, ref_counts, page_map, live) in the
     new numbers; page_map[p] is page p's new number, -1 if it was free."""
-    planes = _planes(cache)
-    rows, width = page_table.shape
-    _same(ref_counts, "ref_counts", planes[2])
-    dev = page_table.device
-    table, refs = torch.empty_like(page_table), torch.empty_like(ref_counts)
-    page_map = torch.empty_like(ref_counts)
-    live = torch.empty(1, dtype=torch.int32, device=dev)
-    st = _stream(stream)
-    ws, wsb = _scratch(_size("kv_compact_workspace_size", planes[2]), dev, workspace, st)
-    _check(lib().kv_compact(*planes, _dev(page_table, "page_table", torch.int32), rows, width,
-                            _dev(ref_counts, "ref_counts", torch.int32), table.data_ptr(),
-                            refs.data_ptr(), page_map.data_ptr(), live.data_ptr(), ws, wsb, st),
-           "kv_compact")
-    return table, refs, page_map, live
+    return (_SERVING or _calls()).kv_compact(cache, page_table, ref_counts, workspace, stream)
 
 
 def token_logprobs(logits, targets, top_k=0, *, stream=None):
@@ -610,23 +446,7 @@ def token_logprobs(logits, targets, top_k=0, *, stream=None):
     negative: none, 0 and rank -1), the row's entropy, how many logits are
     greater than the target's, and the min(top_k, V) largest alternatives as log
     probabilities and ids, ties to the lower id."""
-    at, stride = _rows(logits, "logits", 2)
-    M, V = logits.shape
-    _same(targets, "targets", M)
-    targets_at = _dev(targets, "targets", torch.int64)
-    k = min(int(top_k), V)
-    dev, f32, i32 = logits.device, torch.float32, torch.int32
-    logprobs = torch.empty(M, dtype=f32, device=dev)
-    entropy = torch.empty_like(logprobs)
-    ranks = torch.empty(M, dtype=i32, device=dev)
-    top = torch.empty((M, max(k, 0)), dtype=f32, device=dev)
-    ids = torch.empty((M, max(k, 0)), dtype=i32, device=dev)
-    rc = lib().token_logprobs(at, _dtype(logits, "logits"), stride, targets_at, M, V, k, logprobs.data_ptr(),
-                              entropy.data_ptr(), ranks.data_ptr(), top.data_ptr(), ids.data_ptr(),
-                              _stream(stream))
-    if rc:
-        raise QGError("token_logprobs", rc)
-    return logprobs, entropy, ranks, top, ids
+    return (_SERVING or _calls()).token_logprobs(logits, targets, top_k, stream)
 
 
 def device_error(clear: bool = True) -> int:

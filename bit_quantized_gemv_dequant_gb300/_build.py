@@ -1,6 +1,8 @@
 """Build libqgemv.so in-tree: every .cu under csrc/ compiled for sm_103a in
 parallel with nvcc, then linked into one shared library (CUDA runtime linked
-statically, so the library needs only the driver at run time)."""
+statically, so the library needs only the driver at run time). Beside it the
+Python module _serving.so (csrc/serving.cpp) against this interpreter's and
+torch's headers, which calls that library."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -14,6 +16,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "qgemv")
 LIB = os.path.join(PKG, "libqgemv.so")
+MODULE = os.path.join(PKG, "_serving.so")
+MODULE_SRC = os.path.join(CSRC, "serving.cpp")
+HEADER = os.path.join(INCLUDE, "qgemv.h")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -47,15 +52,43 @@ def _compile(src, extra):
     return obj, ""
 
 
+def _compile_module():
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    obj = os.path.join(OBJDIR, "serving.cpp.o")
+    if _stale(obj, [MODULE_SRC, HEADER, os.path.join(base, "version.py")]):
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-I{INCLUDE}",
+               f"-I{sysconfig.get_paths()['include']}", f"-I{base}/include", "-I/usr/local/cuda/include", "-c",
+               MODULE_SRC, "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for {MODULE_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj, os.path.join(base, "lib")
+
+
+def _link_module(obj, torch_lib):
+    tmp = MODULE + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libqgemv.so", f"-L{torch_lib}", "-ltorch_python",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MODULE)
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
-    if not force and not _stale(LIB, _deps()):
+    if not force and not _stale(LIB, _deps()) and not _stale(MODULE, [MODULE_SRC, HEADER, LIB]):
         return LIB
     if force:
         for o in glob.glob(os.path.join(OBJDIR, "*.o")):
             os.remove(o)
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 4)) as ex:
+        module = ex.submit(_compile_module)
         results = list(ex.map(lambda s: _compile(s, list(extra)), _sources()))
+        module = module.result()
     if verbose:
         for _, log in results:
             if log:
@@ -66,6 +99,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_module(*module)
     return LIB
 
 

@@ -5,6 +5,7 @@ magnitudes and A = sum_j p_j |v_j|, an output may be off by u A for the
 probabilities' rounding and u |out| for its own, doubled, 1e-5 (1 + S) A for
 the f32 scores and sums, and 2^-24 n max|v| for f16 probabilities below its
 normal range; the log-sum by 1e-5 (1 + S)."""
+import ctypes as C
 import math
 
 import pytest
@@ -13,6 +14,13 @@ import torch
 import bit_quantized_gemv_dequant_gb300 as qg
 
 pytestmark = pytest.mark.gpu
+
+
+def workspace_bytes(*shape):
+    n = C.c_size_t()
+    assert qg.lib().attn_paged_workspace_size(*shape, C.byref(n)) == 0
+    return n.value
+
 
 UNIT = {torch.bfloat16: 2.0**-8, torch.float16: 2.0**-11}
 
@@ -186,7 +194,7 @@ def test_repeats_to_the_bit_on_another_stream_and_in_a_graph():
     with torch.cuda.stream(s):
         b = qg.attn_paged(*args)
         out = torch.empty_like(a)
-        need = qg._size("attn_paged_workspace_size", 93, 4, 93, 32, 8, 128)
+        need = workspace_bytes(93, 4, 93, 32, 8, 128)
         ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=s):

@@ -3,6 +3,8 @@
 Codes and scales are defined to the bit and compared so. A product's bound is
 the f32 paths' 1e-5 * sum |terms| + 1e-6 and, for bf16 outputs, one rounding
 (2^-8 of the value) more."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
@@ -10,6 +12,13 @@ import torch
 import bit_quantized_gemv_dequant_gb300 as qg
 
 pytestmark = pytest.mark.gpu
+
+
+def workspace_bytes(*shape):
+    n = C.c_size_t()
+    assert qg.lib().qmm_fp8_b128_workspace_size(*shape, C.byref(n)) == 0
+    return n.value
+
 
 E4M3 = torch.float8_e4m3fn
 DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
@@ -167,7 +176,7 @@ def test_product_of_odd_rows_with_and_without_workspace(M, N, K):
     g = rng(M * N + K)
     a, w = codes_like(g, M, K), codes_like(g, N, K)
     sa, sw = scales_like(g, M, -(-K // 128)), scales_like(g, -(-N // 128), -(-K // 128))
-    need = qg._size("qmm_fp8_b128_workspace_size", M, N, K)
+    need = workspace_bytes(M, N, K)
     guarded = torch.full((need + 64,), 0x7F, dtype=torch.uint8, device="cuda")  # NaN codes around and in it
     check_product(qg.qmm_fp8_b128(a, sa, w, sw, workspace=guarded[:need]), a, sa, w, sw)
     assert (guarded[need:] == 0x7F).all()
