@@ -165,13 +165,11 @@ struct Row {
 struct Stats {
     float c, s, t;  // c = -infinity: nothing yet
 };
-__device__ __forceinline__ Stats join(const Stats& a, const Stats& b) {
-    const float c = fmaxf(a.c, b.c);
-    const float ref = c == -INFINITY ? 0.f : c;
-    // A side without logits has s = t = 0; its distance is cut to a finite number.
-    const float ga = fmaxf((a.c - ref) * kLog2e, -200.f), gb = fmaxf((b.c - ref) * kLog2e, -200.f);
-    const float fa = ex2(ga), fb = ex2(gb);
-    return Stats{c, a.s * fa + b.s * fb, fa * (a.t + ga * a.s) + fb * (b.t + gb * b.s)};
+// The same with c instead of a.c. (Without logits s = t = 0; the distance from
+// -infinity is cut to a finite number.)
+__device__ __forceinline__ Stats rebased(const Stats& a, float c) {
+    const float g = fmaxf((a.c - (c == -INFINITY ? 0.f : c)) * kLog2e, -200.f), f = ex2(g);
+    return Stats{c, a.s * f, f * (a.t + g * a.s)};
 }
 
 struct Thread {
@@ -261,22 +259,16 @@ __device__ __forceinline__ Key warp_sort(Key k) {
     return k;
 }
 
-// Puts `in` to its place in a list over the warp's lanes, which lets its last go.
-__device__ __forceinline__ Key insert(Key list, Key in) {
-    const int lane = threadIdx.x & 31;
-    const int at = __popc(__ballot_sync(0xFFFFFFFFu, list > in));
-    const Key up = __shfl_up_sync(0xFFFFFFFFu, list, 1);
-    return lane == at ? in : lane > at ? up : list;
-}
-
-// The lanes' statistics in one. Both sides of an exchange join in the same order.
+// The lanes' statistics in one, the same on all lanes.
 __device__ __forceinline__ void join_lanes(Stats& st, int& above) {
-    const int lane = threadIdx.x & 31;
+    float c = st.c;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) c = fmaxf(c, __shfl_xor_sync(0xFFFFFFFFu, c, i));
+    st = rebased(st, c);
 #pragma unroll
     for (int i = 16; i; i >>= 1) {
-        const Stats o{__shfl_xor_sync(0xFFFFFFFFu, st.c, i), __shfl_xor_sync(0xFFFFFFFFu, st.s, i),
-                      __shfl_xor_sync(0xFFFFFFFFu, st.t, i)};
-        st = lane & i ? join(o, st) : join(st, o);
+        st.s += __shfl_xor_sync(0xFFFFFFFFu, st.s, i);
+        st.t += __shfl_xor_sync(0xFFFFFFFFu, st.t, i);
         above += __shfl_xor_sync(0xFFFFFFFFu, above, i);
     }
 }
@@ -296,7 +288,9 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) row_kernel(const Lo
     __shared__ __align__(8) uint64_t more[4];  // left[i] written, taken
     __shared__ Left left[2];
     __shared__ int owner[kThreads];            // the threads that can hold the share's largest
-    __shared__ Key found[kTop];                // those
+    __shared__ Key wait[64];                   // keys on their way into the list of those
+    __shared__ __align__(16) uint8_t look[32 * 32];  // the chunks being looked through
+    __shared__ Key found[kTop];
     __shared__ Stats all;                      // and its statistics
     __shared__ int all_above;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -450,13 +444,18 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) row_kernel(const Lo
             ok = false;
         }
         const Left& l = left[rows & 1];
-        Stats st{-INFINITY, 0.f, 0.f};
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) most = fmaxf(most, l.c[i * 32 + lane]);
+        Stats st{most, 0.f, 0.f};
         int above = 0;
         Key own[kWarps];  // of threads lane, 32 + lane, ...: best logit, earlier chunk first
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
             const int t = i * 32 + lane;
-            st = join(st, Stats{l.c[t], l.s[t], l.t[t]});
+            const Stats o = rebased(Stats{l.c[t], l.s[t], l.t[t]}, most);
+            st.s += o.s;
+            st.t += o.t;
             above += l.above[t];
             const int c = l.chunk[t];
             own[i] = c < row.c_hi ? (Key)value_key(l.best[t]) << 32 | (0xFFFFFFFFu - (uint32_t)c) : 0;
@@ -485,35 +484,61 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) row_kernel(const Lo
             }
             __syncwarp();
             Key worst = 0;  // the k-th of `mine`
-            // The owners' chunks, all in a line, 32 at a time; the next ones on the way.
+            int waiting = 0;
+            // Takes the first 32 of the waiting keys into `mine`.
+            auto flush = [&] {
+                __syncwarp();
+                mine = merge_top(mine, warp_sort(lane < waiting ? wait[lane] : 0));
+                worst = __shfl_sync(0xFFFFFFFFu, mine, a.k - 1);
+                const Key more = lane + 32 < waiting ? wait[lane + 32] : 0;
+                __syncwarp();
+                wait[lane] = more;
+                waiting = max(0, waiting - 32);
+                __syncwarp();
+            };
+            // The owners' chunks, all in a line, 32 at a time, the next ones on the way.
             const int per = (row.c_hi - row.c_lo + kThreads - 1) / kThreads, n = owners * per;
-            auto at = [&](int q) { return q < n ? row.c_lo + owner[q / per] + q % per * kThreads : row.c_hi; };
-            int c = at(lane);
             Chunk<T> ch;
-            if (c < row.c_hi) row.load(c, ch);
-            for (int q = 0; q < n; q += 32) {
-                const int cn = at(q + 32 + lane);
+            int c = row.c_hi, cn;
+#pragma unroll 1
+            for (int q0 = -32; q0 < n; q0 += 32) {
+                const int q = q0 + 32 + lane, o = q / per;
+                cn = q < n ? row.c_lo + owner[o] + (q - o * per) * kThreads : row.c_hi;
                 Chunk<T> next;
                 if (cn < row.c_hi) row.load(cn, next);
-                float v[N];
-                ch.get(v);
+                // Which of the chunk's logits may be among the largest, and those one
+                // at a time (from shared memory: the code stays short, for the readers'
+                // sake, who run from the same instruction cache).
+                uint32_t may = 0;
+                if (c < row.c_hi) {
+                    float v[N];
+                    ch.get(v);
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int id = c * N - row.off + i;
-                    const bool may = c < row.c_hi && id >= row.lo && id < row.hi && !(v[i] < least);
-                    if (!__any_sync(0xFFFFFFFFu, may)) continue;
-                    const Key key = may ? key_of(v[i], id) : 0;
-                    unsigned who = __ballot_sync(0xFFFFFFFFu, key > worst);
-                    while (who) {
-                        mine = insert(mine, __shfl_sync(0xFFFFFFFFu, key, __ffs(who) - 1));
-                        worst = __shfl_sync(0xFFFFFFFFu, mine, a.k - 1);
-                        who &= who - 1;
-                        who &= __ballot_sync(0xFFFFFFFFu, key > worst);
+                    for (int i = 0; i < N; ++i) may |= (uint32_t)!(v[i] < least) << i;
+                    const int first = c * N - row.off;  // ids outside the share are padding
+                    if (first < row.lo) may &= ~0u << (row.lo - first);
+                    if (first + N > row.hi) may &= (1u << (row.hi - first)) - 1u;
+                    uint4* to = reinterpret_cast<uint4*>(look + lane * 32);
+                    to[0] = make_uint4(ch.w[0], ch.w[1], ch.w[2], ch.w[3]);
+                    to[1] = make_uint4(ch.w[4], ch.w[5], ch.w[6], ch.w[7]);
+                }
+#pragma unroll 1
+                while (__any_sync(0xFFFFFFFFu, may)) {
+                    Key key = 0;
+                    if (may) {
+                        const int i = __ffs(may) - 1;
+                        key = key_of(to_f32(reinterpret_cast<const T*>(look + lane * 32)[i]), c * N - row.off + i);
+                        may &= may - 1;
                     }
+                    const unsigned who = __ballot_sync(0xFFFFFFFFu, key > worst);
+                    if (key > worst) wait[waiting + __popc(who & ((1u << lane) - 1))] = key;
+                    waiting += __popc(who);
+                    if (waiting >= 32) flush();
                 }
                 c = cn;
                 ch = next;
             }
+            while (waiting > 0) flush();
         }
 
         if (parts > 1) {  // the shares' results meet in the first CTA
@@ -543,8 +568,6 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) row_kernel(const Lo
             }
         }
         if (part == 0) {
-            st.c = __shfl_sync(0xFFFFFFFFu, st.c, 0);
-            st.s = __shfl_sync(0xFFFFFFFFu, st.s, 0);
             const float ls = log2f(st.s);
             const bool nan = st.s != st.s, none = st.c == -INFINITY && !nan;
             auto logp = [&](float x) { return nan ? NAN : x == -INFINITY ? -INFINITY : (x - st.c) - kLn2 * ls; };
