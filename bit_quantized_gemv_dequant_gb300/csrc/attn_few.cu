@@ -357,7 +357,7 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     if (rc == QG_OK) rc = cache_map(&mv, w.a, w.a.v, rows);
     if (rc == QG_OK) rc = launch(kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
     if (rc) return rc;
-    return launch_join<T, D, 16 * RB, 4>(w, s);
+    return launch_join<T, D, 16 * RB, 1, 12>(w, s);
 }
 
 template <class T, int D, int RB>
