@@ -21,9 +21,11 @@ namespace {
 //             take the accumulators into registers, times
 //             a_scale[m, b] * w_scale[n / 128, b] (f32): thread = row of w.
 //
-// The ring takes all of an SM, so a split is limited by how many clusters of its
-// size the GPU can place at once (18 clusters of 8 took two rounds: 12.0 us
-// instead of 7.0 at M = 37, N = 2200, K = 5200).
+// The ring takes all of an SM, so the split is chosen by how many clusters of its
+// size the GPU can place at once (plan() below). Measured, product alone:
+//   N = K = 4096, M = 1         6.3 us  2.7 TB/s of w (launch, first loads, joining)
+//   N = 2200, K = 5200, M = 33  6.8 us  1.7 TB/s
+//   N = 12288, K = 4096, M = 1  10.6 us 4.7 TB/s; M = 64 12.7 us
 //
 // The split's partial sums meet in shared memory over the cluster, each CTA
 // adding up its share of the rows of a in the order of the split: the result
@@ -262,26 +264,26 @@ __global__ void __launch_bounds__(Geo<BN>::kThreads, 1)
     }
 }
 
-// How many clusters of 1 << i CTAs the GPU holds at once, asked once per kernel
-// and device.
+// How many clusters of i CTAs the GPU holds at once, asked once per kernel and
+// device.
 template <int BN, class TY>
 int cluster_room(const DevCtx& dc, const int** room) {
     using G = Geo<BN>;
     static std::once_flag once[64];
     static cudaError_t error[64];
-    static int held[64][4];
+    static int held[64][9];
     std::call_once(once[dc.device], [&] {
         auto kern = swap_kernel<BN, TY>;
         cudaError_t& e = error[dc.device];
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
-        for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+        for (int i = 1; i < 9 && e == cudaSuccess; ++i) {
             cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(1u << i);
+            cfg.gridDim = dim3(i);
             cfg.blockDim = dim3(G::kThreads);
             cfg.dynamicSmemBytes = G::kSmem;
             cudaLaunchAttribute attr{};
             attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = 1u << i;
+            attr.val.clusterDim.x = i;
             attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
@@ -292,20 +294,32 @@ int cluster_room(const DevCtx& dc, const int** room) {
     return error[dc.device] == cudaSuccess ? QG_OK : cuda_fail(error[dc.device]);
 }
 
-// The tiles, and the largest split (its logarithm) whose clusters all run at
-// once with two k blocks per CTA at least.
+// The tiles, and the split of K with the shortest chain of k blocks one after the
+// other: rounds of clusters that run at once, times the k blocks of a CTA and
+// what a round costs besides (start, first loads, joining: about five blocks).
+// N = 12288, K = 4096 is 96 tiles: split in 3, two rounds of 11 blocks keep all SMs
+// loading, one round of 32 only 96 of them (M = 64: 12.7 us and 15.3). Powers of
+// two alone took 7.7 us at N = 2200, K = 5200, M = 33, split in 4.
+constexpr long long kRound = 5;
 struct Plan {
-    long long nt, mt, kb;
-    int log_split;
+    long long nt, mt, kb, cost;
+    int split;
 };
 template <int BN, class TY>
 int plan(const DevCtx& dc, const Fp8Args& a, Plan* p) {
     const int* room = nullptr;
     const int rc = cluster_room<BN, TY>(dc, &room);
     if (rc) return rc;
-    *p = Plan{(a.N + 127) / 128, (a.M + BN - 1) / BN, (a.K + 127) / 128, 0};
-    while (p->log_split < 3 && p->nt * p->mt <= room[p->log_split + 1] && p->kb >= (4 << p->log_split)) ++p->log_split;
-    return QG_OK;
+    *p = Plan{(a.N + 127) / 128, (a.M + BN - 1) / BN, (a.K + 127) / 128, 0, 0};
+    for (int i = 1; i < 9 && (i == 1 || p->kb >= 2 * i); ++i) {
+        if (room[i] < 1) continue;
+        const long long cost = (p->nt * p->mt + room[i] - 1) / room[i] * ((p->kb + i - 1) / i + kRound);
+        if (p->split == 0 || cost < p->cost) {
+            p->cost = cost;
+            p->split = i;
+        }
+    }
+    return p->split ? QG_OK : QG_ERR_UNSUPPORTED;
 }
 
 template <int BN, class TY>
@@ -320,13 +334,13 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     if (pl.nt > 65535 || pl.mt > 65535) return QG_ERR_UNSUPPORTED;
     const Params p{a.sa, a.sw, a.y, (int)a.M, (int)a.N, (int)pl.kb, false, dc.err};
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(1u << pl.log_split, (unsigned)pl.nt, (unsigned)pl.mt);
+    cfg.gridDim = dim3((unsigned)pl.split, (unsigned)pl.nt, (unsigned)pl.mt);
     cfg.blockDim = dim3(G::kThreads);
     cfg.dynamicSmemBytes = G::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1u << pl.log_split;
+    attr[0].val.clusterDim.x = (unsigned)pl.split;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -352,16 +366,14 @@ int launch_swap(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
 
 // Both kernels take about 0.5 us per k block and CTA, so the one with fewer k
 // blocks one after the other is taken. M = 256, N = K = 4096: 11.7 us with the
-// split, 18.1 in 256-wide tiles; M = 256, N = 12288, K = 4096: 32.9 and 19.3.
+// split, 18.1 in 256-wide tiles; M = 256, N = 12288, K = 4096: 32.9 and 18.1.
 bool swap_is_shorter(const DevCtx& dc, const Fp8Args& a) {
     if (a.N > 65535 * 128LL) return false;  // more tiles than a grid's y has room for
     if (a.M <= 64) return true;
     Plan p;
     if (plan<128, float>(dc, a, &p) != QG_OK) return false;
-    const long long ctas = (p.nt * p.mt) << p.log_split, split = 1ll << p.log_split;
-    const long long swap = (ctas + dc.num_sms - 1) / dc.num_sms * ((p.kb + split - 1) / split);
     const long long tiles = 2 * ((a.M + 255) / 256) * ((a.N + 255) / 256);  // per SM
-    return swap <= (tiles + dc.num_sms - 1) / dc.num_sms * p.kb;
+    return p.cost <= (tiles + dc.num_sms - 1) / dc.num_sms * (p.kb + kRound);
 }
 
 int code_map(CUtensorMap* m, const uint8_t* ptr, long long rows, long long cols, int box_rows) {
