@@ -139,9 +139,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     Cuts cuts;
     Place place;
-    if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1;
+    if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1, w.notes[blockIdx.x].bad = 0;
     if (locate<kRT, kKT, kThreads>(w, blockIdx.x, &cuts, &place, reinterpret_cast<long long*>(smem + G::kScratchOff))) {
         const long long n = cuts(blockIdx.x + 1) - cuts(blockIdx.x);
+        if (threadIdx.x == 0) note_start(w, place, n);
         Walk<kRT, kKT> walk(w, place, n);
         bool ok = true;
         if (warp == 8) {
@@ -150,12 +151,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i = 0, tails = 0;
             while (ok && walk.next()) {
                 for (int t = walk.lo; ok && t < walk.hi; ++t) {
-                    const int keys = max(0, min(kKT, walk.span.end - t * kKT));
+                    const int keys = max(0, min(kKT, walk.span.end - t * kKT)), unseen = walk.span.begin - t * kKT;
                     const int copies = (keys + rows - 1) / rows;
                     int page = 0, y = 0;
                     if (lane < copies) {
                         const int j = t * kKT + lane * rows;
-                        page = page_of(w, walk.p.b, j);
+                        page = page_from(w, walk.p.b, j, rows, walk.span.begin);
                         y = walk.p.head * w.a.page_size + j % w.a.page_size;
                     }
                     for (int kv = 0; kv < 2; ++kv, ++i) {
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = false;
                             break;
                         }
-                        const bool part = kv && keys < kKT;  // values past the last key are cleared
+                        const bool part = kv && (keys < kKT || unseen > 0);  // values that no row sees are cleared
                         const uint32_t bar = part ? tail : full(st);
                         const uint32_t dst = base + G::kRingOff + st * G::kTile;
                         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(copies * rows * D * 2));
@@ -183,9 +184,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             ++tails;
                             uint4* v = reinterpret_cast<uint4*>(smem + G::kRingOff + st * G::kTile);
-                            for (int h = 0; h < D / 64; ++h)
+                            for (int h = 0; h < D / 64; ++h) {
+                                for (int e = lane; e < unseen * 8; e += 32)
+                                    v[h * (G::kHalf / 16) + e] = make_uint4(0u, 0u, 0u, 0u);
                                 for (int e = keys * 8 + lane; e < kKT * 8; e += 32)
                                     v[h * (G::kHalf / 16) + e] = make_uint4(0u, 0u, 0u, 0u);
+                            }
                             fence_async_proxy();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(full(st));
@@ -438,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     tmem_ld16(o_at + c, o);
                     if (live && walk.whole) {
+                        if (l == l && !all_finite(reinterpret_cast<const float(&)[16]>(o))) w.notes[blockIdx.x].bad = 1;
                         uint32_t h[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -484,7 +489,7 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     if (rc == QG_OK) rc = cache_map(&mv, w.a, w.a.v, rows);
     if (rc == QG_OK) rc = launch(kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
     if (rc) return rc;
-    return launch_join<T, D, kRT, 4, 2>(w, s);
+    return launch_join<T, D, kRT, kKT, 4, 2>(w, s);
 }
 
 template <class T, int D>

@@ -91,10 +91,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     Cuts cuts;
     Place place;
-    if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1;
+    if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1, w.notes[blockIdx.x].bad = 0;
     if (!locate<RT, kKT, kThreads>(w, blockIdx.x, &cuts, &place, reinterpret_cast<long long*>(smem + G::kScratchOff)))
         return;
     const long long n = cuts(blockIdx.x + 1) - cuts(blockIdx.x);
+    if (threadIdx.x == 0) note_start(w, place, n);
     Walk<RT, kKT> walk(w, place, n);
 
     if (warp == kWarps) {
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane < copies) {
                     const int j = t * kKT + lane * rows;
-                    const int page = page_of(w, walk.p.b, j);
+                    const int page = page_from(w, walk.p.b, j, rows, walk.span.begin);
                     const int y = walk.p.head * w.a.page_size + j % w.a.page_size;
                     const uint32_t dst = base + st * G::kStage + lane * rows * 128;
 #pragma unroll
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[nt][e] *= keep[e >> 1];
             }
-            const int valid = walk.span.end - j0;  // keys of this warp that any row sees
+            const int from = walk.span.begin - j0, valid = walk.span.end - j0;  // keys of this warp that any row sees
 #pragma unroll
             for (int nb = 0; nb < KW / 16; ++nb) {
                 uint32_t pa[4];
@@ -247,14 +248,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pa[2 * h] = pack2<T>(v[0], v[1]);
                     pa[2 * h + 1] = pack2<T>(v[2], v[3]);
                 }
-                // Places past the last key may hold anything, NaN included.
+                // Places that no row sees may hold anything, NaN included.
                 uint32_t mask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-                const bool tail = valid < nb * 16 + 16;
-                if (tail) {
+                const bool edge = valid < nb * 16 + 16 || from > nb * 16;
+                if (edge) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int k = nb * 16 + h * 8 + c2;
-                        mask[h] = (k < valid ? 0xFFFFu : 0u) | (k + 1 < valid ? 0xFFFF0000u : 0u);
+                        mask[h] = (k >= from && k < valid ? 0xFFFFu : 0u) |
+                                  (k + 1 >= from && k + 1 < valid ? 0xFFFF0000u : 0u);
                     }
                 }
                 const int row = wk * KW + nb * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int nt = 0; nt < NT; nt += 2) {
                     uint32_t b[4];
                     ldsm_t(vt + chunk_at<D>(row, nt + (lane >> 4)), b);
-                    if (tail) {
+                    if (edge) {
                         b[0] &= mask[0];
                         b[1] &= mask[1];
                         b[2] &= mask[0];
@@ -327,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 u.z = pack2<T>(v[4] * inv, v[5] * inv);
                 u.w = pack2<T>(v[6] * inv, v[7] * inv);
                 *reinterpret_cast<uint4*>(static_cast<T*>(w.a.out) + at * D + nt * 8) = u;
+                if (ll == ll && !all_finite(v)) w.notes[blockIdx.x].bad = 1;
                 if (w.a.lse && nt == 0)
                     w.a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
             } else {
@@ -357,7 +360,7 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     if (rc == QG_OK) rc = cache_map(&mv, w.a, w.a.v, rows);
     if (rc == QG_OK) rc = launch(kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
     if (rc) return rc;
-    return launch_join<T, D, 16 * RB, 1, 12>(w, s);
+    return launch_join<T, D, 16 * RB, kKT, 1, 12>(w, s);
 }
 
 template <class T, int D, int RB>

@@ -7,22 +7,130 @@ namespace qg {
 namespace attn {
 namespace {
 
+constexpr int kJoinThreads = 128;
+
+template <int N>
+__device__ __forceinline__ bool all_finite(const float (&v)[N]) {
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) z = fmaf(v[i], 0.f, z);
+    return z == z;
+}
+
+// One row of out by a warp, from the keys that it sees alone.
+//
+// In a product of tiles a key that a row does not see enters with the
+// probability 0, and 0 times a value that is infinite or NaN is NaN. Values that
+// no row of the tile sees are cleared before the product; where some rows see a
+// key and some do not, an output that is not finite is found out here: either it
+// stays so, or it came from values that the row does not see. Lane = key for
+// the scores, columns for the output.
+template <class T, int D>
+__device__ __forceinline__ void redo_row(const Work& w, int b, int head, int r) {
+    const Seq s = seq_at(w, b);
+    const int lane = threadIdx.x & 31, tok = r / w.group, pos = s.ctx - s.n + tok;
+    const int h = head * w.group + r % w.group, from = w.a.window ? max(0, pos - w.a.window + 1) : 0;
+    const T* q = static_cast<const T*>(w.a.q) + (long long)(s.first + tok) * w.a.q_stride + (long long)h * D;
+    constexpr int E = D / 32;
+    float m = -INFINITY, l = 0.f, acc[E] = {};
+    for (int j0 = from; j0 <= pos; j0 += 32) {
+        const int j = j0 + lane;
+        float x = -INFINITY;
+        int page = w.a.num_pages;
+        if (j <= pos) {
+            page = page_of(w, b, j);
+            float dot = 0.f;
+            if (page < w.a.num_pages) {
+                const T* k = static_cast<const T*>(w.a.k) +
+                             (((long long)page * w.a.hkv + head) * w.a.page_size + j % w.a.page_size) * D;
+                for (int c = 0; c < D; c += 2) {
+                    const float2 a = unpack2<T>(*reinterpret_cast<const uint32_t*>(q + c));
+                    const float2 e = unpack2<T>(*reinterpret_cast<const uint32_t*>(k + c));
+                    dot = fmaf(a.x, e.x, fmaf(a.y, e.y, dot));
+                }
+            }
+            const float2 z = make_float2(dot, 0.f);
+            x = (w.a.softcap > 0.f ? score2<true>(w, z) : score2<false>(w, z)).x;
+        }
+        float top = x;
+#pragma unroll
+        for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+        const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn, keep = ex2(m - ref), p = ex2(x - ref);
+        m = mn;
+        l *= keep;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= keep;
+        for (int i = 0; i < min(32, pos - j0 + 1); ++i) {
+            const float pi = __shfl_sync(0xFFFFFFFFu, p, i);
+            const int at = __shfl_sync(0xFFFFFFFFu, page, i);
+            l += pi;
+            if (at == w.a.num_pages) continue;
+            const T* v = static_cast<const T*>(w.a.v) +
+                         (((long long)at * w.a.hkv + head) * w.a.page_size + (j0 + i) % w.a.page_size) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 f = unpack2<T>(*reinterpret_cast<const uint32_t*>(v + e));
+                acc[e] = fmaf(pi, f.x, acc[e]);
+                acc[e + 1] = fmaf(pi, f.y, acc[e + 1]);
+            }
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long at = (long long)(s.first + tok) * w.a.hq + h;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(w.a.out) + at * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) out[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// Looks through rows r0 .. r1 - 1 of a sequence and key head, then through those
+// that the main kernel's CTA of this number finished alone (if its note says
+// that some are not finite), for rows to be done again; warp `warp` of `warps`.
+template <class T, int D, int RT, int KT>
+__device__ __noinline__ void redo_rows(const Work& w, int b, int head, int r0, int r1, int warp, int warps) {
+    const Note& n = w.notes[blockIdx.x];
+    Walk<RT, KT> walk(w, Place{n.first_b, n.first_head, n.first_tile, n.first_at}, n.bad ? n.steps : 0);
+    const int lane = threadIdx.x & 31;
+    int at = r0, step = 1;
+    __syncwarp();  // the warp wrote r0 .. r1 - 1 itself
+    for (;;) {
+        for (; at < r1; at += step) {
+            const Seq s = seq_at(w, b);
+            const long long row = (long long)(s.first + at / w.group) * w.a.hq + head * w.group + at % w.group;
+            float v[D / 32];
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) v[e] = to_f32(static_cast<const T*>(w.a.out)[row * D + e * 32 + lane]);
+            if (!__all_sync(0xFFFFFFFFu, all_finite(v))) redo_row<T, D>(w, b, head, at);
+        }
+        do {
+            if (!walk.next()) return;
+        } while (!walk.whole);
+        b = walk.p.b;
+        head = walk.p.head;
+        at = walk.p.tile * RT + warp;
+        r1 = min(walk.s.rows, walk.p.tile * RT + RT);
+        step = warps;
+    }
+}
+
 // Joins the parts of row tiles that a cut fell into. CTA (x, y): the row tile
 // that CTA x's note names and its rows R y .. R y + R - 1, ROWS of them at a
 // time per warp. Parts come in the order of the keys: CTA `from`'s, then the
 // first segments of the CTAs after it up to x. Bound by the latency of its
 // loads, hence PARTS parts (many for short tiles that are cut finely, two for
 // tall ones) and ROWS rows under way at once.
-constexpr int kJoinThreads = 128;
-
-template <class T, int D, int RT, int R, int ROWS, int PARTS>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Work w) {
+//
+// REDO: rows of a tile may see different keys (sequences with several new
+// tokens). Without it the kernel has none of that code, which cost 1.2 of 9.5 us
+// with one token over 700 keys.
+template <class T, int D, int RT, int KT, int R, int ROWS, int PARTS, bool REDO>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Work w) {
     static_assert(R == ROWS * (kJoinThreads / 32), "one round per warp");
     pdl_trigger();
     pdl_wait();
     const Note n = w.notes[blockIdx.x];
     const int lane = threadIdx.x & 31, x = blockIdx.x, r0 = blockIdx.y * R + (threadIdx.x >> 5) * ROWS;
-    if (n.from < 0 || n.r0 + r0 >= n.rows) return;
+    const bool mine = n.from >= 0 && n.r0 + r0 < n.rows;
+    if (!mine && !(REDO && n.bad)) return;
     constexpr int E = D / 32;
     using V = std::conditional_t<E == 4, float4, float2>;
     float m[ROWS], l[ROWS], v[ROWS][E];
@@ -34,7 +142,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Work w) {
         for (int e = 0; e < E; ++e) v[i][e] = 0.f;
     }
     // The running maximum rescales what is there, as in the kernels.
-    for (int k0 = n.from; k0 <= x; k0 += PARTS) {
+    for (int k0 = mine ? n.from : x + 1; k0 <= x; k0 += PARTS) {
         float2 ml[ROWS][PARTS];
         V o[ROWS][PARTS];
 #pragma unroll
@@ -69,16 +177,25 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Work w) {
             }
         }
     }
+    bool redo = n.bad;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int row = n.r0 + r0 + i;
-        if (row >= n.rows) break;
+        if (!mine || row >= n.rows) break;
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
         const long long at = n.out_row + (long long)(row / w.group) * w.a.hq + n.head + row % w.group;
         uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(w.a.out) + at * D + lane * E);
 #pragma unroll
         for (int e = 0; e < E; e += 2) out[e / 2] = pack2<T>(v[i][e] * inv, v[i][e + 1] * inv);
         if (w.a.lse && lane == 0) w.a.lse[at] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
+        redo |= l[i] == l[i] && !all_finite(v[i]);
+    }
+    if constexpr (REDO) {
+        if (__any_sync(0xFFFFFFFFu, redo))  // the note says nothing of rows if none are this warp's
+            redo_rows<T, D, RT, KT>(w, mine ? n.b : 0, mine ? n.head / w.group : 0, mine ? n.r0 + r0 : 0,
+                                    mine ? min(n.rows, n.r0 + r0 + ROWS) : 0,
+                                    blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5),
+                                    gridDim.y * (kJoinThreads / 32));
     }
 }
 
@@ -98,10 +215,12 @@ int launch(K kern, dim3 grid, int threads, int smem, cudaStream_t s, const A&...
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }
 
-template <class T, int D, int RT, int ROWS, int PARTS>
+template <class T, int D, int RT, int KT, int ROWS, int PARTS>
 int launch_join(const Work& w, cudaStream_t s) {
     constexpr int R = ROWS * (kJoinThreads / 32);
-    return launch(join_kernel<T, D, RT, R, ROWS, PARTS>, dim3(w.ctas, RT / R), kJoinThreads, 0, s, w);
+    return w.a.max_new > 1
+               ? launch(join_kernel<T, D, RT, KT, R, ROWS, PARTS, true>, dim3(w.ctas, RT / R), kJoinThreads, 0, s, w)
+               : launch(join_kernel<T, D, RT, KT, R, ROWS, PARTS, false>, dim3(w.ctas, RT / R), kJoinThreads, 0, s, w);
 }
 
 }  // namespace

@@ -37,9 +37,13 @@ struct Work {
 // A row tile that ends in a CTA and was begun in another: CTA `from`, slot `slot`.
 struct Note {
     int from, slot;  // from = -1: none
+    int bad;         // a row that the CTA finished alone is not finite, though its sum is a number
+    int b;           // the tile's sequence
     int out_row;     // row of q and out of the tile's first token's first head
     int rows, r0;    // rows of the sequence, first of the tile
     int head;
+    int first_b, first_head, first_tile, first_at;  // the CTA's first step
+    long long steps;
 };
 
 struct Seq {
@@ -65,10 +69,10 @@ __device__ __forceinline__ Seq seq_at(const Work& w, int b) {
     return s;
 }
 
-// The key tiles [lo, hi) that row tile i meets, and the first key that none of
-// its rows sees. A row tile that sees nothing has one (empty) step.
+// The key tiles [lo, hi) that row tile i meets; its rows see the keys begin ..
+// end - 1 and no others. A row tile that sees nothing has one (empty) step.
 struct Span {
-    int lo, hi, end;
+    int lo, hi, begin, end;
 };
 template <int RT, int KT>
 __device__ __forceinline__ Span span_of(const Work& w, const Seq& s, int i) {
@@ -76,8 +80,9 @@ __device__ __forceinline__ Span span_of(const Work& w, const Seq& s, int i) {
     const int first = s.ctx - s.n + r0 / w.group, last = s.ctx - s.n + r1 / w.group;
     Span p;
     p.end = last + 1;
-    if (p.end <= 0) return Span{0, 1, 0};
-    p.lo = w.a.window ? max(0, first - w.a.window + 1) / KT : 0;
+    if (p.end <= 0) return Span{0, 1, 0, 0};
+    p.begin = w.a.window ? max(0, first - w.a.window + 1) : 0;
+    p.lo = p.begin / KT;
     p.hi = (p.end + KT - 1) / KT;
     return p;
 }
@@ -182,6 +187,16 @@ __device__ bool locate(const Work& w, int cta, Cuts* cuts, Place* at, long long*
     return true;
 }
 
+// Leaves where the CTA's steps begin, for whoever walks them again.
+__device__ __forceinline__ void note_start(const Work& w, const Place& at, long long steps) {
+    Note& n = w.notes[blockIdx.x];
+    n.first_b = at.b;
+    n.first_head = at.head;
+    n.first_tile = at.tile;
+    n.first_at = at.at;
+    n.steps = steps;
+}
+
 // Walks the segments of a CTA's steps: for each, a row tile and the key tiles
 // lo .. hi - 1 of it that are this CTA's.
 template <int RT, int KT>
@@ -209,6 +224,7 @@ struct Walk {
         const int from = cuts.holder(start);
         Note& n = w.notes[cta];
         n.slot = cuts(from) < start ? 1 : 0;
+        n.b = p.b;
         n.out_row = s.first * w.a.hq;
         n.rows = s.rows;
         n.r0 = p.tile * rt;
@@ -248,6 +264,11 @@ __device__ __forceinline__ int page_of(const Work& w, int b, int j) {
     if (page >= 0 && page < w.a.num_pages) return page;
     report_error(w.err, DEVERR_INDEX);
     return w.a.num_pages;
+}
+
+// The same for the `rows` keys from j on, of which those before `begin` are not seen.
+__device__ __forceinline__ int page_from(const Work& w, int b, int j, int rows, int begin) {
+    return j + rows <= begin ? w.a.num_pages : page_of(w, b, j);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,

@@ -312,10 +312,11 @@ QG_API int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* 
  * and sees the keys j <= p and, with window > 0, j > p - window:
  *   s_j = scale * (q . k_j), with softcap > 0: softcap * tanh(s_j / softcap)
  *   out = sum_j exp(s_j - lse) v_j,  lse = log sum_j exp(s_j)
- * A row that sees no key gives out = 0 and lse = -infinity. Places past
- * context_len and pages not in the table are never part of a result,
- * whatever they hold (NaN included). Rows of q at or after q_offsets[batch]
- * are left alone.
+ * A row that sees no key gives out = 0 and lse = -infinity. Keys and values
+ * that a row does not see are never part of its result, whatever they hold
+ * (infinities and NaN included), and table entries of pages that no row of
+ * the sequence sees a key of may hold anything. Rows of q at or after
+ * q_offsets[batch] are left alone.
  *  - q: [tokens, q_heads, head_dim] of `dtype` (QG_F16 or QG_BF16, also the
  *    cache's and out's), rows q_stride elements apart (a multiple of 8, q
  *    16-byte aligned); out: the same, dense; lse: f32 [tokens, q_heads] or

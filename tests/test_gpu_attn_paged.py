@@ -242,6 +242,64 @@ def test_a_nan_reaches_its_rows_and_no_others(new):
     assert qg.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("page", [8, 64, 256])
+@pytest.mark.parametrize("window", [1, 60, 129, 300])
+@pytest.mark.parametrize("new", [[1, 1, 1], [7, 1, 12], [150, 2, 129]])
+def test_what_lies_before_every_window_may_be_anything(new, window, page, dtype):
+    """Pages that no new token sees have left the table, and their last places before a window are NaN."""
+    ctx = [700, 1500, 140]
+    args = make(16, new, ctx, 8, 2, 64, page, dtype)
+    good = check(args, window=window)
+    q, k, v, table, off, lens = args
+    for b, (n, c) in enumerate(zip(new, ctx)):
+        begin = max(0, c - n + 1 - window)
+        for i in range(begin // page):
+            table[b, i] = -1 if i % 2 else 1 << 30
+        if begin % page:
+            for x in (k, v):
+                x[int(table[b, begin // page]), :, :begin % page] = float("nan")
+    got = qg.attn_paged(*args, window=window)
+    assert torch.equal(got, good) and qg.device_error() == 0
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("softcap,window", [(0.0, 0), (20.0, 90)])
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("new,ctx", [([5, 1], [300, 300]), ([2, 3, 4] * 30, [200] * 90), ([40, 3], [90, 40]),
+                                     ([150, 1], [150, 700]), ([600, 200, 1], [1000, 200, 3])])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(new, ctx, d, dtype, softcap, window, value):
+    """One value of one key among the new tokens: its column of the rows that see it, and nothing else."""
+    args = make(17, new, ctx, 8, 2, d, 16, dtype)
+    q, k, v, table, off, lens = args
+    kw = dict(scale=d ** -0.5, softcap=softcap, window=window)
+    finite = v.clone()
+    spots = []
+    for b, (n, c) in enumerate(zip(new, ctx)):
+        if n > 1:
+            j = c - n + (2 * n) // 3  # two thirds of the new tokens are before it
+            finite[int(table[b, j // 16]), 1, j % 16, 5] = 0.0
+            v[int(table[b, j // 16]), 1, j % 16, 5] = value
+            spots.append((b, j))
+    ref, mass, rl, S, vm = reference(q, k, finite, *args[3:], d ** -0.5, softcap, window)
+    out, lse = qg.attn_paged(*args, return_lse=True, **kw)
+    sees = torch.zeros(ref.shape, dtype=torch.bool, device="cuda")
+    for b, j in spots:
+        for i in range(new[b]):
+            pos = ctx[b] - new[b] + i
+            if pos >= j and (not window or j > pos - window):
+                sees[int(off[b]) + i, 4:, 5] = True
+    if value != value:
+        assert torch.isnan(out[sees].float()).all()
+    else:
+        assert (out[sees] == value).all()
+    u = UNIT[dtype]
+    tol = (2 * u + 1e-5 * (1 + S)) * mass + 2 * u * ref.abs() + 2.0**-24 * max(ctx) * vm
+    assert ((out.double() - ref).abs() <= tol)[~sees].all()
+    assert ((lse.double() - rl).abs() <= 1e-5 * (1 + S)).all()
+    assert qg.device_error() == 0
+
+
 def test_nothing_to_do_and_refusals():
     q, k, v, table, off, ctx = make(14, [2, 3], [20, 30], 8, 2, 64, 16, torch.bfloat16)
     none = torch.zeros(3, dtype=torch.int32, device="cuda")
