@@ -51,7 +51,8 @@ struct Geo {
     static constexpr int kRingOff = 2 * kTile;
     static constexpr int kBarOff = kRingOff + kStages * kTile;
     static constexpr int kScratchOff = kBarOff + 16 * kStages + 128;
-    static constexpr int kSmem = 1024 + kScratchOff + 256;
+    static constexpr int kStageOff = kScratchOff + 256;  // 4 KB per softmax warp, outputs on their way
+    static constexpr int kSmem = 1024 + kStageOff + 8 * 4096;
     static constexpr uint32_t kO = 256;                // tensor memory: S0, S1, O0, O1
 };
 
@@ -81,6 +82,14 @@ constexpr uint32_t idesc(int n, bool b_rows_are_k) {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void fence_async_proxy() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -139,11 +148,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     Cuts cuts;
     Place place;
+    Seq seq;
     if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1, w.notes[blockIdx.x].bad = 0;
-    if (locate<kRT, kKT, kThreads>(w, blockIdx.x, &cuts, &place, reinterpret_cast<long long*>(smem + G::kScratchOff))) {
+    if (locate<kRT, kKT, kThreads>(w, blockIdx.x, &cuts, &place, &seq, reinterpret_cast<long long*>(smem + G::kScratchOff))) {
         const long long n = cuts(blockIdx.x + 1) - cuts(blockIdx.x);
         if (threadIdx.x == 0) note_start(w, place, n);
-        Walk<kRT, kKT> walk(w, place, n);
+        Walk<kRT, kKT> walk(w, place, seq, n);
         bool ok = true;
         if (warp == 8) {
             // -------------------------------------------------------- producer
@@ -436,25 +446,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
                 const long long at = (long long)(s.first + r / w.group) * w.a.hq + walk.p.head * w.group + r % w.group;
                 const long long pt = ((long long)blockIdx.x * 2 + walk.slot) * kRT + t * 128 + row;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
+                // 128 bytes of each row at a time through shared memory, so that eight
+                // lanes store to one row (16 bytes of 32 rows by each store took
+                // about 1000 cycles per 16 columns).
+                const uint32_t stage = base + G::kStageOff + warp * 4096, mine = stage + lane * 128, swz = lane & 7;
+                const int rows_left = s.rows - (r0 + t * 128 + (warp & 3) * 32);
+                auto leave = [&](char* to, long long stride) {
                     __syncwarp();
-                    tmem_ld16(o_at + c, o);
-                    if (live && walk.whole) {
-                        if (l == l && !all_finite(reinterpret_cast<const float(&)[16]>(o))) w.notes[blockIdx.x].bad = 1;
-                        uint32_t h[8];
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = i * 4 + (lane >> 3), ch = lane & 7;
+                        const long long row_at = stride ? rr * stride : __shfl_sync(0xFFFFFFFFu, at, rr) * (D * 2);
+                        if (rr < rows_left)
+                            *reinterpret_cast<uint4*>(to + row_at + ch * 16) = ld_shared16(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                    }
+                    __syncwarp();
+                };
+                if (walk.whole) {
+                    float finite = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 64) {
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t o[16], h[8];
+                            tmem_ld16(o_at + c + k * 16, o);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            h[e] = pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(w.a.out) + at * D + c);
-                        dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                        dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
-                    } else if (live) {
-                        uint4* dst = reinterpret_cast<uint4*>(w.part + pt * D + c);
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 v = make_float2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                                finite = fmaf(v.x, 0.f, fmaf(v.y, 0.f, finite));
+                                h[e] = pack2<T>(v.x, v.y);
+                            }
+                            st_shared16(mine + ((2 * k ^ swz) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+                            st_shared16(mine + ((2 * k + 1 ^ swz) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+                        }
+                        leave(static_cast<char*>(w.a.out) + c * 2, 0);
+                    }
+                    if (live && l == l && finite != finite) w.notes[blockIdx.x].bad = 1;
+                } else {
+                    const long long part0 = ((long long)blockIdx.x * 2 + walk.slot) * kRT + t * 128 + (warp & 3) * 32;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+#pragma unroll 1
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t o[16];
+                            tmem_ld16(o_at + c + k * 16, o);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                            for (int e = 0; e < 4; ++e)
+                                st_shared16(mine + ((4 * k + e ^ swz) << 4),
+                                            make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                        }
+                        leave(reinterpret_cast<char*>(w.part + part0 * D + c), D * 4);
                     }
                 }
                 tc_fence_before();

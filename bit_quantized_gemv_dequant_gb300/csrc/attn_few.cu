@@ -91,12 +91,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     Cuts cuts;
     Place place;
+    Seq seq;
     if (threadIdx.x == 0) w.notes[blockIdx.x].from = -1, w.notes[blockIdx.x].bad = 0;
-    if (!locate<RT, kKT, kThreads>(w, blockIdx.x, &cuts, &place, reinterpret_cast<long long*>(smem + G::kScratchOff)))
+    if (!locate<RT, kKT, kThreads>(w, blockIdx.x, &cuts, &place, &seq, reinterpret_cast<long long*>(smem + G::kScratchOff)))
         return;
     const long long n = cuts(blockIdx.x + 1) - cuts(blockIdx.x);
     if (threadIdx.x == 0) note_start(w, place, n);
-    Walk<RT, kKT> walk(w, place, n);
+    Walk<RT, kKT> walk(w, place, seq, n);
 
     if (warp == kWarps) {
         // ------------------------------------------------------------ producer

@@ -88,7 +88,8 @@ __device__ __forceinline__ void redo_row(const Work& w, int b, int head, int r) 
 template <class T, int D, int RT, int KT>
 __device__ __noinline__ void redo_rows(const Work& w, int b, int head, int r0, int r1, int warp, int warps) {
     const Note& n = w.notes[blockIdx.x];
-    Walk<RT, KT> walk(w, Place{n.first_b, n.first_head, n.first_tile, n.first_at}, n.bad ? n.steps : 0);
+    Walk<RT, KT> walk(w, Place{n.first_b, n.first_head, n.first_tile, n.first_at},
+                      n.bad ? seq_at(w, n.first_b) : Seq{}, n.bad ? n.steps : 0);
     const int lane = threadIdx.x & 31;
     int at = r0, step = 1;
     __syncwarp();  // the warp wrote r0 .. r1 - 1 itself

@@ -123,12 +123,45 @@ struct Cuts {
     }
 };
 
-// The cuts, and the place of CTA `cta`'s first step, found by the whole block of
-// NT threads: a scan over the sequences, whose counts stay in registers if there
-// are no more than threads, then the head and the tile in the sequence. False
-// if the CTA has no steps. scratch: NT / 32 + 2 long longs of shared memory.
+// The scan of locate for up to 32 sequences, by each warp for itself: no
+// barriers, and the sequence found comes from its lane.
+template <int RT, int KT>
+__device__ __forceinline__ bool locate_few(const Work& w, int cta, Cuts* cuts, Place* at, Seq* s, long long* per,
+                                           long long* left) {
+    const int lane = threadIdx.x & 31;
+    Seq mine{};
+    long long steps = 0;
+    if (lane < w.a.batch) {
+        mine = seq_at(w, lane);
+        steps = steps_of<RT, KT>(w, mine);
+    }
+    const long long v = steps * w.a.hkv;
+    long long x = v;
+#pragma unroll
+    for (int i = 1; i < 32; i *= 2) {
+        const long long o = __shfl_up_sync(0xFFFFFFFFu, x, i);
+        if (lane >= i) x += o;
+    }
+    *cuts = Cuts(__shfl_sync(0xFFFFFFFFu, x, 31), w.ctas);
+    if (cta >= cuts->n) return false;
+    const long long t = (*cuts)(cta);
+    const int b = __ffs(__ballot_sync(0xFFFFFFFFu, t >= x - v && t < x)) - 1;
+    at->b = b;
+    *left = t - __shfl_sync(0xFFFFFFFFu, x - v, b);
+    *per = __shfl_sync(0xFFFFFFFFu, steps, b);
+    s->first = __shfl_sync(0xFFFFFFFFu, mine.first, b);
+    s->n = __shfl_sync(0xFFFFFFFFu, mine.n, b);
+    s->rows = __shfl_sync(0xFFFFFFFFu, mine.rows, b);
+    s->ctx = __shfl_sync(0xFFFFFFFFu, mine.ctx, b);
+    return true;
+}
+
+// The same for any number of sequences, by the whole block of NT threads; their
+// counts stay in registers if there are no more than threads. scratch: NT / 32 + 2
+// long longs of shared memory.
 template <int RT, int KT, int NT>
-__device__ bool locate(const Work& w, int cta, Cuts* cuts, Place* at, long long* scratch) {
+__device__ __forceinline__ bool locate_many(const Work& w, int cta, Cuts* cuts, Place* at, Seq* s, long long* per,
+                                            long long* rem, long long* scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long* found = scratch + NT / 32;
     // Steps of sequence b0 + thread, those of the block's sequences before it,
@@ -170,9 +203,23 @@ __device__ bool locate(const Work& w, int cta, Cuts* cuts, Place* at, long long*
     }
     __syncthreads();
     at->b = (int)found[0];
-    long long left = found[1];
-    const Seq s = seq_at(w, at->b);
-    const long long per = steps_of<RT, KT>(w, s);
+    *rem = found[1];
+    *s = seq_at(w, at->b);
+    *per = steps_of<RT, KT>(w, *s);
+    return true;
+}
+
+// The cuts, and the place of CTA `cta`'s first step: a scan over the sequences,
+// then the head and the tile in the sequence s. False if the CTA has no steps.
+// (A third of a short call's time was this scan; with one token over 700 keys
+// the form for few sequences saves 0.65 us of 8.25.)
+template <int RT, int KT, int NT>
+__device__ __forceinline__ bool locate(const Work& w, int cta, Cuts* cuts, Place* at, Seq* seq, long long* scratch) {
+    long long per = 0, left = 0;
+    if (!(w.a.batch <= 32 ? locate_few<RT, KT>(w, cta, cuts, at, seq, &per, &left)
+                          : locate_many<RT, KT, NT>(w, cta, cuts, at, seq, &per, &left, scratch)))
+        return false;
+    const Seq s = *seq;
     at->head = 0;
     while (left >= per) {  // few heads; a division of 64 bits takes longer
         left -= per;
@@ -211,11 +258,9 @@ struct Walk {
     int slot;         // where its part goes if not
     bool first;
 
-    __device__ Walk(const Work& work, const Place& at, long long n) : w(work), left(n), p(at), first(true) {
-        if (left > 0) {
-            s = seq_at(w, p.b);
-            span = span_of<RT, KT>(w, s, p.tile);
-        }
+    __device__ Walk(const Work& work, const Place& at, const Seq& seq, long long n)
+        : w(work), left(n), p(at), s(seq), first(true) {
+        if (left > 0) span = span_of<RT, KT>(w, s, p.tile);
     }
     // Leaves this segment's note, when it ends a row tile that another CTA began.
     __device__ void note(const Cuts& cuts, int rt, int cta) const {
