@@ -14,6 +14,9 @@ Workspace: calls that need device scratch (split-K partial sums) get it from
 a torch buffer per (device, stream) that grows on demand, unless the caller
 passes one. Calls on different streams therefore never share scratch; calls
 on one stream are ordered by the stream.
+
+A serving operator given a stream runs as under torch.cuda.stream(stream): its
+new outputs belong to that stream.
 """
 from __future__ import annotations
 

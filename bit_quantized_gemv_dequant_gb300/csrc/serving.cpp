@@ -10,6 +10,7 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -18,8 +19,10 @@
 #include <cmath>
 #include <exception>
 #include <map>
+#include <optional>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "qgemv.h"
 
@@ -134,8 +137,10 @@ qg_stream_t stream_of(PyObject* o) {
 
 // The caller's workspace, or a buffer of this (device, stream) that grows on
 // demand: calls on different streams may run at the same time and must not
-// share one. Guarded by the interpreter's lock; never destroyed, as the process
-// may end after CUDA has.
+// share one. A buffer that became too small is kept, because a captured graph may
+// use it; each is twice the one before at least, so all of them together are less
+// than twice the last. Guarded by the interpreter's lock; never destroyed, as the
+// process may end after CUDA has.
 struct Scratch {
     void* p = nullptr;
     size_t n = 0;
@@ -146,10 +151,11 @@ Scratch scratch(size_t need, PyObject* workspace, const Tensor& like, qg_stream_
         return {t.data_ptr(), (size_t)t.nbytes()};
     }
     if (need == 0) return {};
-    static auto* held = new std::map<std::pair<int, qg_stream_t>, Tensor>;
-    Tensor& t = (*held)[{like.get_device(), s}];
-    if (!t.defined() || (size_t)t.numel() < need) t = make({(int64_t)need}, ScalarType::Byte, like);
-    return {t.data_ptr(), (size_t)t.numel()};
+    static auto* held = new std::map<std::pair<int, qg_stream_t>, std::vector<Tensor>>;
+    std::vector<Tensor>& t = (*held)[{like.get_device(), s}];
+    const size_t had = t.empty() ? 0 : (size_t)t.back().numel();
+    if (had < need) t.push_back(make({(int64_t)std::max(need, 2 * had)}, ScalarType::Byte, like));
+    return {t.back().data_ptr(), (size_t)t.back().numel()};
 }
 
 // The library's call, without the interpreter's lock.
@@ -173,7 +179,10 @@ PyObject* tuple(const T&... t) {
     return r;
 }
 
-// A Python function of N arguments, exceptions turned into Python's.
+// A Python function of N arguments, the last one the stream, exceptions turned
+// into Python's. With a stream given the call is as under torch.cuda.stream(it):
+// new outputs and scratch belong to it, so that no work still under way on the
+// current stream has to do with their memory.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != N) {
@@ -181,6 +190,10 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return nullptr;
     }
     try {
+        std::optional<c10::cuda::CUDAStreamGuard> guard;
+        if (N > 1 && a[N - 1] != Py_None)
+            guard.emplace(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream_of(a[N - 1])),
+                                                           c10::cuda::current_device()));
         return F(a);
     } catch (const Raised&) {
         return nullptr;
