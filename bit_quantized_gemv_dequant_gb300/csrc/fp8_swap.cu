@@ -25,7 +25,7 @@ namespace {
 // size the GPU can place at once (plan() below). Measured, product alone:
 //   N = K = 4096, M = 1         6.3 us  2.7 TB/s of w (launch, first loads, joining)
 //   N = 2200, K = 5200, M = 33  6.8 us  1.7 TB/s
-//   N = 12288, K = 4096, M = 1  10.6 us 4.7 TB/s; M = 64 12.7 us
+//   N = K = 12288, M = 1        28.0 us 5.4 TB/s (96 SMs load)
 //
 // The split's partial sums meet in shared memory over the cluster, each CTA
 // adding up its share of the rows of a in the order of the split: the result
@@ -294,32 +294,29 @@ int cluster_room(const DevCtx& dc, const int** room) {
     return error[dc.device] == cudaSuccess ? QG_OK : cuda_fail(error[dc.device]);
 }
 
-// The tiles, and the split of K with the shortest chain of k blocks one after the
-// other: rounds of clusters that run at once, times the k blocks of a CTA and
-// what a round costs besides (start, first loads, joining: about five blocks).
-// N = 12288, K = 4096 is 96 tiles: split in 3, two rounds of 11 blocks keep all SMs
-// loading, one round of 32 only 96 of them (M = 64: 12.7 us and 15.3). Powers of
-// two alone took 7.7 us at N = 2200, K = 5200, M = 33, split in 4.
-constexpr long long kRound = 5;
+// The tiles, and the largest split of K whose clusters all run at once with two
+// k blocks per CTA at least; no split if the tiles fill more than half of the GPU.
+// A second round costs more than a longer first one: N = K = 12288, M = 1, 96
+// tiles: 28.0 us without a split, 36 to 50 with any (76 clusters of 2 run at
+// once, 46 of 3, 36 of 4, 23 of 6, 15 of 8); N = K = 8192, 64 tiles: 14.4 us split
+// in 2, 17.0 without and 17.8 in 4; N = 2200, K = 5200, 18 tiles: 5.65 us split in
+// 6, 5.9 in 4, 9.6 in 8.
 struct Plan {
-    long long nt, mt, kb, cost;
+    long long nt, mt, kb;
     int split;
+    long long rounds;
 };
 template <int BN, class TY>
 int plan(const DevCtx& dc, const Fp8Args& a, Plan* p) {
     const int* room = nullptr;
     const int rc = cluster_room<BN, TY>(dc, &room);
     if (rc) return rc;
-    *p = Plan{(a.N + 127) / 128, (a.M + BN - 1) / BN, (a.K + 127) / 128, 0, 0};
-    for (int i = 1; i < 9 && (i == 1 || p->kb >= 2 * i); ++i) {
-        if (room[i] < 1) continue;
-        const long long cost = (p->nt * p->mt + room[i] - 1) / room[i] * ((p->kb + i - 1) / i + kRound);
-        if (p->split == 0 || cost < p->cost) {
-            p->cost = cost;
-            p->split = i;
-        }
-    }
-    return p->split ? QG_OK : QG_ERR_UNSUPPORTED;
+    *p = Plan{(a.N + 127) / 128, (a.M + BN - 1) / BN, (a.K + 127) / 128, 1, 1};
+    for (int i = 2; i < 9 && p->kb >= 2 * i; ++i)
+        if (p->nt * p->mt <= room[i]) p->split = i;
+    if (room[p->split] < 1) return QG_ERR_UNSUPPORTED;
+    p->rounds = (p->nt * p->mt + room[p->split] - 1) / room[p->split];
+    return QG_OK;
 }
 
 template <int BN, class TY>
@@ -373,7 +370,7 @@ bool swap_is_shorter(const DevCtx& dc, const Fp8Args& a) {
     Plan p;
     if (plan<128, float>(dc, a, &p) != QG_OK) return false;
     const long long tiles = 2 * ((a.M + 255) / 256) * ((a.N + 255) / 256);  // per SM
-    return p.cost <= (tiles + dc.num_sms - 1) / dc.num_sms * (p.kb + kRound);
+    return p.rounds * ((p.kb + p.split - 1) / p.split) <= (tiles + dc.num_sms - 1) / dc.num_sms * p.kb;
 }
 
 int code_map(CUtensorMap* m, const uint8_t* ptr, long long rows, long long cols, int box_rows) {
