@@ -37,7 +37,13 @@ using fp8::tmem_wait32;
 //                   last scores of this one are there
 //   warp 8          TMA producer: ring of K and V tiles, taken alternately
 //   warp 9          MMA issuer
-// Ten warps leave 200 registers per thread: a row's 128 scores stay in them.
+// Ten warps are three to some of the schedulers, which leaves 168 registers per
+// thread: a row's 128 scores stay in them.
+//
+// With the joining kernel: 2 x 2048 new tokens over 16384 and 8200 keys, 32/8
+// heads of 128, bf16: 554 us, 1.37 PFLOP/s, at the power limit; tensor pipes 52 %
+// busy. 13 sequences of up to 130 new tokens, 20/4 heads of 64, capped, windowed:
+// 44 us, latency from end to end (4 or 5 steps per CTA).
 constexpr int kKT = 128;
 constexpr int kRT = 256;
 constexpr int kThreads = 320;

@@ -34,6 +34,9 @@ namespace {
 // statistics is the work of one more warp while the others read the next row
 // (done by all warps between two rows it took 55 us of 159 for 2048 rows of
 // 131072 bf16 logits with the 5 largest).
+//
+// 2048 x 131072 bf16, 5 largest: 120 us, 4.5 TB/s, two thirds of all issue slots
+// taken. One row of 50021 f32, 20 largest: 11.0 us, the latency of the finish.
 constexpr int kThreads = 256;               // that read logits; a producer and a finishing warp more
 constexpr int kWarps = kThreads / 32;
 constexpr int kTop = 32;                    // most alternatives
