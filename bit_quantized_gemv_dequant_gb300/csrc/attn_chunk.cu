@@ -43,7 +43,7 @@ using fp8::tmem_wait32;
 // With the joining kernel: 2 x 2048 new tokens over 16384 and 8200 keys, 32/8
 // heads of 128, bf16: 554 us, 1.37 PFLOP/s, at the power limit; tensor pipes 52 %
 // busy. 13 sequences of up to 130 new tokens, 20/4 heads of 64, capped, windowed:
-// 44 us, latency from end to end (4 or 5 steps per CTA).
+// 43 us, latency from end to end (4 or 5 steps per CTA).
 constexpr int kKT = 128;
 constexpr int kRT = 256;
 constexpr int kThreads = 320;
@@ -375,15 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_ld32_async(s_at + 96, x[3]);
                             }
                         }
-                        if constexpr (MODE != kPositive) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float2 v = score2<MODE == kCapped>(
-                                    w, make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
-                                x[c][e] = __float_as_uint(v.x);
-                                x[c][e + 1] = __float_as_uint(v.y);
-                            }
-                        }
+                        if constexpr (MODE != kPositive)
+                            scores<MODE == kCapped, 32>(w, [&](int e) { return __uint_as_float(x[c][e]); },
+                                                        [&](int e, float v) { x[c][e] = __float_as_uint(v); });
                         if (masked) {
                             const int hi = pos - j0 - c * 32;                                // last key seen
                             const int lo = w.a.window ? pos - w.a.window - j0 - c * 32 : -1;  // first key seen - 1

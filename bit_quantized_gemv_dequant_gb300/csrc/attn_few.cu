@@ -199,14 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma<T>(x[2 * nb + 1], q[k], b[2], b[3]);
                 }
             }
-#pragma unroll
-            for (int nt = 0; nt < KW / 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const float2 v = score2<CAP>(w, make_float2(x[nt][e], x[nt][e + 1]));
-                    x[nt][e] = v.x;
-                    x[nt][e + 1] = v.y;
-                }
+            scores<CAP, KW / 2>(w, [&](int e) { return x[e / 4][e % 4]; }, [&](int e, float v) { x[e / 4][e % 4] = v; });
             const bool masked = j0 + KW - 1 > pos_lo || (w.a.window && j0 <= pos_hi - w.a.window);
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll

@@ -1,5 +1,6 @@
 // attn_paged: which kernel takes which sequences, and the workspace.
 #include <algorithm>
+#include <cmath>
 
 #include "attn_work.cuh"
 
@@ -35,7 +36,8 @@ int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, cudaStream_t s) {
     w.group = a.hq / a.hkv;
     w.scale_log2 = a.scale * kLog2e;
     if (a.softcap > 0.f) {
-        w.cap_in = 2.f * kLog2e * a.scale / a.softcap;
+        w.cap_in = a.scale / a.softcap;
+        w.small = 0.5f / std::fabs(w.cap_in);
         w.cap_out = a.softcap * kLog2e;
     }
     w.err = dc.err;

@@ -25,8 +25,9 @@ using prefill::prefetch_tmap;
 struct Work {
     AttnArgs a;
     int group;
-    float scale_log2;        // scale * log2(e); without a cap scores go straight to base 2
-    float cap_in, cap_out;   // 2 log2(e) scale / softcap, softcap * log2(e)
+    float scale_log2;        // scale * log2(e): scores are in base 2
+    float small;             // products up to this in size are far from the cap
+    float cap_in, cap_out;   // scale / softcap, softcap * log2(e)
     float* part;             // [G][2][RT][D] unnormalised outputs of cut row tiles
     float2* ml;              // [G][2][RT] their maximum (base 2) and sum
     struct Note* notes;      // [G]
@@ -331,17 +332,71 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Scores of two dot products, in base 2. With a cap, softcap * tanh(scale x /
-// softcap) where tanh(z) = 1 - 2 / (1 + e^2z), whose absolute error is a few
-// 2^-24; an infinite e^2z gives the cap.
+__device__ __forceinline__ float within(float x, float most) {  // NaN stays NaN
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(most));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(-most));
+    return r;
+}
+
+// Scores of two dot products, in base 2. With a cap, softcap * tanh(z), z = scale x /
+// softcap, as z P(z^2) / Q(z^2): P and Q of degree 4 with the least largest
+// relative error for |z| up to 8.5 (1.2e-8, by least squares weighted anew until
+// the errors are level), where tanh is 1 within 2^-23; in f32 within 5 units of 2^-24
+// of the score itself. (1 - 2 / (1 + e^2z) is off by 2^-23 of the cap, which small
+// scores feel.)
 template <bool CAP>
 __device__ __forceinline__ float2 score2(const Work& w, float2 x) {
     if (!CAP) return __fmul2_rn(x, make_float2(w.scale_log2, w.scale_log2));
-    float2 e = __fmul2_rn(x, make_float2(w.cap_in, w.cap_in));
-    e = __fadd2_rn(make_float2(ex2(e.x), ex2(e.y)), make_float2(1.f, 1.f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
-    return __ffma2_rn(e, make_float2(-2.f * w.cap_out, -2.f * w.cap_out), make_float2(w.cap_out, w.cap_out));
+    auto two = [](float v) { return make_float2(v, v); };
+    x = __fmul2_rn(x, two(w.cap_in));
+    const float2 z = make_float2(within(x.x, 8.5f), within(x.y, 8.5f)), s = __fmul2_rn(z, z);
+    float2 p = two(1.4268720427e-8f), q = two(8.1449280742e-7f);
+    p = __ffma2_rn(p, s, two(2.1250718418e-5f));
+    q = __ffma2_rn(q, s, two(3.3488337938e-4f));
+    p = __ffma2_rn(p, s, two(3.5340089817e-3f));
+    q = __ffma2_rn(q, s, two(2.6022685692e-2f));
+    p = __ffma2_rn(p, s, two(0.13413232565f));
+    q = __ffma2_rn(q, s, two(0.46746554971f));
+    p = __ffma2_rn(p, s, two(1.f));
+    q = __ffma2_rn(q, s, two(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(q.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(q.y));
+    return __fmul2_rn(__fmul2_rn(__fmul2_rn(z, two(w.cap_out)), p), q);
+}
+
+// N scores of each lane of a warp, get(i) and put(i, score). As long as no |z| is
+// over a half, as is the rule (caps are there for the odd large score), tanh is
+// z (1 + z^2 R(z^2)) with R of degree 3, fitted like P and Q to 1.5e-8.
+// 13 sequences of up to 130 tokens: 43.0 us, and 48.6 with the quotient alone.
+template <bool CAP, int N, class Get, class Put>
+__device__ __forceinline__ void scores(const Work& w, const Get& get, const Put& put) {
+    auto two = [](float v) { return make_float2(v, v); };
+    if constexpr (CAP) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) top = fmaxf(fmaxf(top, fabsf(get(i))), fabsf(get(i + 1)));
+        if (!__any_sync(0xFFFFFFFFu, top > w.small)) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float2 x = make_float2(get(i), get(i + 1));
+                const float2 z = __fmul2_rn(x, two(w.cap_in)), s = __fmul2_rn(z, z), y = __fmul2_rn(x, two(w.scale_log2));
+                float2 r = __ffma2_rn(two(1.7241498455e-2f), s, two(-5.3045496345e-2f));
+                r = __ffma2_rn(r, s, two(0.13325878978f));
+                r = __ffma2_rn(r, s, two(-0.33333143592f));
+                r = __ffma2_rn(__fmul2_rn(r, s), y, y);
+                put(i, r.x);
+                put(i + 1, r.y);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 v = score2<CAP>(w, make_float2(get(i), get(i + 1)));
+        put(i, v.x);
+        put(i + 1, v.y);
+    }
 }
 
 // Up to 16 * row_blocks rows per sequence and key head (row_blocks 1, 2, 4).
