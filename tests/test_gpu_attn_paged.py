@@ -300,6 +300,46 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them(new, ctx, d, dt
     assert qg.device_error() == 0
 
 
+@pytest.mark.parametrize("softcap", [0.5, 30.0, 1000.0])
+@pytest.mark.parametrize("scale", [0.125, -1.0])
+@pytest.mark.parametrize("new", [1, 600])
+def test_capped_scores_are_as_exact_as_their_size(new, scale, softcap):
+    """With a window of one key the log sum is the score itself: products from 2^-24 to 2^14, exact in f32, of either
+    sign. tanh is good to 5 units of 2^-24, and seven roundings (two constants, the products, the change of base) come
+    on top: 12 units of the score."""
+    n = 1200
+    g = torch.Generator("cuda").manual_seed(18)
+    sizes = torch.arange(n, device="cuda") % 38 - 24
+    a = torch.ldexp(torch.randint(64, 128, (n,), generator=g, device="cuda") / 64.0, sizes // 2)
+    b = torch.ldexp(torch.randint(64, 128, (n,), generator=g, device="cuda") / 64.0, sizes - sizes // 2)
+    b = torch.where(torch.arange(n, device="cuda") % 3 == 0, -b, b)
+    q = torch.zeros(n, 1, 64, dtype=torch.float16, device="cuda")
+    k = torch.zeros(n // 16, 1, 16, 64, dtype=torch.float16, device="cuda")
+    q[:, 0, 7] = a.half()
+    k.view(n, 64)[:, 7] = b.half()
+    assert torch.equal(q[:, 0, 7].double(), a.double()) and torch.equal(k.view(n, 64)[:, 7].double(), b.double())
+    v = torch.randn(n // 16, 1, 16, 64, generator=g, device="cuda").half()
+    pages = torch.arange(n // 16, dtype=torch.int32, device="cuda")
+    if new == 1:  # n sequences of one token, whose windows end at keys 0, 1, 2 ...
+        args = (q, k, v, pages.expand(n, -1).contiguous(), torch.arange(n + 1, dtype=torch.int32, device="cuda"),
+                torch.arange(1, n + 1, dtype=torch.int32, device="cuda"))
+    else:
+        # two sequences of 600 tokens, 37 and a half pages each
+        k2, v2 = (x.view(n, 64)[new:] for x in (k, v))
+        fill = torch.zeros(8, 64, dtype=torch.float16, device="cuda")
+        k = torch.cat([k.view(n, 64)[:new], fill, k2, fill]).view(-1, 1, 16, 64)
+        v = torch.cat([v.view(n, 64)[:new], fill, v2, fill]).view(-1, 1, 16, 64)
+        args = (q, k, v, torch.arange(76, dtype=torch.int32, device="cuda").view(2, 38),
+                torch.tensor([0, new, n], dtype=torch.int32, device="cuda"),
+                torch.tensor([new, n - new], dtype=torch.int32, device="cuda"))
+    out, lse = qg.attn_paged(*args, max_new=new, scale=scale, softcap=softcap, window=1, return_lse=True)
+    want = softcap * torch.tanh(scale * a.double() * b.double() / softcap)
+    assert ((lse[:, 0].double() - want).abs() <= 12 * 2.0**-24 * want.abs()).all()
+    rows = v.view(-1, 64)
+    assert torch.equal(out.view(n, 64), rows if new == 1 else torch.cat([rows[:new], rows[608:608 + n - new]]))
+    assert qg.device_error() == 0
+
+
 def test_nothing_to_do_and_refusals():
     q, k, v, table, off, ctx = make(14, [2, 3], [20, 30], 8, 2, 64, 16, torch.bfloat16)
     none = torch.zeros(3, dtype=torch.int32, device="cuda")
