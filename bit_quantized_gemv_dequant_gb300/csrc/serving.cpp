@@ -158,13 +158,28 @@ Scratch scratch(size_t need, PyObject* workspace, const Tensor& like, qg_stream_
     return {t.back().data_ptr(), (size_t)t.back().numel()};
 }
 
-// The library's call, without the interpreter's lock.
+// The interpreter's lock is released while one of these lives, and taken again
+// however its scope is left.
+class Unlocked {
+  public:
+    Unlocked() : state_(PyEval_SaveThread()) {}
+    ~Unlocked() { PyEval_RestoreThread(state_); }
+    Unlocked(const Unlocked&) = delete;
+    Unlocked& operator=(const Unlocked&) = delete;
+
+  private:
+    PyThreadState* state_;
+};
+
+// The library's call, without the interpreter's lock. f may throw: it asks
+// tensors for their data, which those under a transform do not give.
 template <class F>
 void call(const char* what, F&& f) {
     int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = f();
-    Py_END_ALLOW_THREADS
+    {
+        const Unlocked unlocked;
+        status = f();
+    }
     check(status, what);
 }
 
