@@ -19,6 +19,7 @@
 #include <cmath>
 #include <exception>
 #include <map>
+#include <mutex>
 #include <optional>
 #include <string>
 #include <utility>
@@ -137,13 +138,20 @@ qg_stream_t stream_of(PyObject* o) {
 
 // The caller's workspace, or a buffer of this (device, stream) that grows on
 // demand: calls on different streams may run at the same time and must not
-// share one. A buffer that became too small is kept, because a captured graph may
+// share one. On one stream the kernels of a call that pass data through it must
+// not have another call's between them, hence a mutex for each, held while a call
+// enqueues. A buffer that became too small is kept, because a captured graph may
 // use it; each is twice the one before at least, so all of them together are less
-// than twice the last. Guarded by the interpreter's lock; never destroyed, as the
-// process may end after CUDA has.
+// than twice the last. The map is guarded by the interpreter's lock; never
+// destroyed, as the process may end after CUDA has.
+struct Held {
+    std::vector<Tensor> buffers;
+    std::mutex enqueue;
+};
 struct Scratch {
     void* p = nullptr;
     size_t n = 0;
+    std::mutex* enqueue = nullptr;
 };
 Scratch scratch(size_t need, PyObject* workspace, const Tensor& like, qg_stream_t s) {
     if (workspace != Py_None) {
@@ -151,11 +159,12 @@ Scratch scratch(size_t need, PyObject* workspace, const Tensor& like, qg_stream_
         return {t.data_ptr(), (size_t)t.nbytes()};
     }
     if (need == 0) return {};
-    static auto* held = new std::map<std::pair<int, qg_stream_t>, std::vector<Tensor>>;
-    std::vector<Tensor>& t = (*held)[{like.get_device(), s}];
+    static auto* held = new std::map<std::pair<int, qg_stream_t>, Held>;
+    Held& h = (*held)[{like.get_device(), s}];
+    std::vector<Tensor>& t = h.buffers;
     const size_t had = t.empty() ? 0 : (size_t)t.back().numel();
     if (had < need) t.push_back(make({(int64_t)std::max(need, 2 * had)}, ScalarType::Byte, like));
-    return {t.back().data_ptr(), (size_t)t.back().numel()};
+    return {t.back().data_ptr(), (size_t)t.back().numel(), &h.enqueue};
 }
 
 // The interpreter's lock is released while one of these lives, and taken again
@@ -171,16 +180,23 @@ class Unlocked {
     PyThreadState* state_;
 };
 
-// The library's call, without the interpreter's lock. f may throw: it asks
-// tensors for their data, which those under a transform do not give.
+// The library's call, without the interpreter's lock but with the scratch's. f
+// may throw: it asks tensors for their data, which those under a transform do not
+// give.
 template <class F>
-void call(const char* what, F&& f) {
+void call(const char* what, std::mutex* enqueue, F&& f) {
     int status;
     {
         const Unlocked unlocked;
+        std::unique_lock<std::mutex> alone;
+        if (enqueue) alone = std::unique_lock<std::mutex>(*enqueue);
         status = f();
     }
     check(status, what);
+}
+template <class F>
+void call(const char* what, F&& f) {
+    call(what, nullptr, std::forward<F>(f));
 }
 
 PyObject* wrap(const Tensor& t) { return THPVariable_Wrap(t); }
@@ -264,7 +280,7 @@ PyObject* qmm_fp8_b128(PyObject* const* a) {
     const uintptr_t odd = (uintptr_t)K | (uintptr_t)x.data_ptr() | (uintptr_t)w.data_ptr();
     if (odd & 15) check(qmm_fp8_b128_workspace_size(M, N, K, &need), "qmm_fp8_b128");
     const Scratch ws = scratch(need, a[6], x, s);
-    call("qmm_fp8_b128", [&] {
+    call("qmm_fp8_b128", ws.enqueue, [&] {
         return ::qmm_fp8_b128(at_of<uint8_t>(x), at_of<float>(sx), at_of<uint8_t>(w), at_of<float>(sw), y.data_ptr(), type,
                               M, N, K, ws.p, ws.n, s);
     });
@@ -308,7 +324,7 @@ PyObject* attn_paged(PyObject* const* a) {
     size_t need = 0;
     check(attn_paged_workspace_size(T, B, max_new, Hq, Hkv, D, &need), "attn_paged");
     const Scratch ws = scratch(need, a[13], q, s);
-    call("attn_paged", [&] {
+    call("attn_paged", ws.enqueue, [&] {
         return ::attn_paged(q.data_ptr(), stride, k.data_ptr(), v.data_ptr(), at_of<int32_t>(table), at_of<int32_t>(offsets),
                             at_of<int32_t>(lens), out.data_ptr(), lse.defined() ? at_of<float>(lse) : nullptr, dtype, T, B,
                             max_new, Hq, Hkv, D, pages, page, table.size(1), scale, softcap, window, ws.p, ws.n, s);
@@ -382,7 +398,7 @@ PyObject* kv_fork(PyObject* const* a) {
     size_t need = 0;
     check(kv_fork_workspace_size(n, &need), "kv_fork");
     const Scratch ws = scratch(need, a[6], table, s);
-    call("kv_fork", [&] {
+    call("kv_fork", ws.enqueue, [&] {
         return ::kv_fork(p.cache, p.planes, p.pages, p.bytes, page_size, at_of<int32_t>(table), at_of<int32_t>(lens),
                          at_of<int32_t>(refs), R, W, at_of<int32_t>(parents), n, at_of<int32_t>(ct), at_of<int32_t>(cl),
                          at_of<int32_t>(nr), ws.p, ws.n, s);
@@ -425,7 +441,7 @@ PyObject* kv_compact(PyObject* const* a) {
     size_t need = 0;
     check(kv_compact_workspace_size(p.pages, &need), "kv_compact");
     const Scratch ws = scratch(need, a[3], table, s);
-    call("kv_compact", [&] {
+    call("kv_compact", ws.enqueue, [&] {
         return ::kv_compact(p.cache, p.planes, p.pages, p.bytes, at_of<int32_t>(table), R, W, at_of<int32_t>(refs),
                             at_of<int32_t>(nt), at_of<int32_t>(nr), at_of<int32_t>(map), at_of<int32_t>(live), ws.p, ws.n, s);
     });

@@ -1,10 +1,14 @@
 """The serving operators' calls as a program makes them: under transforms, from several threads, in several graphs and
 among calls that overlap."""
+import concurrent.futures
 import os
 import subprocess
 import sys
 
 import pytest
+import torch
+
+import bit_quantized_gemv_dequant_gb300 as qg
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +31,67 @@ assert (codes.float() == 448).all() and qg.device_error() == 0
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.split() == ["raised", "raised"], (r.returncode, r.stdout, r.stderr[-2000:])
+
+
+def attention(seed, lens=(900, 70, 1300), new=(1, 1, 1)):
+    """A call's arguments: sequences that several CTAs share, so that parts meet in the scratch."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    counts = [-(-n // 16) for n in lens]
+    pages = sum(counts)
+    order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(lens), max(counts)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(counts):
+        table[b, :n] = order[at:at + n]
+        at += n
+    k, v = (torch.randn(pages, 2, 16, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(sum(new), 8, 64, generator=g, device="cuda").bfloat16()
+    offsets = torch.tensor([0] + list(new), device="cuda").cumsum(0).to(torch.int32)
+    return q, k, v, table, offsets, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def in_threads(work, n):
+    """[work(0), ... work(n - 1)], each by a thread of its own; an exception in one is raised here."""
+    with concurrent.futures.ThreadPoolExecutor(n) as pool:
+        return [f.result() for f in [pool.submit(work, i) for i in range(n)]]
+
+
+class Fork:
+    """A cache of four planes with five rows of 40 tokens, and a fork of them."""
+
+    def __init__(self, seed, children):
+        g = torch.Generator("cuda").manual_seed(seed)
+        self.cache = torch.randint(-999, 999, (4, 64, 16, 8), generator=g, device="cuda", dtype=torch.int32)
+        order = torch.randperm(64, generator=g, device="cuda").to(torch.int32)
+        self.table = order[:15].view(5, 3).contiguous()
+        self.refs = torch.zeros(64, dtype=torch.int32, device="cuda")
+        self.refs[self.table.flatten().long()] = 1
+        self.lens = torch.full((5,), 40, dtype=torch.int32, device="cuda")
+        self.parents = torch.randint(0, 5, (children,), generator=g, device="cuda").to(torch.int32)
+
+    def __call__(self):
+        return qg.kv_fork(self.cache, self.table, self.lens, self.refs, self.parents, 16)
+
+    def right(self, out):
+        """Each child's last page is a copy of its parent's."""
+        table, lens, _ = out
+        fresh, old = table[:, 2].long(), self.table[self.parents.long(), 2].long()
+        return bool((lens == 40).all()) and torch.equal(self.cache[:, fresh], self.cache[:, old])
+
+
+def test_two_threads_on_one_stream():
+    """Each call's two kernels pass data through the stream's scratch: no other thread's come between them."""
+    args = [attention(1), attention(2, (40, 1500, 300), (30, 1, 50))]
+    want = [qg.attn_paged(*a) for a in args]
+    forks = [Fork(3, 7), Fork(4, 11)]
+
+    def work(i):
+        torch.cuda.synchronize()
+        wrong = 0
+        for _ in range(200):
+            wrong += not torch.equal(qg.attn_paged(*args[i]), want[i])
+            forks[i].cache[:, :, :] = forks[i].cache.flip(0)  # other contents every time
+            wrong += not forks[i].right(forks[i]())
+        return wrong
+
+    assert in_threads(work, 2) == [0, 0] and qg.device_error() == 0
