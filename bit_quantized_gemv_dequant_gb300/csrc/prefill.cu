@@ -615,6 +615,16 @@ int encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
     });
     if (g_encode_rc != cudaSuccess) return cuda_fail(g_encode_rc);
     if (!g_encode) return QG_ERR_UNSUPPORTED;
+    // It refuses a thread without a current context, which one that has made no
+    // call on the device yet does not have: asking for a limit makes the device's
+    // current.
+    thread_local bool bound = false;
+    if (!bound) {
+        size_t unused = 0;
+        const cudaError_t e = cudaDeviceGetLimit(&unused, cudaLimitStackSize);
+        if (e != cudaSuccess) return cuda_fail(e);
+        bound = true;
+    }
     *out = g_encode;
     return QG_OK;
 }

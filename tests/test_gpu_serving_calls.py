@@ -95,3 +95,16 @@ def test_two_threads_on_one_stream():
         return wrong
 
     assert in_threads(work, 2) == [0, 0] and qg.device_error() == 0
+
+
+def test_first_call_of_a_thread():
+    """A thread that has done nothing on the device before."""
+    one, chunk = attention(5), attention(6, (400, 90), (200, 20))
+    codes = [torch.randn(m, 512, device="cuda").to(torch.float8_e4m3fn) for m in (3, 700, 300)]
+    scales = [torch.ones(m, 4, device="cuda") for m in (3, 700, 3)]
+    calls = [lambda: qg.attn_paged(*one, max_new=1), lambda: qg.attn_paged(*chunk)]
+    calls += [lambda i=i: qg.qmm_fp8_b128(codes[i], scales[i], codes[2], scales[2]) for i in range(2)]
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        assert torch.equal(in_threads(lambda i: call(), 1)[0], want)
