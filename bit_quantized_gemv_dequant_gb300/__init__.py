@@ -13,7 +13,9 @@ present: there is no CPU fallback.
 Workspace: calls that need device scratch (split-K partial sums) get it from
 a torch buffer per (device, stream) that grows on demand, unless the caller
 passes one. Calls on different streams therefore never share scratch; calls
-on one stream are ordered by the stream.
+on one stream are ordered by the stream. A call that torch.cuda.graph captures
+takes its scratch from the graph's own memory, so that graphs may run beside
+each other; under another kind of capture the caller passes a workspace.
 
 A serving operator given a stream runs as under torch.cuda.stream(stream): its
 new outputs belong to that stream.
@@ -182,6 +184,10 @@ def _scratch(need, device, workspace, stream):
         return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
     if need == 0:
         return None, 0
+    if torch.cuda.is_current_stream_capturing():
+        # The graph may run on any stream, beside other graphs: scratch of its own.
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        return buf.data_ptr(), need
     # One buffer per (device, stream): two calls on different streams may run
     # at the same time and must not share split-K scratch.
     key = (device.index, stream)

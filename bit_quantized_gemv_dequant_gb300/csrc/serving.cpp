@@ -23,7 +23,6 @@
 #include <optional>
 #include <string>
 #include <utility>
-#include <vector>
 
 #include "qgemv.h"
 
@@ -140,15 +139,16 @@ qg_stream_t stream_of(PyObject* o) {
 // demand: calls on different streams may run at the same time and must not
 // share one. On one stream the kernels of a call that pass data through it must
 // not have another call's between them, hence a mutex for each, held while a call
-// enqueues. A buffer that became too small is kept, because a captured graph may
-// use it; each is twice the one before at least, so all of them together are less
-// than twice the last. The map is guarded by the interpreter's lock; never
-// destroyed, as the process may end after CUDA has.
+// enqueues. A call that is being captured gets a buffer of its own, from the
+// graph's memory: the graph may run on any stream, beside other graphs. The map
+// is guarded by the interpreter's lock; never destroyed, as the process may end
+// after CUDA has.
 struct Held {
-    std::vector<Tensor> buffers;
+    Tensor buffer;
     std::mutex enqueue;
 };
 struct Scratch {
+    Tensor owner;  // another thread may grow the buffer before this call is enqueued
     void* p = nullptr;
     size_t n = 0;
     std::mutex* enqueue = nullptr;
@@ -156,15 +156,20 @@ struct Scratch {
 Scratch scratch(size_t need, PyObject* workspace, const Tensor& like, qg_stream_t s) {
     if (workspace != Py_None) {
         const Tensor& t = dense(workspace, "workspace");
-        return {t.data_ptr(), (size_t)t.nbytes()};
+        return {t, t.data_ptr(), (size_t)t.nbytes()};
     }
     if (need == 0) return {};
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    // (the legacy stream answers with an error while another stream is captured)
+    if (cudaStreamIsCapturing(reinterpret_cast<cudaStream_t>(s), &status) != cudaSuccess) (void)cudaGetLastError();
+    if (status != cudaStreamCaptureStatusNone) {
+        const Tensor t = make({(int64_t)need}, ScalarType::Byte, like);
+        return {t, t.data_ptr(), need};
+    }
     static auto* held = new std::map<std::pair<int, qg_stream_t>, Held>;
     Held& h = (*held)[{like.get_device(), s}];
-    std::vector<Tensor>& t = h.buffers;
-    const size_t had = t.empty() ? 0 : (size_t)t.back().numel();
-    if (had < need) t.push_back(make({(int64_t)std::max(need, 2 * had)}, ScalarType::Byte, like));
-    return {t.back().data_ptr(), (size_t)t.back().numel(), &h.enqueue};
+    if (!h.buffer.defined() || (size_t)h.buffer.numel() < need) h.buffer = make({(int64_t)need}, ScalarType::Byte, like);
+    return {h.buffer, h.buffer.data_ptr(), (size_t)h.buffer.numel(), &h.enqueue};
 }
 
 // The interpreter's lock is released while one of these lives, and taken again

@@ -108,3 +108,40 @@ def test_first_call_of_a_thread():
         want = call()
         torch.cuda.synchronize()
         assert torch.equal(in_threads(lambda i: call(), 1)[0], want)
+
+
+def captured(call):
+    """A graph of 20 calls, captured on the stream that torch.cuda.graph takes by default, and the last one's result."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(20):
+            out = call()
+    return graph, out
+
+
+def test_graphs_beside_each_other():
+    """Two graphs replayed at the same time on two streams, with eager calls on a third."""
+    args = [attention(7), attention(8, (40, 1500, 300), (30, 1, 50)), attention(9, (800, 600), (1, 1))]
+    want = [qg.attn_paged(*a) for a in args]
+    forks = [Fork(10, 7), Fork(11, 11)]
+    made = [captured(lambda a=a: qg.attn_paged(*a)) for a in args[:2]]
+    made_forks = [captured(f) for f in forks]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for (_, out), f in zip(made, forks):
+            out.zero_()
+            f.cache.copy_(f.cache.flip(0))
+        torch.cuda.synchronize()
+        for s, (graph, _), (fork, _) in zip(streams, made, made_forks):
+            with torch.cuda.stream(s):
+                graph.replay()
+                fork.replay()
+        eager = [qg.attn_paged(*args[2]) for _ in range(10)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, w) for (_, out), w in zip(made, want))
+        assert all(torch.equal(out, want[2]) for out in eager)
+        assert all(f.right(out) for f, (_, out) in zip(forks, made_forks))
+    assert qg.device_error() == 0
