@@ -29,7 +29,7 @@ template <class T, int D>
 __device__ __forceinline__ void redo_row(const Work& w, int b, int head, int r) {
     const Seq s = seq_at(w, b);
     const int lane = threadIdx.x & 31, tok = r / w.group, pos = s.ctx - s.n + tok;
-    const int h = head * w.group + r % w.group, from = w.a.window ? max(0, pos - w.a.window + 1) : 0;
+    const int h = head * w.group + r % w.group, from = w.a.window && pos >= w.a.window ? pos - w.a.window + 1 : 0;
     const T* q = static_cast<const T*>(w.a.q) + (long long)(s.first + tok) * w.a.q_stride + (long long)h * D;
     constexpr int E = D / 32;
     float m = -INFINITY, l = 0.f, acc[E] = {};

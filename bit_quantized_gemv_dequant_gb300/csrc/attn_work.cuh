@@ -82,7 +82,7 @@ __device__ __forceinline__ Span span_of(const Work& w, const Seq& s, int i) {
     Span p;
     p.end = last + 1;
     if (p.end <= 0) return Span{0, 1, 0, 0};
-    p.begin = w.a.window ? max(0, first - w.a.window + 1) : 0;
+    p.begin = w.a.window && first >= w.a.window ? first - w.a.window + 1 : 0;  // first may be far below 0
     p.lo = p.begin / KT;
     p.hi = (p.end + KT - 1) / KT;
     return p;

@@ -189,7 +189,8 @@ int attn_paged(const void* q, int64_t q_stride, const void* k_cache, const void*
     a.width = (int)table_width;
     a.scale = scale;
     a.softcap = softcap;
-    a.window = (int)std::min(window, kMaxInt);
+    // A window as long as the table hides nothing: none, which keeps position - window an int.
+    a.window = window < table_width * page_size ? (int)window : 0;
     const DevCtx* dc = nullptr;
     rc = device_ctx(&dc);
     if (rc) return rc;

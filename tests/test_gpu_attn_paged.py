@@ -363,3 +363,18 @@ def test_nothing_to_do_and_refusals():
                       table, off, ctx)
     with pytest.raises(qg.QGError):  # out over q
         qg.attn_paged(*ok, out=q)
+
+
+@pytest.mark.parametrize("new,ctx", [([4, 1, 3], [1, 500, 30]), ([90, 4, 30], [20, 1, 700])])
+def test_windows_longer_than_any_context(new, ctx):
+    """They hide nothing, also where rows sit far before the first key."""
+    args = list(make(16, [min(n, t) for n, t in zip(new, ctx)], ctx, 8, 2, 64, 16, torch.bfloat16))
+    g = torch.Generator("cuda").manual_seed(17)
+    args[0] = torch.randn(sum(new), 8, 64, generator=g, device="cuda").bfloat16()
+    args[4] = torch.tensor([0] + new, device="cuda").cumsum(0).to(torch.int32)
+    want, wlse = qg.attn_paged(*args, return_lse=True)
+    most = args[3].shape[1] * 16
+    for window in (most - 1, most, most + 1, 2**31 - 2, 2**31 - 1, 2**31, 2**40, 2**63 - 1):
+        out = check(tuple(args), window=window)
+        assert torch.equal(out, want), window
+        assert torch.equal(qg.attn_paged(*args, window=window, return_lse=True)[1], wlse), window
