@@ -25,7 +25,8 @@ __global__ void __launch_bounds__(kGThreads)
                    TY* __restrict__ y, int M, int N, int K, int KB) {
     __shared__ float as[kGChunk][kGTile + 4];
     __shared__ float ws[kGChunk][kGTile + 4];
-    const long long m0 = (long long)blockIdx.y * kGTile, n0 = (long long)blockIdx.x * kGTile;
+    const unsigned nt = (N - 1) / kGTile + 1;
+    const long long m0 = (long long)(blockIdx.x / nt) * kGTile, n0 = (long long)(blockIdx.x % nt) * kGTile;
     const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
     float total[4][4] = {}, part[4][4] = {};
     for (int k0 = 0; k0 < K; k0 += kGChunk) {
@@ -119,9 +120,9 @@ int pad_launch(const DevCtx& dc, const uint8_t* src, uint8_t* dst, long long row
 
 template <class TY>
 int general_launch(const Fp8Args& a, cudaStream_t s) {
-    const long long gx = (a.N + kGTile - 1) / kGTile, gy = (a.M + kGTile - 1) / kGTile;
-    if (gx > 0x7FFFFFFFLL || gy > 65535) return QG_ERR_UNSUPPORTED;
-    general_kernel<TY><<<dim3((unsigned)gx, (unsigned)gy), kGThreads, 0, s>>>(
+    const long long tiles = ((a.N + kGTile - 1) / kGTile) * ((a.M + kGTile - 1) / kGTile);
+    if (tiles > 0x7FFFFFFFLL) return QG_ERR_UNSUPPORTED;  // y alone would be 2^43 values
+    general_kernel<TY><<<(unsigned)tiles, kGThreads, 0, s>>>(
         a.a, a.sa, a.w, a.sw, static_cast<TY*>(a.y), (int)a.M, (int)a.N, (int)a.K,
         (int)((a.K + 127) / 128));
     return launched();

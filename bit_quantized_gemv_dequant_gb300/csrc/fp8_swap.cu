@@ -365,7 +365,7 @@ int launch_swap(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
 // blocks one after the other is taken. M = 256, N = K = 4096: 11.7 us with the
 // split, 18.1 in 256-wide tiles; M = 256, N = 12288, K = 4096: 32.9 and 18.1.
 bool swap_is_shorter(const DevCtx& dc, const Fp8Args& a) {
-    if (a.N > 65535 * 128LL) return false;  // more tiles than a grid's y has room for
+    if (a.N > 65535 * 128LL || a.M > 65535 * 128LL) return false;  // more tiles than a grid's y or z has room for
     if (a.M <= 64) return true;
     Plan p;
     if (plan<128, float>(dc, a, &p) != QG_OK) return false;

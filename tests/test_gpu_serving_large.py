@@ -112,3 +112,22 @@ def test_log_probabilities(dtype):
             assert torch.equal(a[-4:], b)
     assert (got[4][:-4] == torch.arange(7, device="cuda")).all() and (got[2][:-4] == 0).all()
     assert qg.device_error() == 0
+
+
+@pytest.mark.parametrize("M,N", [(65535 * 128 + 1, 64), (3, 65535 * 128 + 1)])
+@pytest.mark.parametrize("K,workspace", [(128, 0), (24, 0), (24, None)])
+def test_product_of_more_tiles_than_a_grid_has_rows(M, N, K, workspace):
+    """Few columns and millions of rows, and the reverse: on the tensor cores and, without a workspace, on the CUDA cores."""
+    g = rng(7)
+    a = torch.randint(0, 120, (M, K), generator=g, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+    w = torch.randint(0, 120, (N, K), generator=g, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+    sa = torch.rand(M, 1, generator=g, device="cuda")
+    sw = torch.rand(-(-N // 128), 1, generator=g, device="cuda")
+    none = torch.empty(16, dtype=torch.uint8, device="cuda") if workspace == 0 else None
+    y = qg.qmm_fp8_b128(a, sa, w, sw, workspace=none)
+    swn = sw.double().repeat_interleave(128, 0)[:N]
+    m = torch.cat([torch.arange(0, M, 99991, device="cuda"), torch.arange(max(0, M - 300), M, device="cuda")])
+    n = torch.cat([torch.arange(0, N, 99991, device="cuda"), torch.arange(max(0, N - 300), N, device="cuda")])
+    ref = (a[m].double() * sa[m].double()) @ (w[n].double() * swn[n]).t()
+    assert ((y[m][:, n].double() - ref).abs() <= 1e-5 * ref.abs() + 1e-6).all()  # all terms are positive
+    assert qg.device_error() == 0
