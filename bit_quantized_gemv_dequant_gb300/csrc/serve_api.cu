@@ -13,6 +13,8 @@ namespace qg {
 namespace {
 
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
+// Sizes and counts that kernels step through in ints, by up to 8192 at a time.
+constexpr int64_t kMaxCount = kMaxInt - 0x3FFF;
 constexpr int64_t kMaxBytes = (int64_t)1 << 56;  // no buffer is larger
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -61,7 +63,7 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 int check_planes(const PagePlanes& p) {
     if (!p.cache || p.planes <= 0 || p.num_pages <= 0 || p.page_bytes <= 0 || p.page_bytes % 16)
         return QG_ERR_INVALID_ARG;
-    if (p.num_pages > kMaxInt || p.planes > kMaxInt ||
+    if (p.num_pages > kMaxCount || p.planes > kMaxCount ||
         p.page_bytes > kMaxBytes / p.num_pages / p.planes)
         return QG_ERR_UNSUPPORTED;
     return aligned(p.cache, 16) ? QG_OK : QG_ERR_MISALIGNED;
@@ -71,7 +73,7 @@ bool page_size_ok(int64_t n) { return n >= 8 && n <= 256 && (n & (n - 1)) == 0; 
 
 int check_table(int64_t rows, int64_t width) {
     if (rows <= 0 || width <= 0) return QG_ERR_INVALID_ARG;
-    return rows > kMaxInt || width > kMaxInt || rows * width > kMaxInt ? QG_ERR_UNSUPPORTED : QG_OK;
+    return rows > kMaxCount || width > kMaxCount / rows ? QG_ERR_UNSUPPORTED : QG_OK;
 }
 
 cudaStream_t cu(qg_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -82,7 +84,7 @@ int attn_shape(AttnArgs* a, int64_t tokens, int64_t batch, int64_t max_new, int6
     if (tokens < 0 || batch <= 0 || max_new < 0 || hq <= 0 || hkv <= 0 || hq % hkv)
         return QG_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return QG_ERR_UNSUPPORTED;
-    if (hq / hkv > 128 || hq > 65535 || batch > 65535 || tokens > kMaxInt / hq)
+    if (hq / hkv > 128 || hq > 65535 || batch > 65535 || tokens > kMaxCount / hq)
         return QG_ERR_UNSUPPORTED;
     a->tokens = (int)tokens;
     a->batch = (int)batch;
@@ -103,7 +105,7 @@ extern "C" {
 int quantize_fp8_b128(const void* x, int x_dtype, int64_t x_stride, uint8_t* codes, float* scales,
                       int64_t M, int64_t K, qg_stream_t stream) {
     if (!x || !codes || !scales || M <= 0 || K <= 0 || !is_type(x_dtype)) return QG_ERR_INVALID_ARG;
-    if (M > kMaxInt || K > kMaxInt) return QG_ERR_UNSUPPORTED;
+    if (M > kMaxCount || K > kMaxCount) return QG_ERR_UNSUPPORTED;
     int64_t xb = 0;
     if (!span(M, K, x_stride, size_of(x_dtype), &xb)) return QG_ERR_INVALID_ARG;
     if (!aligned(x, size_of(x_dtype)) || !aligned(scales, 4)) return QG_ERR_MISALIGNED;
@@ -122,7 +124,7 @@ int qmm_fp8_b128(const uint8_t* a, const float* a_scales, const uint8_t* w, cons
     if (!a || !a_scales || !w || !w_scales || !y || M <= 0 || N <= 0 || K <= 0)
         return QG_ERR_INVALID_ARG;
     if (y_dtype != QG_F32 && y_dtype != QG_BF16) return QG_ERR_INVALID_ARG;
-    if (M > kMaxInt || N > kMaxInt || K > kMaxInt || M > kMaxBytes / 4 / N)
+    if (M > kMaxCount || N > kMaxCount || K > kMaxCount || M > kMaxBytes / 4 / N)
         return QG_ERR_UNSUPPORTED;
     if (!aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(y, size_of(y_dtype)))
         return QG_ERR_MISALIGNED;
@@ -143,7 +145,7 @@ int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) 
     if (!bytes) return QG_ERR_INVALID_ARG;
     *bytes = 0;
     if (M <= 0 || N <= 0 || K <= 0) return QG_ERR_INVALID_ARG;
-    if (M > kMaxInt || N > kMaxInt || K > kMaxInt) return QG_ERR_UNSUPPORTED;
+    if (M > kMaxCount || N > kMaxCount || K > kMaxCount) return QG_ERR_UNSUPPORTED;
     *bytes = (size_t)(M + N) * (size_t)((K + 15) / 16 * 16);
     return QG_OK;
 }
@@ -165,7 +167,7 @@ int attn_paged(const void* q, int64_t q_stride, const void* k_cache, const void*
         return QG_ERR_INVALID_ARG;
     rc = check_table(batch, table_width);
     if (rc) return rc;
-    if (num_pages > kMaxInt || table_width > kMaxInt / page_size) return QG_ERR_UNSUPPORTED;
+    if (num_pages > kMaxCount || table_width > kMaxCount / page_size) return QG_ERR_UNSUPPORTED;
     const int64_t cb = kv_heads * page_size * head_dim * 2;
     if (num_pages > kMaxBytes / cb) return QG_ERR_UNSUPPORTED;
     int64_t qb = 0;
@@ -223,7 +225,7 @@ int kv_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, 
         return QG_ERR_INVALID_ARG;
     if (tokens > 0 && (!k || !v || !slots)) return QG_ERR_INVALID_ARG;
     if (head_dim % 8) return QG_ERR_UNSUPPORTED;
-    if (kv_heads > 65535 || head_dim > 65535 || tokens > kMaxInt || num_pages > kMaxInt ||
+    if (kv_heads > 65535 || head_dim > 65535 || kv_heads * head_dim > kMaxCount || tokens > kMaxCount || num_pages > kMaxCount ||
         num_pages > kMaxBytes / (kv_heads * page_size * head_dim * 2))
         return QG_ERR_UNSUPPORTED;
     int64_t kb = 0, vb = 0;
@@ -252,7 +254,7 @@ int kv_copy_pages(void* cache, int64_t planes, int64_t num_pages, int64_t page_b
     int rc = check_planes(p);
     if (rc) return rc;
     if (n < 0 || (n > 0 && (!src || !dst))) return QG_ERR_INVALID_ARG;
-    if (n > kMaxInt) return QG_ERR_UNSUPPORTED;
+    if (n > kMaxCount) return QG_ERR_UNSUPPORTED;
     if (!aligned(src, 4) || !aligned(dst, 4)) return QG_ERR_MISALIGNED;
     const Region out[] = {{cache, planes * num_pages * page_bytes}};
     const Region in[] = {{src, n * 4}, {dst, n * 4}};
@@ -268,7 +270,7 @@ int kv_fork_workspace_size(int64_t children, size_t* bytes) {
     if (!bytes) return QG_ERR_INVALID_ARG;
     *bytes = 0;
     if (children < 0) return QG_ERR_INVALID_ARG;
-    if (children > kMaxInt) return QG_ERR_UNSUPPORTED;
+    if (children > kMaxCount) return QG_ERR_UNSUPPORTED;
     // the children's sources and destinations, and the free pages they take
     *bytes = (size_t)children * 12 + 16;
     return QG_OK;
@@ -287,7 +289,7 @@ int kv_fork(void* cache, int64_t planes, int64_t num_pages, int64_t page_bytes, 
     if (!page_size_ok(page_size) || !page_table || !lens || !ref_counts || !new_refs || children < 0)
         return QG_ERR_INVALID_ARG;
     if (children > 0 && (!parents || !child_table || !child_lens)) return QG_ERR_INVALID_ARG;
-    if (children > kMaxInt / table_width) return QG_ERR_UNSUPPORTED;
+    if (children > kMaxCount / table_width) return QG_ERR_UNSUPPORTED;
     const void* ints[] = {page_table, lens, ref_counts, parents, child_table, child_lens, new_refs};
     for (const void* i : ints)
         if (!aligned(i, 4)) return QG_ERR_MISALIGNED;
@@ -320,7 +322,7 @@ int kv_free(const int32_t* page_table, const int32_t* lens, const int32_t* ref_c
     if (!page_table || !lens || !ref_counts || !drop || !new_table || !new_lens || !new_refs ||
         num_pages <= 0)
         return QG_ERR_INVALID_ARG;
-    if (num_pages > kMaxInt) return QG_ERR_UNSUPPORTED;
+    if (num_pages > kMaxCount) return QG_ERR_UNSUPPORTED;
     const void* ints[] = {page_table, lens, ref_counts, new_table, new_lens, new_refs};
     for (const void* i : ints)
         if (!aligned(i, 4)) return QG_ERR_MISALIGNED;
@@ -341,7 +343,7 @@ int kv_compact_workspace_size(int64_t num_pages, size_t* bytes) {
     if (!bytes) return QG_ERR_INVALID_ARG;
     *bytes = 0;
     if (num_pages <= 0) return QG_ERR_INVALID_ARG;
-    if (num_pages > kMaxInt) return QG_ERR_UNSUPPORTED;
+    if (num_pages > kMaxCount) return QG_ERR_UNSUPPORTED;
     // the number of moves, then their sources and destinations (at most half
     // of the pages move)
     *bytes = 16 + (size_t)((num_pages + 1) / 2) * 8;

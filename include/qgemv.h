@@ -266,7 +266,9 @@ QG_API int qmm_af4_g64(const float* x, const uint32_t* plane, const uint32_t* me
  * additions: element types are named by QG_F32 / QG_F16 / QG_BF16, strides
  * count elements, and index arrays are device memory that the kernels check
  * as they read it (an index out of its range is never followed; the device
- * error word records it, see qg_device_error). */
+ * error word records it, see qg_device_error). Sizes and counts, and the
+ * products tokens * heads, kv_heads * head_dim, rows * table_width and
+ * table_width * page_size, are at most 2^31 - 2^14 (else QG_ERR_UNSUPPORTED). */
 enum { QG_F32 = 0, QG_F16 = 1, QG_BF16 = 2 };
 
 /* 8-bit floating point (e4m3) with one scale per 128 values of K.

@@ -120,3 +120,40 @@ def test_logprobs():
             x_2=(at(0) + 2, MISALIGNED), targets_2=(at(10) + 4, MISALIGNED), h_2=(at(11), INVALID),
             ti_2=(at(0) + 4, INVALID), V_3=(1 << 30, INVALID))
     refused("token_logprobs", dict(good, stride=1 << 31), V=((1 << 30) + 1, UNSUPPORTED))
+
+
+def test_sizes_next_to_31_bits():
+    """Kernels step through sizes in ints: what a step could carry past 2^31 - 1 is refused, what could not is not."""
+    most = (1 << 31) - (1 << 14)
+    n = C.c_size_t()
+    for big in (most, (1 << 31) - 1):
+        status = OK if big == most else UNSUPPORTED
+        for shape in ((big, 1, 16), (1, big, 16), (1, 1, big)):
+            assert qg.lib().qmm_fp8_b128_workspace_size(*shape, C.byref(n)) == status, shape
+        assert qg.lib().kv_fork_workspace_size(big, C.byref(n)) == status
+        assert qg.lib().kv_compact_workspace_size(big, C.byref(n)) == status
+    over, far = most + 1, 1 << 50
+    product = dict(a=at(0), sa=far, w=2 * far, sw=3 * far, y=4 * far, dtype=F32, M=1, N=1, K=1, ws=None, wsb=0, stream=None)
+    refused("qmm_fp8_b128", product, M=(over, UNSUPPORTED), N=(over, UNSUPPORTED), K=(over, UNSUPPORTED))
+    quantize = dict(x=at(0), dtype=F32, stride=1 << 31, codes=far, scales=2 * far, M=1, K=1, stream=None)
+    refused("quantize_fp8_b128", quantize, M=(over, UNSUPPORTED), K=(over, UNSUPPORTED))
+    attn = dict(q=at(0), stride=64, k=far, v=2 * far, table=3 * far, offsets=4 * far, lens=5 * far, out=6 * far,
+                lse=None, dtype=BF16, tokens=1, batch=1, max_new=1, hq=1, hkv=1, d=64, pages=1, page=256, width=1,
+                scale=1.0, softcap=0.0, window=0, ws=None, wsb=0, stream=None)
+    refused("attn_paged", attn, tokens=(over, UNSUPPORTED), pages=(over, UNSUPPORTED), width=(over // 256 + 1, UNSUPPORTED))
+    append = dict(k=at(0), v=far, ks=1 << 33, vs=1 << 33, x=F16, kc=2 * far, vc=3 * far, c=F16, slots=4 * far, tokens=1,
+                  heads=1, d=8, pages=1, page=8, stream=None)
+    refused("kv_append", append, tokens=(over, UNSUPPORTED), pages=(over, UNSUPPORTED))
+    refused("kv_append", dict(append, heads=65528), d=(32776, UNSUPPORTED))  # 2^31 + 2^15 - 64 values in a row
+    planes = dict(cache=far, planes=1, pages=1, bytes=16)
+    copy = dict(planes, src=at(40), dst=at(41), n=3, stream=None)
+    refused("kv_copy_pages", copy, planes=(over, UNSUPPORTED), pages=(over, UNSUPPORTED), n=(over, UNSUPPORTED))
+    free = dict(table=at(0), lens=far, refs=2 * far, drop=3 * far, rows=1, width=1, pages=1, nt=4 * far, nl=5 * far,
+                nr=6 * far, stream=None)
+    refused("kv_free", free, rows=(over, UNSUPPORTED), width=(over, UNSUPPORTED), pages=(over, UNSUPPORTED))
+    fork = dict(planes, page=16, table=at(40), lens=2 * far, refs=3 * far, rows=1, width=1, parents=4 * far, children=1,
+                ct=5 * far, cl=6 * far, nr=7 * far, ws=8 * far, wsb=4096, stream=None)
+    refused("kv_fork", fork, rows=(over, UNSUPPORTED), width=(over, UNSUPPORTED), children=(over, UNSUPPORTED))
+    compact = dict(planes, table=2 * far, rows=1, width=1, refs=3 * far, nt=4 * far, nr=5 * far, map=6 * far, live=7 * far,
+                   ws=8 * far, wsb=4096, stream=None)
+    refused("kv_compact", compact, rows=(over, UNSUPPORTED), width=(over, UNSUPPORTED), pages=(over, UNSUPPORTED))
