@@ -198,7 +198,7 @@ int attn_paged(const void* q, int64_t q_stride, const void* k_cache, const void*
     if (rc) return rc;
     rc = check_workspace(workspace, workspace_bytes, attn_workspace_bytes(*dc, a));
     if (rc) return rc;
-    if (a.tokens == 0 || a.max_new == 0) return QG_OK;
+    if (a.tokens == 0) return QG_OK;  // with max_new = 0 the kernel records sequences that have some
     return attn_launch(*dc, a, workspace, cu(stream));
 }
 

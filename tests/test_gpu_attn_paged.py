@@ -378,3 +378,13 @@ def test_windows_longer_than_any_context(new, ctx):
         out = check(tuple(args), window=window)
         assert torch.equal(out, want), window
         assert torch.equal(qg.attn_paged(*args, window=window, return_lse=True)[1], wlse), window
+
+
+def test_no_new_tokens_allowed():
+    """max_new = 0: sequences with new tokens are recorded, nothing is written; without any it is an empty step."""
+    args = make(18, [2, 1], [20, 40], 8, 2, 64, 16, torch.bfloat16)
+    out = torch.full((3, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    qg.attn_paged(*args, out=out, max_new=0)
+    assert qg.device_error() == 32 and (out == 7).all()
+    qg.attn_paged(*args[:4], torch.zeros_like(args[4]), args[5], out=out, max_new=0)
+    assert qg.device_error() == 0 and (out == 7).all()
