@@ -291,7 +291,9 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a, unsign
                 if (fresh >= 0) atomicAdd(a.new_refs + fresh, 1 - min(0, a.refs[fresh]));
                 if (want && fresh < 0) report_error(err, DEVERR_NO_PAGE);
                 a.child_lens[c0 + i] = want && fresh < 0 ? whole * a.page_size : n;
-                ws_src[c0 + i] = fresh >= 0 ? old[whole] : -1;
+                const int last = fresh >= 0 ? old[whole] : -1;
+                if (fresh >= 0 && last < 0) report_error(err, DEVERR_INDEX);  // the copies report those past the last page
+                ws_src[c0 + i] = last;
                 ws_dst[c0 + i] = fresh;
             }
         }

@@ -362,6 +362,9 @@ QG_API int attn_paged_workspace_size(int64_t tokens, int64_t batch, int64_t max_
  * one if that is partly filled. Its entries after that are -1. The k-th
  * child that needs a page takes the k-th lowest free one; if there is none,
  * the child ends at its whole pages and the device error word says so.
+ * Entries of the parent's pages that name no page are recorded too: a whole
+ * one stays -1, and in place of the last one the child has a page without
+ * its contents.
  * Writes child_table [children, table_width], child_lens [children] and
  * new_refs [num_pages] (workspace: kv_fork_workspace_size()).
  *

@@ -268,3 +268,20 @@ def test_refusals():
         qg.kv_append(k, k, kc, kc, s)
     with pytest.raises(qg.QGError):  # a cache of 32-bit values
         qg.kv_append(k, k, kc.float(), kc.float(), s)
+
+
+@pytest.mark.parametrize("entry", [-1, -7, 6, 10**6])
+def test_fork_of_a_row_without_its_last_page(entry):
+    """A partly filled last page that the table does not name: recorded, and no page is read for it."""
+    for where in (0, 1):
+        cache = cache_of(9, 2, 6, 4, 8)
+        before = cache.clone()
+        table, refs = i32([[4, 2, -1], [0, 3, -1]]), i32([1, 0, 1, 1, 1, 0])
+        table[0, where] = entry
+        child, lens, new = qg.kv_fork(cache, table, i32([12, 13]), refs, i32([0, 1]), 8)
+        assert qg.device_error() == 32
+        assert lens.tolist() == [12, 13] and child[1].tolist() == [0, 5, -1]
+        assert child[0].tolist() == ([-1, 1, -1] if where == 0 else [4, 1, -1])
+        assert new.tolist() == [2, 1, 1, 1, 1 if where == 0 else 2, 1]
+        assert torch.equal(cache[:, 5], before[:, 3]) and torch.equal(cache[:, [0, 2, 3, 4]], before[:, [0, 2, 3, 4]])
+        assert torch.equal(cache[:, 1], before[:, 2] if where == 0 else before[:, 1])
