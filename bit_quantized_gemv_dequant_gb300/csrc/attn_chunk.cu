@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *slot;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     Cuts cuts;
     Place place;
     Seq seq;
@@ -528,7 +528,7 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     const int rows = std::min(w.a.page_size, kKT);
     int rc = cache_map(&mk, w.a, w.a.k, rows);
     if (rc == QG_OK) rc = cache_map(&mv, w.a, w.a.v, rows);
-    if (rc == QG_OK) rc = launch(kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
+    if (rc == QG_OK) rc = launch(may_overlap(), kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
     if (rc) return rc;
     return launch_join<T, D, kRT, kKT, 4, 2>(w, s);
 }

@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&map_v);
     }
     __syncthreads();
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     Cuts cuts;
     Place place;
     Seq seq;
@@ -356,7 +356,7 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     const int rows = std::min(w.a.page_size, kKT);
     int rc = cache_map(&mk, w.a, w.a.k, rows);
     if (rc == QG_OK) rc = cache_map(&mv, w.a, w.a.v, rows);
-    if (rc == QG_OK) rc = launch(kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
+    if (rc == QG_OK) rc = launch(may_overlap(), kern, dim3(w.ctas), kThreads, Geo<D>::kSmem, s, mk, mv, w);
     if (rc) return rc;
     return launch_join<T, D, 16 * RB, kKT, 1, 12>(w, s);
 }

@@ -126,8 +126,8 @@ __device__ __noinline__ void redo_rows(const Work& w, int b, int head, int r0, i
 template <class T, int D, int RT, int KT, int R, int ROWS, int PARTS, bool REDO>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Work w) {
     static_assert(R == ROWS * (kJoinThreads / 32), "one round per warp");
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     const Note n = w.notes[blockIdx.x];
     const int lane = threadIdx.x & 31, x = blockIdx.x, r0 = blockIdx.y * R + (threadIdx.x >> 5) * ROWS;
     const bool mine = n.from >= 0 && n.r0 + r0 < n.rows;
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 template <class K, class... A>
-int launch(K kern, dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {
+int launch(bool overlap, K kern, dim3 grid, int threads, int smem, cudaStream_t s, const A&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -211,7 +211,7 @@ int launch(K kern, dim3 grid, int threads, int smem, cudaStream_t s, const A&...
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = overlap ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }
@@ -220,8 +220,8 @@ template <class T, int D, int RT, int KT, int ROWS, int PARTS>
 int launch_join(const Work& w, cudaStream_t s) {
     constexpr int R = ROWS * (kJoinThreads / 32);
     return w.a.max_new > 1
-               ? launch(join_kernel<T, D, RT, KT, R, ROWS, PARTS, true>, dim3(w.ctas, RT / R), kJoinThreads, 0, s, w)
-               : launch(join_kernel<T, D, RT, KT, R, ROWS, PARTS, false>, dim3(w.ctas, RT / R), kJoinThreads, 0, s, w);
+               ? launch(true, join_kernel<T, D, RT, KT, R, ROWS, PARTS, true>, dim3(w.ctas, RT / R), kJoinThreads, 0, s, w)
+               : launch(true, join_kernel<T, D, RT, KT, R, ROWS, PARTS, false>, dim3(w.ctas, RT / R), kJoinThreads, 0, s, w);
 }
 
 }  // namespace

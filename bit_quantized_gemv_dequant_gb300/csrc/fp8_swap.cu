@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(Geo<BN>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *slot;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
 
     float2 acc[G::kOwn / 2];
 #pragma unroll
@@ -342,7 +342,7 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = may_overlap() ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, swap_kernel<BN, TY>, mw, ma, p);
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }

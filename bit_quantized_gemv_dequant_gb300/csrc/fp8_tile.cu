@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();  // the other CTA's barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *slot;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -379,13 +379,13 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = may_overlap() ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ma, mw, my, p);
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }

@@ -95,8 +95,8 @@ struct Remap {
 
 __global__ void __launch_bounds__(kCopyThreads)
     copy_kernel(const PagePlanes p, const CopyList l, const Remap r, unsigned* err) {
-    fp8::pdl_trigger();
     fp8::pdl_wait();
+    fp8::pdl_trigger();
     for (long long i = (long long)blockIdx.x * kCopyThreads + threadIdx.x; r.table && i < r.n;
          i += (long long)gridDim.x * kCopyThreads) {
         const int32_t page = r.table[i];
@@ -145,19 +145,19 @@ __global__ void __launch_bounds__(kCopyThreads)
 }
 
 int copy_launch(const DevCtx& dc, const PagePlanes& p, const CopyList& l, const Remap& r,
-                long long most, cudaStream_t s) {
+                long long most, bool overlap, cudaStream_t s) {
     const long long pieces = (p.page_bytes / 16 + kPiece - 1) / kPiece;
     const long long work = std::max(most * p.planes * pieces, (r.n + kCopyThreads - 1) / kCopyThreads);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)std::max(1LL, std::min<long long>(work, (long long)dc.num_sms * 8)));
     cfg.blockDim = dim3(kCopyThreads);
     cfg.stream = s;
-    // starts while the kernel with the tables ends, and waits for it
+    // after the kernel with the tables it starts while that one ends, and waits for it
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = overlap ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, copy_kernel, p, l, r, dc.err);
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }
@@ -413,14 +413,14 @@ int kv_append_launch(const DevCtx& dc, const AppendArgs& a, cudaStream_t s) {
 
 int kv_copy_launch(const DevCtx& dc, const PagePlanes& p, const int32_t* src, const int32_t* dst,
                    long long n, cudaStream_t s) {
-    return copy_launch(dc, p, CopyList{src, dst, nullptr, n}, Remap{}, n, s);
+    return copy_launch(dc, p, CopyList{src, dst, nullptr, n}, Remap{}, n, may_overlap(), s);
 }
 
 int kv_fork_launch(const DevCtx& dc, const ForkArgs& a, cudaStream_t s) {
     int rc = cluster_launch(fork_kernel, s, a, dc.err);
     if (rc || a.children == 0) return rc;
     return copy_launch(dc, a.p, CopyList{a.ws, a.ws + a.children, nullptr, a.children}, Remap{},
-                       a.children, s);
+                       a.children, true, s);
 }
 
 int kv_free_launch(const DevCtx& dc, const FreeArgs& a, cudaStream_t s) {
@@ -433,7 +433,7 @@ int kv_compact_launch(const DevCtx& dc, const CompactArgs& a, cudaStream_t s) {
     const long long most = (a.p.num_pages + 1) / 2;
     const int32_t* src = a.ws + 4;
     return copy_launch(dc, a.p, CopyList{src, src + most, a.ws, 0},
-                       Remap{a.table, a.map, a.new_table, (long long)a.rows * a.width}, most, s);
+                       Remap{a.table, a.map, a.new_table, (long long)a.rows * a.width}, most, true, s);
 }
 
 }  // namespace qg

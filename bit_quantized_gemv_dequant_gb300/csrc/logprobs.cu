@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) row_kernel(const Lo
         fence_mbar_init();
     }
     __syncthreads();
-    fp8::pdl_trigger();
     fp8::pdl_wait();
+    fp8::pdl_trigger();
     int st = 0;          // place of the next stage in the ring
     uint32_t ph = 0;     // and its phase
 
@@ -619,7 +619,7 @@ int logprobs_launch(const DevCtx& dc, const LogprobArgs& a, cudaStream_t s) {
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 2;
+        cfg.numAttrs = may_overlap() ? 2 : 1;
         const cudaError_t e = cudaLaunchKernelEx(&cfg, row_kernel<T>, a, dc.err);
         return e == cudaSuccess ? (int)QG_OK : cuda_fail(e);
     });

@@ -665,8 +665,8 @@ int launch_main(const DevCtx& dc, const CUtensorMap& mq, const CUtensorMap& mx, 
     return e == cudaSuccess ? QG_OK : cuda_fail(e);
 }
 
-// prep_kernel as a programmatic dependent of the preceding kernel (it waits
-// for it before touching any data).
+// prep_kernel as a programmatic dependent of the preceding kernel, where it may be
+// (it waits for it before touching any data).
 int launch_prep(unsigned blocks, cudaStream_t s, const float* x, __half* xh, float* xsum,
                 float* inv, const float* sc, const float* bi, float* sc_t, float* bi_t,
                 float* bpart, float qmax, int M, int N, int K, int gs, int G, int Mp) {
@@ -679,7 +679,7 @@ int launch_prep(unsigned blocks, cudaStream_t s, const float* x, __half* xh, flo
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = may_overlap() ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, prep_kernel, x, xh, xsum, inv, sc, bi, sc_t, bi_t,
                                        bpart, qmax, M, N, K, gs, G, Mp);
     return e == cudaSuccess ? QG_OK : cuda_fail(e);

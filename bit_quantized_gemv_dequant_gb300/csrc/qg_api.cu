@@ -23,6 +23,7 @@ std::once_flag g_once[kMaxDevices];
 int g_ctx_rc[kMaxDevices];
 thread_local int t_last_cuda_error = 0;
 std::atomic<long long> g_opt_pdl{0};
+std::atomic<bool> g_independent{false};  // QG_OPT_PDL has been 2
 std::atomic<long long> g_opt_prefill_min_m{64};
 std::atomic<long long> g_opt_stream{1};
 std::atomic<long long> g_opt_stream_warps{0};
@@ -292,6 +293,8 @@ long long launch_option(int option) {
     }
 }
 
+bool may_overlap() { return !g_independent.load(std::memory_order_relaxed); }
+
 int cuda_fail(cudaError_t e) {
     t_last_cuda_error = static_cast<int>(e);
     return QG_ERR_CUDA;
@@ -533,6 +536,7 @@ int qg_set_option(int option, int64_t value) {
     switch (option) {
         case QG_OPT_PDL:
             if (value < 0 || value > 2) return QG_ERR_INVALID_ARG;
+            if (value == 2) g_independent.store(true, std::memory_order_relaxed);
             g_opt_pdl.store(value, std::memory_order_relaxed);
             return QG_OK;
         case QG_OPT_PREFILL_MIN_M:

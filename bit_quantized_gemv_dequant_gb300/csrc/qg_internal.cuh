@@ -155,6 +155,18 @@ struct DevCtx {
 // Process-wide launch options set through qg_set_option().
 long long launch_option(int option);
 
+// Whether the first kernel of a call may be launched with programmatic stream
+// serialization whatever QG_OPT_PDL says: it starts while the kernel before it
+// ends, and its griddepcontrol.wait waits for that kernel alone. That is all there
+// is to wait for as long as every kernel has waited itself, so no longer once calls
+// may have been made under QG_OPT_PDL = 2. (Measured, a kernel is not complete
+// before the one that it did not wait for is; nothing documents that.)
+//
+// Every kernel that is launched this way lets its successor start only once it has
+// waited: a call under QG_OPT_PDL = 2, which may not wait for it, is then past
+// everything that came before it.
+bool may_overlap();
+
 // ----------------------------------------------------------------- launchers
 // GEMV family (gemv.cu). fmt: see GemvFmt. Returns a qg_status.
 // FMT_AF4: the prepared AF4-g64 layout (qmm_af4_g64); only the

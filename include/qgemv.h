@@ -437,15 +437,21 @@ QG_API int qg_workspace_size(int op, int64_t M, int64_t N, int64_t K, int group_
  * weights satisfy this). Back-to-back decode projections overlap one call's
  * ramp-up with the previous call's tail this way.
  *
- * QG_OPT_PDL = 2 adds a second promise: the call reads nothing the kernel
- * immediately preceding it on the stream writes, and writes nothing that
- * kernel reads or writes (independent projections, e.g. several projections
- * of one input, or calls on distinct buffers). The register-resident-x
- * kernel (QG_OPT_XREG) and the staged kernel (when the call needs no split-K
- * workspace, which consecutive calls may share) then do not wait for their
- * predecessor at all, so consecutive independent calls run concurrently; the
- * other kernels behave as with 1. A kernel launched after such a call
- * without programmatic dependent launch still waits for it as usual. */
+ * QG_OPT_PDL = 2 adds a second promise: the call reads nothing that the call
+ * (or other kernel) before it on the stream writes, and writes nothing that
+ * that one reads or writes (independent projections, e.g. several projections
+ * of one input, or calls on distinct buffers). Where that one was itself made
+ * under 1 or 2 the same holds against the one before it, and so on back to the
+ * first that was not; a call of a serving operator (below the projections in
+ * this file) ends the row too. The register-resident-x kernel (QG_OPT_XREG) and
+ * the staged kernel (when the call needs no split-K workspace, which
+ * consecutive calls may share) then do not wait for their predecessor at all,
+ * so consecutive independent calls run concurrently; the other kernels behave
+ * as with 1. A call that does depend on calls made under 2 is made under 0, a
+ * serving operator under any setting: it waits for all of them. (The kernels of
+ * serving operators and the tensor-core prefill overlap the end of the kernel
+ * before them whatever the setting is, until it has been 2 for the first time;
+ * from then on their calls wait before they start.) */
 /*
  * QG_OPT_PREFILL_MIN_M (default 64, >= 1): smallest M for which qmm_affine
  * (and the Q4_0 / Q4_K calls) take the tensor-core prefill path when its

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import bit_quantized_gemv_dequant_gb300 as qg
+from bit_quantized_gemv_dequant_gb300 import synth
 
 pytestmark = pytest.mark.gpu
 
@@ -144,4 +145,78 @@ def test_graphs_beside_each_other():
         assert all(torch.equal(out, w) for (_, out), w in zip(made, want))
         assert all(torch.equal(out, want[2]) for out in eager)
         assert all(f.right(out) for f, (_, out) in zip(forks, made_forks))
+    assert qg.device_error() == 0
+
+
+@pytest.fixture
+def pdl():
+    """Sets QG_OPT_PDL; it is what it was afterwards."""
+    old = qg.get_option(qg.QG_OPT_PDL)
+    yield lambda value: qg.set_option(qg.QG_OPT_PDL, value)
+    qg.set_option(qg.QG_OPT_PDL, old)
+
+
+def projection(seed, n, k):
+    w = torch.from_numpy(synth.q4_k_case(seed, 64, k, 1)["w"]).cuda()
+    return w.flatten().repeat(n // 64)
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+def test_serving_after_independent_projections(pdl, mode):
+    """Projections that need not wait for each other, then a call that reads what all of them wrote."""
+    n, parts = 16384, 3
+    ws = [projection(20 + i, n, 4096) for i in range(parts)]
+    g = torch.Generator("cuda").manual_seed(21)
+    xs = [torch.randn(1, 4096, generator=g, device="cuda") for _ in range(12)]
+    targets = torch.randint(0, n * parts, (1,), generator=g, device="cuda")
+    logits = torch.empty(1, n * parts, device="cuda")
+    pieces = [logits[:, i * n:(i + 1) * n] for i in range(parts)]
+
+    def step(x, mode):
+        pdl(mode)
+        for w, piece in zip(ws, pieces):
+            qg.qgemv_q4_k(w, x, piece, N=n)
+        return qg.token_logprobs(logits, targets, 5)
+
+    want = [step(x, 0) for x in xs]
+    got = [step(x, mode) for x in xs]
+    for a, b in zip(want, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    assert qg.device_error() == 0
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+def test_independent_projection_after_serving(pdl, mode):
+    """A projection that has nothing to do with the serving call before it, but with what came before that."""
+    n, k = 4096, 4096
+    w = projection(30, n, k)
+    g = torch.Generator("cuda").manual_seed(31)
+    big = torch.randn(4096, 4096, generator=g, device="cuda")
+    x = torch.empty(1, k, device="cuda")
+    args = attention(32)
+    fork, codes = Fork(33, 7), torch.ones(2, 512, device="cuda").to(torch.float8_e4m3fn)
+    small = torch.randn(3, 5000, generator=g, device="cuda")
+    rows, one = torch.zeros(3, dtype=torch.int64, device="cuda"), torch.ones(2, 4, device="cuda")
+    pair = torch.arange(2, dtype=torch.int32, device="cuda")
+    serving = [lambda: qg.attn_paged(*args, max_new=1), lambda: qg.attn_paged(*args, max_new=40), fork,
+               lambda: qg.kv_copy_pages(fork.cache, pair, pair + 2), lambda: qg.qmm_fp8_b128(codes, one, codes, one[:1]),
+               lambda: qg.qmm_fp8_b128(codes.repeat(80, 1), one.repeat(80, 1), codes, one[:1]),
+               lambda: qg.token_logprobs(small, rows, 3)]
+
+    def run(mode):
+        out = []
+        for i, call in enumerate(serving):
+            pdl(0)
+            v = torch.full((4096, 1), 0.01 * (i + 1), device="cuda")
+            for _ in range(3):
+                v = torch.mm(big, v) / 64
+            torch.mm(v.t(), big, out=x)  # (some time on the way, so that a call that does not wait reads the old x)
+            call()
+            pdl(mode)
+            out.append(qg.qgemv_q4_k(w, x, N=n))
+        return out
+
+    want = run(0)
+    for a, b in zip(want, run(mode)):
+        assert torch.equal(a, b)
     assert qg.device_error() == 0
