@@ -220,3 +220,41 @@ def test_independent_projection_after_serving(pdl, mode):
     for a, b in zip(want, run(mode)):
         assert torch.equal(a, b)
     assert qg.device_error() == 0
+
+
+def chain():
+    """Steps in which every call reads what the one before wrote, without a pause: the results of all of them."""
+    q, k, v, table, offsets, lens = attention(40, (900, 70, 1300), (1, 30, 1))
+    g = torch.Generator("cuda").manual_seed(41)
+    w = torch.randn(512, 512, generator=g, device="cuda").to(torch.float8_e4m3fn)
+    head = torch.randn(5000, 512, generator=g, device="cuda").to(torch.float8_e4m3fn)
+    one, many = torch.ones(4, 4, device="cuda"), torch.ones(40, 4, device="cuda")
+    targets = torch.randint(0, 5000, (32,), generator=g, device="cuda")
+    last = torch.tensor([n - 1 for n, c in ((900, 1), (70, 30), (1300, 1)) for _ in range(c)], device="cuda")
+    row = torch.tensor([0] + [1] * 30 + [2], device="cuda")
+    slots = table.long()[row, last // 16] * 16 + last % 16
+    slots[1:30] = -1
+    out = []
+    for _ in range(20):
+        a, lse = qg.attn_paged(q, k, v, table, offsets, lens, max_new=30, return_lse=True)
+        codes, scales = qg.quantize_fp8_b128(a.view(32, 512))
+        x = qg.qmm_fp8_b128(codes, scales, w, one, out_dtype=torch.bfloat16)
+        q = x.view(32, 8, 64)
+        qg.kv_append(q[:, :2], q[:, 2:4], k, v, slots)
+        codes, scales = qg.quantize_fp8_b128(x)
+        out += [a, lse, x, *qg.token_logprobs(qg.qmm_fp8_b128(codes, scales, head, many), targets, 3)]
+    torch.cuda.synchronize()
+    return [t.cpu() for t in out]
+
+
+def test_overlapped_calls_give_the_same(pdl, tmp_path):
+    """In a process where QG_OPT_PDL has never been 2, calls start while the one before ends; here they do not."""
+    code = "import sys, torch; sys.path[:0] = ['tests', '.']; import test_gpu_serving_calls as t; torch.save(t.chain(), sys.argv[1])"
+    r = subprocess.run([sys.executable, "-c", code, str(tmp_path / "out.pt")], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    pdl(2)
+    pdl(0)
+    for a, b in zip(torch.load(tmp_path / "out.pt"), chain(), strict=True):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    assert qg.device_error() == 0
