@@ -14,12 +14,14 @@ namespace {
 // A row is read once, by one CTA or, when there are few rows, by a cluster of
 // them, each taking a share of it; bound by the bytes of the logits.
 //
-// Each thread keeps, in base 2 with d = x log2(e) - c (c: its running maximum
-// times log2(e)),
+// Each thread keeps, in base 2 with d = x log2(e) - b, where c is a logit next to
+// its running maximum and b = c log2(e) rounded to f32,
 //     s = sum 2^d,  t = sum d 2^d,
-// which a larger maximum, c' = c + g, turns into 2^-g s and 2^-g (t - g s).
-// At the end, with c, s, t of the whole row,
-//     log p(x) = ln2 (x log2(e) - c - log2 s),  entropy = ln2 (log2 s - t / s).
+// which a larger base b + g turns into 2^-g s and 2^-g (t - g s). The rounding of b
+// is the same in every term and d is rounded once (a fused multiplication), so it
+// moves s by 2^r, r = c log2(e) - b. At the end, with c, s, t of the whole row,
+//     log p(x) = (x - c) - (ln s - r ln2),  entropy = ln s - ln2 t / s.
+// Both are within a few 2^-24 of ln s and of themselves.
 //
 // A producer warp copies the row's aligned middle into a ring of 16 KB stages by
 // bulk copies, and on into the CTA's next row, so that the loads go on while a row
@@ -35,7 +37,7 @@ namespace {
 // (done by all warps between two rows it took 55 us of 159 for 2048 rows of
 // 131072 bf16 logits with the 5 largest).
 //
-// 2048 x 131072 bf16, 5 largest: 120 us, 4.5 TB/s, two thirds of all issue slots
+// 2048 x 131072 bf16, 5 largest: 121 us, 4.5 TB/s, two thirds of all issue slots
 // taken. One row of 50021 f32, 20 largest: 11.0 us, the latency of the finish.
 constexpr int kThreads = 256;               // that read logits; a producer and a finishing warp more
 constexpr int kWarps = kThreads / 32;
@@ -45,7 +47,11 @@ constexpr int kStageChunks = kPer * kThreads;
 constexpr int kStages = 6;
 constexpr int kRing = kStages * kStageChunks * 32;
 constexpr int kCtasPerSm = 2;
-constexpr float kLazy = 20.f;               // exponentials up to e^20 are left as they are
+// The maximum is followed in steps of 2 bits: d up to 2 rounds no worse than the
+// exponential does, and a row that is dominated by one logit has it as its base
+// (otherwise another with a fourth of its probability). With steps of 29 bits log
+// probabilities were off by 3e-6 and entropies by 1e-5.
+constexpr float kLazy = 1.3862944f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 using Key = unsigned long long;
@@ -168,15 +174,24 @@ struct Row {
 struct Stats {
     float c, s, t;  // c = -infinity: nothing yet
 };
-// The same with c instead of a.c. (Without logits s = t = 0; the distance from
-// -infinity is cut to a finite number.)
+// The base of c, and whether it is a number (it is not next to the type's largest,
+// nor for nothing; differences come first then).
+__device__ __forceinline__ float base_of(float c) { return __fmul_rn(c, kLog2e); }
+__device__ __forceinline__ bool has_base(float c) { return fabsf(base_of(c)) <= 3.4028235e38f; }
+// From base c to a's, which is not larger. (From nothing: cut to a finite number.)
+__device__ __forceinline__ float gap(float a, float c) {
+    const float g = has_base(c) ? base_of(a) - base_of(c) : (a - (c == -INFINITY ? 0.f : c)) * kLog2e;
+    return fmaxf(g, -200.f);
+}
+// The same with c instead of a.c. (Without logits s = t = 0.)
 __device__ __forceinline__ Stats rebased(const Stats& a, float c) {
-    const float g = fmaxf((a.c - (c == -INFINITY ? 0.f : c)) * kLog2e, -200.f), f = ex2(g);
+    const float g = gap(a.c, c), f = ex2(g);
     return Stats{c, a.s * f, f * (a.t + g * a.s)};
 }
 
 struct Thread {
     Stats st;
+    float minus_b;  // minus the base of st.c
     float best;     // the largest logit, NaN above all, and the first chunk with it
     int best_chunk;
     int above;
@@ -193,17 +208,18 @@ struct Thread {
             best = cm;
             best_chunk = chunk;
         }
-        if (cm > st.c + kLazy) {  // always at first: st.c is -infinity
-            const float g = fmaxf((st.c - cm) * kLog2e, -200.f);  // with s = t = 0 then
-            const float f = ex2(g);
+        if (cm > st.c + kLazy) {  // always at first: st.c is -infinity, s = t = 0
+            // (where a base is not a number the old sums vanish beside the new logit)
+            const float m = -base_of(cm), g = fmaxf(m - minus_b, -200.f), f = ex2(g);
             st.t = f * (st.t + g * st.s);
             st.s *= f;
             st.c = cm;
+            minus_b = m;
         }
         const float2 l2 = make_float2(kLog2e, kLog2e);
         float2 ss = make_float2(0.f, 0.f), tt = make_float2(0.f, 0.f);
         {
-            const float2 mc = make_float2(-st.c * kLog2e, -st.c * kLog2e);
+            const float2 mc = make_float2(minus_b, minus_b);
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
                 const float2 d = __ffma2_rn(make_float2(v[i], v[i + 1]), l2, mc);
@@ -213,14 +229,16 @@ struct Thread {
             }
         }
         // Not finite: a masked logit (0 times infinity), a value whose multiple by
-        // log2(e) is out of range, or a NaN. Again, difference first and cut off.
+        // log2(e) is out of range, or a NaN. Again, cut off, and difference first if
+        // there is no base.
         if (!(fabsf(tt.x + tt.y) < 1e30f)) {
-            const float ref = st.c == -INFINITY ? 0.f : st.c;
-            const float2 mc = make_float2(-ref, -ref);
+            const bool based = has_base(st.c);
+            const float ref = based || st.c == -INFINITY ? 0.f : st.c, off = based ? minus_b : 0.f;
+            const float2 mr = make_float2(-ref, -ref), mc = make_float2(off, off);
             ss = tt = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                float2 d = __fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), mc), l2);
+                float2 d = __ffma2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), mr), l2, mc);
                 // 2^-200 is 0 in f32: a masked logit adds 0; NaN stays
                 d.x = max_nan(d.x, -200.f);
                 d.y = max_nan(d.y, -200.f);
@@ -376,7 +394,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) row_kernel(const Lo
             const int64_t target_n = rn < a.M ? a.targets[rn] : -1;
             uint32_t xt2 = 0;
             if constexpr (sizeof(T) == 2) xt2 = pack2<T>(xt, xt);  // exact: xt is a logit (or infinity)
-            Thread th{{-INFINITY, 0.f, 0.f}, -INFINITY, row.c_lo + (int)threadIdx.x, 0};
+            Thread th{{-INFINITY, 0.f, 0.f}, INFINITY, -INFINITY, row.c_lo + (int)threadIdx.x, 0};
 #pragma unroll 1
             for (int c0 = row.c_lo; c0 < row.c_hi; c0 += kStageChunks) {
                 if (ok && !warp_bar_wait(full(st), ph)) {
@@ -571,12 +589,14 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) row_kernel(const Lo
             }
         }
         if (part == 0) {
-            const float ls = log2f(st.s);
             const bool nan = st.s != st.s, none = st.c == -INFINITY && !nan;
-            auto logp = [&](float x) { return nan ? NAN : x == -INFINITY ? -INFINITY : (x - st.c) - kLn2 * ls; };
+            const float ln = logf(st.s), rest = has_base(st.c) ? fmaf(st.c, kLog2e, -base_of(st.c)) : 0.f;
+            const float all_ln = fmaf(-kLn2, rest, ln);
+            // (neither a probability over 1 nor an entropy below 0 by rounding)
+            auto logp = [&](float x) { return nan ? NAN : x == -INFINITY ? -INFINITY : fminf((x - st.c) - all_ln, 0.f); };
             if (lane == 0) {
                 a.logprobs[r] = given ? logp(xt) : 0.f;
-                a.entropy[r] = nan ? NAN : none ? 0.f : kLn2 * (ls - st.t / st.s);
+                a.entropy[r] = nan ? NAN : none ? 0.f : fmaxf(fmaf(-kLn2, st.t / st.s, ln), 0.f);
                 a.ranks[r] = !given ? -1 : xt != xt ? 0 : above;
             }
             if (lane < a.k) {

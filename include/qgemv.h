@@ -414,7 +414,9 @@ QG_API int kv_compact_workspace_size(int64_t num_pages, size_t* bytes);
  * has log probabilities -infinity and entropy 0. A NaN makes a row's log
  * probabilities and entropy NaN and counts as the largest logit.
  * top_k <= min(32, V); with top_k = 0, top_values and top_ids may be NULL.
- * (+infinity makes them NaN too.) V <= 2^30. Sums are f32. */
+ * (+infinity makes them NaN too.) V <= 2^30. Sums are f32; log probabilities
+ * and entropies are as exact for rows far from 0 or dominated by one logit as
+ * for others, log probabilities never above 0 and entropies never below. */
 QG_API int token_logprobs(const void* logits, int dtype, int64_t row_stride,
                           const int64_t* targets, int64_t M, int64_t V, int top_k,
                           float* logprobs, float* entropy, int32_t* ranks, float* top_values,

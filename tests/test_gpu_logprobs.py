@@ -164,3 +164,79 @@ def test_nothing_to_do_and_refusals():
     for k in (-1, 33):
         with pytest.raises((ValueError, RuntimeError)):
             qg.token_logprobs(x, t, k)
+
+
+def adds(M, V, dtype):
+    """The longest chain of f32 additions of a sum: in a chunk of 32 bytes, a thread's chunks of its share of the row
+    (one of at most 8, at least 2 chunks each), 8 threads of a lane, 5 steps over the lanes, 3 over the shares."""
+    n, parts = 32 // dtype.itemsize, 1
+    while parts < 8 and M * parts * 2 <= 2 * torch.cuda.get_device_properties(0).multi_processor_count and V >= parts * 1024 * n:
+        parts *= 2
+    return n // 2 + -(-V // (256 * parts * n)) + 1 + 8 + 5 + 3
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("kind", ["one at 10", "one at 18", "one at 18.7", "one at 19.5", "one at 22", "one at 40", "offset 30",
+                                  "offset 1000", "offset 10000", "offset -10000", "masked 1000", "lowest -1000", "growing to 60"])
+@pytest.mark.parametrize("M,V", [(128, 32000), (1, 50021), (400, 9001)])
+def test_error_does_not_grow_with_the_logits(M, V, kind, dtype):
+    """Rows that one logit dominates, and rows far from 0. With u = 2^-24, e = (adds + 8) u bounds the relative error of a
+    sum of exponentials, each within 4 u and (d of size |d| rounded once) u |d|; H bounds the sums' mean |d|. A log
+    probability is off by e and its own three roundings, an entropy by e (1 + mean |d|) for each of its two sums."""
+    g = torch.Generator("cuda").manual_seed(V + len(kind))
+    *what, size = kind.split()
+    what, size = what[0], float(size)
+    x = torch.randn(M, V, generator=g, device="cuda") * (1 if what == "one" else 3)
+    if what == "one":
+        x[torch.arange(M, device="cuda"), torch.randint(0, V, (M,), generator=g, device="cuda")] = size
+    elif what == "growing":
+        x = x / 3 + torch.arange(V, device="cuda") * (size / V)
+    else:
+        x = x + size
+    x = x.to(dtype)
+    hidden = torch.rand(M, V, generator=g, device="cuda") < 0.5
+    if what == "masked":
+        x[hidden] = -math.inf
+    elif what == "lowest":
+        x[hidden] = torch.finfo(dtype).min
+    targets = torch.randint(0, V, (M,), generator=g, device="cuda")
+    targets[::2] = x[::2].float().argmax(1)
+    lp, h, _, top, _ = qg.token_logprobs(x, targets, 9)
+    ref = torch.log_softmax(x.double(), 1)
+    entropy = torch.special.entr(ref.exp()).sum(1)
+    u = 2.0**-24
+    e = (adds(M, V, dtype) + 8) * u
+    want = ref.gather(1, targets[:, None]).squeeze(1)
+    for got, exact in ((lp, want), (top, ref.sort(1, descending=True).values[:, :9])):
+        room = e + u * (3 * exact.abs() + 2 * entropy.view(-1, *[1] * (exact.dim() - 1)))
+        seen = ~torch.isinf(exact)
+        assert torch.equal(torch.isinf(got), ~seen)
+        assert ((got.double() - exact).abs() <= room)[seen].all(), float(((got.double() - exact).abs() - room)[seen].max())
+        assert (got <= 0).all()
+    assert ((h.double() - entropy).abs() <= 4 * e * (1 + entropy)).all(), float(((h.double() - entropy).abs() / (1 + entropy)).max() / e)
+    assert (h >= 0).all() and qg.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,V", [(1, 70), (3, 20000), (300, 3000)])
+def test_logits_next_to_the_largest_numbers(M, V, dtype):
+    """Logits whose multiple by log2(e) is out of range."""
+    most = torch.finfo(dtype).max
+    two = math.log(0.5)
+    for fill, some, want in ((-most, None, -math.log(V)), (most, None, -math.log(V)), (0.0, most, two), (-most, 3.0, two),
+                             (-most, most, two), (-math.inf, -most, two), (-math.inf, most, two), (-0.9 * most, 0.9 * most, two),
+                             (0.8 * most, most, two), (-most, -0.8 * most, two)):
+        x = torch.full((M, V), fill, dtype=dtype, device="cuda")
+        if some is not None:
+            x[:, [V // 3, V - 1]] = some
+        targets = torch.full((M,), V - 1, device="cuda")
+        targets[1::2] = 0
+        lp, h, r, top, ids = qg.token_logprobs(x, targets, 2)
+        tol = (adds(M, V, dtype) + 8) * 2.0**-24 + 3 * 2.0**-24 * abs(want)
+        assert ((lp[::2] - want).abs() <= tol).all() and ((top - want).abs() <= tol).all()
+        assert ((h + want).abs() <= 4 * tol * (1 - want)).all()
+        assert (r[::2] == 0).all() and ids[0].tolist() == ([0, 1] if some is None else [V // 3, V - 1])
+        if some is not None:  # -infinity where the difference passes f32's range
+            away = torch.tensor(fill, dtype=dtype).double() - torch.tensor(some, dtype=dtype).double()
+            assert torch.allclose(lp[1::2], away.float().cuda() + want, rtol=2.0**-20, atol=0.0)
+    assert qg.device_error() == 0
