@@ -124,14 +124,19 @@ double number(PyObject* o) {
     return v;
 }
 
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v != 0;
+}
+
 qg_stream_t stream_of(PyObject* o) {
     if (o == Py_None) return reinterpret_cast<qg_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
-    if (PyLong_Check(o)) return reinterpret_cast<qg_stream_t>(PyLong_AsVoidPtr(o));
-    PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
+    PyObject* v = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
     if (!v) throw Raised{};
     void* p = PyLong_AsVoidPtr(v);
     Py_DECREF(v);
-    if (PyErr_Occurred()) throw Raised{};
+    if (!p && PyErr_Occurred()) throw Raised{};
     return reinterpret_cast<qg_stream_t>(p);
 }
 
@@ -318,7 +323,7 @@ PyObject* attn_paged(PyObject* const* a) {
     if (a[7] != Py_None) {
         lse = dense(a[7], "lse", ScalarType::Float);
         shape(lse, "lse", {T, Hq});
-    } else if (PyObject_IsTrue(a[12])) {
+    } else if (truth(a[12])) {
         lse = make({T, Hq}, ScalarType::Float, q);
     }
     const int64_t max_new = a[8] == Py_None ? T : integer(a[8]);

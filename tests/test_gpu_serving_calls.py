@@ -258,3 +258,14 @@ def test_overlapped_calls_give_the_same(pdl, tmp_path):
     for a, b in zip(torch.load(tmp_path / "out.pt"), chain(), strict=True):
         assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
     assert qg.device_error() == 0
+
+
+def test_arguments_that_are_no_streams_or_truth_values():
+    x, args = torch.ones(2, 128, device="cuda"), attention(50)
+    with pytest.raises(OverflowError):
+        qg.quantize_fp8_b128(x, stream=1 << 200)
+    with pytest.raises(AttributeError):
+        qg.quantize_fp8_b128(x, stream="0")
+    with pytest.raises(RuntimeError):  # a tensor of several values
+        qg.attn_paged(*args, return_lse=x)
+    assert qg.quantize_fp8_b128(x, stream=0)[1].shape == (2, 1)
