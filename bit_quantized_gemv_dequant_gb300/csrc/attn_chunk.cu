@@ -30,6 +30,9 @@ using fp8::tmem_wait32;
 // The maximum m follows the scores lazily: O and the sum are rescaled only when
 // a row's new maximum is over 2^8 times the one in use (probabilities up to
 // 2^8 cost nothing in f16 or bf16, and the quotient by the sum is the same).
+// Probabilities enter the product with V rounded to its type, which the tensor
+// cores ask of both operands; their remainders as a second product would be half as
+// much tensor work again. It adds a quarter to the error of the output's own rounding.
 // Rows past the last one repeat it; their results are not stored.
 //
 //   warps 0-3, 4-7  softmax and output of block 0, 1; they also gather their

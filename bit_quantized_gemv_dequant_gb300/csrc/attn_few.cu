@@ -18,8 +18,16 @@ namespace {
 // 64 / (4 / RB) keys w / RB of each step; warps with the same rows and other
 // keys keep their own softmax and meet at the end of the segment.
 //
+// Probabilities enter the product with V in 16 bits. HALF, for at most 8 rows:
+// a product's rows 8-15 then hold what the rounding took off rows 0-7, and the two
+// sums are added at the end, so outputs are as exact as with f32 probabilities
+// at no cost (half the exponentials, in fact: 327.5 us for 128 single tokens
+// without, 340 with a cap and 315). With more rows the remainders would be products
+// of their own: 17 % of 64 rows' time (430 and 500 us), for errors a quarter larger
+// than those of the output's own rounding; not taken.
+//
 // With the joining kernel: 128 single tokens over 65 to 8192 keys, 32/8 heads of
-// 128: 327 us, 6.63 TB/s; one token over 700 keys: 7.6 us, most of it the
+// 128: 325 us, 6.68 TB/s; one token over 700 keys: 7.5 us, most of it the
 // latency of finding the step, its page and its keys, and of a second launch.
 constexpr int kKT = 64;
 constexpr int kWarps = 4;
@@ -65,13 +73,14 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
     return (uint32_t)((chunk >> 3) * Geo<D>::kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-template <class T, int D, int RB, bool CAP>
+template <class T, int D, int RB, bool HALF, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                const Work w) {
     using G = Geo<D>;
     constexpr int RT = 16 * RB, KS = kWarps / RB, KW = kKT / KS;  // keys of a step per warp
     constexpr int NT = D / 8;                                     // 8-column tiles of the output
+    constexpr int RH = HALF ? 1 : 2;                              // rows g, g + 8 of a lane
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -151,9 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Seq s = walk.s;
         // Q as the products' left operand: rows g and g + 8 of this warp's block.
         uint32_t q[D / 16][4];
-        int pos[2];
+        int pos[RH];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < RH; ++h) {
             const int r = r0 + rb * 16 + g + 8 * h;
             const int tok = min(r, s.rows - 1) / w.group;
             pos[h] = s.ctx - s.n + tok;
@@ -164,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < D / 16; ++k) {
                 q[k][h] = __ldg(qp + k * 8);
                 q[k][2 + h] = __ldg(qp + k * 8 + 4);
+                if (HALF) q[k][1] = q[k][3] = 0;
             }
         }
         const int pos_lo = s.ctx - s.n + r0 / w.group;  // of the tile's rows
@@ -199,13 +209,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma<T>(x[2 * nb + 1], q[k], b[2], b[3]);
                 }
             }
-            scores<CAP, KW / 2>(w, [&](int e) { return x[e / 4][e % 4]; }, [&](int e, float v) { x[e / 4][e % 4] = v; });
+            constexpr int E = 2 * RH;  // a lane's scores of 8 keys
+            scores<CAP, KW / 8 * E>(w, [&](int e) { return x[e / E][e % E]; }, [&](int e, float v) { x[e / E][e % E] = v; });
             const bool masked = j0 + KW - 1 > pos_lo || (w.a.window && j0 <= pos_hi - w.a.window);
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int nt = 0; nt < KW / 8; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < E; ++e) {
                     float v = x[nt][e];
                     if (masked) {
                         const int j = j0 + nt * 8 + c2 + (e & 1), p = pos[e >> 1];
@@ -216,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             float keep[2], ref[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < RH; ++h) {
                 top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 1));
                 top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 2));
                 const float mn = fmaxf(m[h], top[h]);
@@ -225,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m[h] = mn;
                 l[h] *= keep[h];
             }
+            if (HALF) keep[1] = keep[0];
             if (__any_sync(0xFFFFFFFFu, keep[0] != 1.f || keep[1] != 1.f)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -239,11 +251,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     float* v = x[2 * nb + h];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < E; ++e) {
                         v[e] = ex2(v[e] - ref[e >> 1]);
                         l[e >> 1] += v[e];
                     }
                     pa[2 * h] = pack2<T>(v[0], v[1]);
+                    if constexpr (HALF) {  // the remainders
+                        const float2 r = unpack2<T>(pa[2 * h]);
+                        v[2] = v[0] - r.x;
+                        v[3] = v[1] - r.y;
+                    }
                     pa[2 * h + 1] = pack2<T>(v[2], v[3]);
                 }
                 // Places that no row sees may hold anything, NaN included.
@@ -277,18 +294,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         // --------------------------------------------------- end of a segment
+        if constexpr (HALF) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+            for (int nt = 0; nt < NT; ++nt) {
+                // (an infinite value stays one: with a remainder of 0 or less it would be NaN)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) o[nt][e] += isinf(o[nt][e]) ? 0.f : o[nt][2 + e];
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < RH; ++h) {
             l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
             l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
         }
         if ((lane & 3) == 0) {
             mls[warp * 16 + g] = make_float2(m[0], l[0]);
-            mls[warp * 16 + g + 8] = make_float2(m[1], l[1]);
+            if (!HALF) mls[warp * 16 + g + 8] = make_float2(m[1], l[1]);
         }
         float* mine = merge + warp * 16 * D;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < RH; ++h) {
             // 8-float groups rotate by the row, so that a warp's stores spread over the banks
             const int r = g + 8 * h;
 #pragma unroll
@@ -343,10 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <class T, int D, int RB, bool CAP>
+template <class T, int D, int RB, bool HALF, bool CAP>
 int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     static int configured[64] = {0};
-    auto kern = few_kernel<T, D, RB, CAP>;
+    auto kern = few_kernel<T, D, RB, HALF, CAP>;
     if (!configured[dc.device]) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
         if (e != cudaSuccess) return cuda_fail(e);
@@ -361,13 +386,14 @@ int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
     return launch_join<T, D, 16 * RB, kKT, 1, 12>(w, s);
 }
 
-template <class T, int D, int RB>
+template <class T, int D, int RB, bool HALF = false>
 int launch_cap(const DevCtx& dc, const Work& w, cudaStream_t s) {
-    return w.a.softcap > 0.f ? launch_one<T, D, RB, true>(dc, w, s) : launch_one<T, D, RB, false>(dc, w, s);
+    return w.a.softcap > 0.f ? launch_one<T, D, RB, HALF, true>(dc, w, s) : launch_one<T, D, RB, HALF, false>(dc, w, s);
 }
 
 template <class T, int D>
 int launch_rows(const DevCtx& dc, const Work& w, int rb, cudaStream_t s) {
+    if ((long long)w.a.max_new * w.group <= 8) return launch_cap<T, D, 1, true>(dc, w, s);
     return rb == 1 ? launch_cap<T, D, 1>(dc, w, s) : rb == 2 ? launch_cap<T, D, 2>(dc, w, s)
                                                              : launch_cap<T, D, 4>(dc, w, s);
 }

@@ -327,8 +327,10 @@ QG_API int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* 
  *    <= 128.
  *  - max_new: no sequence has more new tokens than this (rows past it are
  *    not computed and the device error word says so).
- *  - Scores, sums and outputs are accumulated in f32; the probabilities
- *    enter the product with V rounded to `dtype`.
+ *  - Scores, sums and outputs are accumulated in f32. The probabilities
+ *    enter the product with V rounded to `dtype`; if max_new * q_heads /
+ *    kv_heads is at most 8, with their remainders, which makes them exact to
+ *    2^-16.
  *  - workspace: attn_paged_workspace_size() bytes. */
 QG_API int attn_paged(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
                       const int32_t* page_table, const int32_t* q_offsets,

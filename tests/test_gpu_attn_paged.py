@@ -388,3 +388,39 @@ def test_no_new_tokens_allowed():
     assert qg.device_error() == 32 and (out == 7).all()
     qg.attn_paged(*args[:4], torch.zeros_like(args[4]), args[5], out=out, max_new=0)
     assert qg.device_error() == 0 and (out == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,new", [(8, 1, 1), (4, 4, 1), (12, 4, 2), (4, 2, 4), (2, 2, 8)])
+def test_few_rows_are_as_exact_as_their_rounding(hq, hkv, new, d, dtype):
+    """Up to 8 rows per key head: the output is a rounding of a number that is off by 2^-16 (probabilities) + 1e-5 (1 + S)
+    (scores and sums) of A = sum_j p_j |v_j|, and 2^-24 n max|v| below f16's normal range: what its distance from the
+    exact one exceeds half the spacing of the type's numbers there by. (A is often many times the output.)"""
+    ctx = [8, 9, 13, 20, 33, 70, 150, 700]
+    args = list(make(19, [new] * len(ctx), ctx, hq, hkv, d, 16, dtype))
+    args[0] = args[0] * 0.1
+    out = qg.attn_paged(*args, max_new=new)
+    ref, mass, _, S, vm = reference(*args, d**-0.5, 0.0, 0)
+    # numbers from 2^e to 2^(e + 1) are 2^e ulp apart, and the reference may round up to the next 2^e
+    exponent = torch.frexp(torch.maximum(out.double().abs(), ref.abs())).exponent - 1
+    spacing = torch.ldexp(torch.full_like(ref, 2 * UNIT[dtype]), exponent)
+    if dtype == torch.float16:
+        spacing = spacing.clamp(min=2.0**-24)
+    beyond = (out.double() - ref).abs() - spacing / 2
+    room = (2.0**-16 + 1e-5 * (1 + S)) * mass + (2.0**-24 * max(ctx) * vm if dtype == torch.float16 else 0.0)
+    assert (beyond <= room).all(), float((beyond - room).max())
+    assert qg.device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (32, 2)])
+def test_infinite_values_stay_infinite(hq, hkv):
+    args = make(20, [1, 1], [40, 300], hq, hkv, 64, 16, torch.bfloat16)
+    good = qg.attn_paged(*args, max_new=1)
+    v, table = args[2], args[3]
+    v[int(table[0, 1]), 1, 3, 5], v[int(table[1, 2]), 0, 7, 9] = math.inf, -math.inf
+    out, group = qg.attn_paged(*args, max_new=1), hq // hkv
+    assert (out[0, group:, 5] == math.inf).all() and (out[1, :group, 9] == -math.inf).all()
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[0, group:, 5] = same[1, :group, 9] = False
+    assert torch.equal(out[same], good[same])
