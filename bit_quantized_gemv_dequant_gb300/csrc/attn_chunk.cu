@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (threadIdx.x == 0) walk.note(cuts, kRT, blockIdx.x);
                 if (live) {
                     if (!walk.whole) w.ml[pt] = make_float2(m, l);
-                    else if (w.a.lse) w.a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                    else if (w.a.lse) w.a.lse[at] = l == 0.f ? -INFINITY : fmaf(m, w.to_ln, logf(l));
                 }
             }
         }

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(static_cast<T*>(w.a.out) + at * D + nt * 8) = u;
                 if (ll == ll && !all_finite(v)) w.notes[blockIdx.x].bad = 1;
                 if (w.a.lse && nt == 0)
-                    w.a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+                    w.a.lse[at] = ll == 0.f ? -INFINITY : fmaf(mm, w.to_ln, logf(ll));
             } else {
                 const long long at = ((long long)blockIdx.x * 2 + walk.slot) * RT + r;
                 float4* dst = reinterpret_cast<float4*>(w.part + at * D + nt * 8);

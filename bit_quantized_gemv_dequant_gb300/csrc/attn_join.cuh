@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(w.a.out) + at * D + lane * E);
 #pragma unroll
         for (int e = 0; e < E; e += 2) out[e / 2] = pack2<T>(v[i][e] * inv, v[i][e + 1] * inv);
-        if (w.a.lse && lane == 0) w.a.lse[at] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
+        if (w.a.lse && lane == 0) w.a.lse[at] = l[i] == 0.f ? -INFINITY : fmaf(m[i], w.to_ln, logf(l[i]));
         redo |= l[i] == l[i] && !all_finite(v[i]);
     }
     if constexpr (REDO) {

@@ -40,6 +40,8 @@ int attn_launch(const DevCtx& dc, const AttnArgs& a, void* ws, cudaStream_t s) {
         w.small = 0.5f / std::fabs(w.cap_in);
         w.cap_out = a.softcap * kLog2e;
     }
+    w.to_ln = a.softcap > 0.f ? (float)((double)a.softcap / w.cap_out) : (float)((double)a.scale / w.scale_log2);
+    if (!std::isnormal(w.to_ln)) w.to_ln = 0.69314718f;  // a scale of 0, or one out of range
     w.err = dc.err;
     w.ctas = dc.num_sms;
     const int rt = row_tile(a);

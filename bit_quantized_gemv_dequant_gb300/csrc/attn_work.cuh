@@ -26,6 +26,7 @@ struct Work {
     AttnArgs a;
     int group;
     float scale_log2;        // scale * log2(e): scores are in base 2
+    float to_ln;             // what a score in base 2 is in base e, by the factor as rounded
     float small;             // products up to this in size are far from the cap
     float cap_in, cap_out;   // scale / softcap, softcap * log2(e)
     float* part;             // [G][2][RT][D] unnormalised outputs of cut row tiles
