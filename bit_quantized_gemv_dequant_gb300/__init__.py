@@ -406,8 +406,11 @@ def attn_paged(q, k_cache, v_cache, page_table, q_offsets, context_lens, out=Non
     int32 [batch, width]; q_offsets int32 [batch + 1]: sequence b's new tokens
     are rows q_offsets[b] .. q_offsets[b + 1] - 1; context_lens int32 [batch]:
     its keys, the new ones included. max_new: the most new tokens that any
-    sequence has (default: all of q's rows). scale: default head_dim ** -0.5.
-    softcap > 0 caps the scores, window > 0 limits how far back a row sees."""
+    sequence has (default: all of q's rows); the kernel is chosen by it, so say
+    1 for a batch of single tokens (a quarter faster than the default for 128).
+    scale: default head_dim ** -0.5. softcap > 0 caps the scores, window > 0
+    limits how far back a row sees. Rows at or after q_offsets[batch] are left as
+    they are."""
     return (_SERVING or _calls()).attn_paged(q, k_cache, v_cache, page_table, q_offsets, context_lens, out, lse,
                                                 max_new, scale, softcap, window, return_lse, workspace, stream)
 

@@ -44,8 +44,8 @@ using fp8::tmem_wait32;
 // thread: a row's 128 scores stay in them.
 //
 // With the joining kernel: 2 x 2048 new tokens over 16384 and 8200 keys, 32/8
-// heads of 128, bf16: 554 us, 1.37 PFLOP/s, at the power limit; tensor pipes 52 %
-// busy. 13 sequences of up to 130 new tokens, 20/4 heads of 64, capped, windowed:
+// heads of 128, bf16: 556 to 583 us, 1.30 to 1.36 PFLOP/s, by the GPU: at the power
+// limit (SM clock 1965 MHz); tensor pipes 52 % busy. 13 sequences of up to 130 new tokens, 20/4 heads of 64, capped, windowed:
 // 43 us, latency from end to end (4 or 5 steps per CTA).
 constexpr int kKT = 128;
 constexpr int kRT = 256;

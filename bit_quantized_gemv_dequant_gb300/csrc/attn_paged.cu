@@ -17,8 +17,13 @@ size_t part_bytes(const DevCtx& dc, int rt, int d) {
 
 // Rows per tile, by the most rows that a sequence can have: up to 64 the
 // streaming kernel, whose tile is the least that holds them, else the
-// tensor-core kernel for the whole batch (its single tokens too: a step with
-// one row costs it little more than the bytes of the keys and values).
+// tensor-core kernel for the whole batch, whose steps take as long for one row as
+// for 128. The bound counts, not the rows: 128 single tokens over 65 to 8192 keys
+// take 322 us with max_new = 1, 438 with 8 (32 rows), 727 with 16 (64 rows) and
+// 401 with 17 or more. Both sides of the last border, 32/8 heads of 128: one
+// sequence of 16 new tokens over 4000 keys 21 us here and 35 there, eight over 1000
+// 26.5 and 27.7; 64 over 8192 keys 726 and 373, so for much work the border lies
+// too high (the host does not know the lengths).
 int row_tile(const AttnArgs& a) {
     const long long rows = (long long)a.max_new * (a.hq / a.hkv);
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;

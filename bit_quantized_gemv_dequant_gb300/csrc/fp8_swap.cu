@@ -25,7 +25,8 @@ namespace {
 // size the GPU can place at once (plan() below). Measured, product alone:
 //   N = K = 4096, M = 1         6.3 us  2.7 TB/s of w (launch, first loads, joining)
 //   N = 2200, K = 5200, M = 33  6.8 us  1.7 TB/s
-//   N = K = 12288, M = 1        28.0 us 5.4 TB/s (96 SMs load)
+//   N = K = 12288, M = 1        28.0 us 5.4 TB/s (96 of 152 SMs load: a split is the
+//                               same for all tiles, and two each would not fit)
 //
 // The split's partial sums meet in shared memory over the cluster, each CTA
 // adding up its share of the rows of a in the order of the split: the result

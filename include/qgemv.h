@@ -326,7 +326,8 @@ QG_API int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* 
  *  - head_dim 64 or 128; q_heads a multiple of kv_heads, q_heads / kv_heads
  *    <= 128.
  *  - max_new: no sequence has more new tokens than this (rows past it are
- *    not computed and the device error word says so).
+ *    not computed and the device error word says so). The kernel is chosen
+ *    by it: a bound near the truth is faster.
  *  - Scores, sums and outputs are accumulated in f32. The probabilities
  *    enter the product with V rounded to `dtype`; if max_new * q_heads /
  *    kv_heads is at most 8, with their remainders, which makes them exact to
