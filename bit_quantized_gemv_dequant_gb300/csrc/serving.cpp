@@ -165,8 +165,11 @@ Scratch scratch(size_t need, PyObject* workspace, const Tensor& like, qg_stream_
     }
     if (need == 0) return {};
     cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
-    // (the legacy stream answers with an error while another stream is captured)
-    if (cudaStreamIsCapturing(reinterpret_cast<cudaStream_t>(s), &status) != cudaSuccess) (void)cudaGetLastError();
+    if (cudaStreamIsCapturing(reinterpret_cast<cudaStream_t>(s), &status) != cudaSuccess) {
+        // the legacy stream, while another one is captured: it is not itself
+        (void)cudaGetLastError();
+        status = cudaStreamCaptureStatusNone;
+    }
     if (status != cudaStreamCaptureStatusNone) {
         const Tensor t = make({(int64_t)need}, ScalarType::Byte, like);
         return {t, t.data_ptr(), need};
