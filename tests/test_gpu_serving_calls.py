@@ -269,3 +269,19 @@ def test_arguments_that_are_no_streams_or_truth_values():
     with pytest.raises(RuntimeError):  # a tensor of several values
         qg.attn_paged(*args, return_lse=x)
     assert qg.quantize_fp8_b128(x, stream=0)[1].shape == (2, 1)
+
+
+def test_first_call_of_a_thread_is_captured():
+    args = attention(60)
+    want = qg.attn_paged(*args)
+    torch.cuda.synchronize()
+
+    def work(_):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = qg.attn_paged(*args)
+        graph.replay()
+        torch.cuda.synchronize()
+        return out
+
+    assert torch.equal(in_threads(work, 1)[0], want)
