@@ -424,3 +424,27 @@ def test_infinite_values_stay_infinite(hq, hkv):
     same = torch.ones_like(out, dtype=torch.bool)
     same[0, group:, 5] = same[1, :group, 9] = False
     assert torch.equal(out[same], good[same])
+
+
+@pytest.mark.parametrize("scale", [64**-0.5, 128**-0.5, 0.1, 0.3, 0.7, 0.011, 1.7, 3.1, 0.0475])
+@pytest.mark.parametrize("new", [1, 600])
+def test_log_sums_of_one_key_are_its_scores(new, scale):
+    """With a window of one key the log sum is scale * product, products exact in f32: three roundings (the product with the
+    scale, the factor back to base e, the product with that), 3 units of 2^-24 of the score. The scale is an f32."""
+    n = 1200
+    g = torch.Generator("cuda").manual_seed(21)
+    a, b = (torch.randint(1024, 2048, (n,), generator=g, device="cuda") / 1024.0 for _ in range(2))
+    q = torch.zeros(n, 1, 64, dtype=torch.float16, device="cuda")
+    k = torch.zeros(n // 16, 1, 16, 64, dtype=torch.float16, device="cuda")
+    q[:, 0, 7], k.view(n, 64)[:, 7] = a.half(), b.half()
+    pages = torch.arange(n // 16, dtype=torch.int32, device="cuda")
+    if new == 1:
+        table, off = pages.expand(n, -1).contiguous(), torch.arange(n + 1, dtype=torch.int32, device="cuda")
+        lens = torch.arange(1, n + 1, dtype=torch.int32, device="cuda")
+    else:
+        table, off = pages.expand(2, -1).contiguous(), torch.tensor([0, 600, n], dtype=torch.int32, device="cuda")
+        lens = torch.tensor([600, n], dtype=torch.int32, device="cuda")
+    _, lse = qg.attn_paged(q, k, k, table, off, lens, max_new=new, scale=scale, window=1, return_lse=True)
+    score = a.double() * b.double() * torch.tensor(scale, dtype=torch.float32).double().item()
+    assert ((lse[:, 0].double() - score).abs() <= 3.001 * 2.0**-24 * score).all(), float(((lse[:, 0].double() - score).abs() / score).max() * 2**24)
+    assert qg.device_error() == 0
