@@ -1,6 +1,7 @@
 """Quantized GEMV with fused dequantization for GB300 (sm_103a), and the
-operators around it in a serving step: the block-scaled fp8 product, attention
-over a paged cache, the upkeep of its pages and token log probabilities.
+operators around it in a serving step: the block-scaled fp8 products, norms and
+gates, attention over a paged cache, the upkeep of its pages and token log
+probabilities.
 
 The compute lives in the CUDA library libqgemv.so (C ABI in include/qgemv.h);
 this module is a thin binding over it with the same names, by ctypes and, for
@@ -53,8 +54,9 @@ EXPORTS = ("qgemv_q4_0", "qgemv_dual_q4_0", "qgemv_q4_k", "qmm_affine", "qkv_spl
            "qg_status_string", "qg_last_cuda_error", "qg_device_error",
            "qg_selftest_wait_timeout", "qg_set_option", "qg_get_option",
            "qgemv_q4_k_noalloc", "qg_prepare_af4_g64", "qmm_af4_g64", "qgemv_dual_q4_0_host",
-           "quantize_fp8_b128", "qmm_fp8_b128", "qmm_fp8_b128_workspace_size", "attn_paged", "attn_paged_workspace_size",
-           "kv_append", "kv_copy_pages", "kv_fork", "kv_fork_workspace_size", "kv_free",
+           "quantize_fp8_b128", "qmm_fp8_b128", "qmm_fp8_b128_workspace_size", "qmm_fp8_b128_grouped",
+           "qmm_fp8_b128_grouped_workspace_size", "rms_norm", "rms_norm_fp8_b128", "silu_mul", "silu_mul_fp8_b128",
+           "attn_paged", "attn_paged_workspace_size", "kv_append", "kv_append_rope", "kv_copy_pages", "kv_fork", "kv_fork_workspace_size", "kv_free",
            "kv_compact", "kv_compact_workspace_size", "token_logprobs")
 
 _LIB = None
@@ -105,9 +107,16 @@ def lib():
             "quantize_fp8_b128": [P, I, I64, P, P, I64, I64, P],
             "qmm_fp8_b128": [P, P, P, P, P, I, I64, I64, I64, P, SZ, P],
             "qmm_fp8_b128_workspace_size": [I64, I64, I64, C.POINTER(SZ)],
+            "qmm_fp8_b128_grouped": [P, P, P, P, P, P, I, I64, I64, I64, I64, P, SZ, P],
+            "qmm_fp8_b128_grouped_workspace_size": [I64, I64, I64, I64, C.POINTER(SZ)],
+            "rms_norm": [P, I, I64, P, I, I64, P, I, C.c_float, C.c_float, P, I, P, I64, I64, I64, P],
+            "rms_norm_fp8_b128": [P, I, I64, P, I, I64, P, I, C.c_float, C.c_float, P, P, P, I64, I64, I64, P],
+            "silu_mul": [P, I64, P, I64, I, P, I, I64, I64, P],
+            "silu_mul_fp8_b128": [P, I64, P, I64, I, P, P, I64, I64, P],
             "attn_paged": [P, I64] + [P] * 7 + [I] + [I64] * 9 + [C.c_float] * 2 + [I64, P, SZ, P],
             "attn_paged_workspace_size": [I64] * 6 + [C.POINTER(SZ)],
             "kv_append": [P, P, I64, I64, I, P, P, I, P] + [I64] * 5 + [P],
+            "kv_append_rope": [P, P, P, I64, I64, I64, I, P, P, I64, I, P, P, P, I, P] + [I64] * 6 + [P],
             "kv_copy_pages": [P, I64, I64, I64, P, P, I64, P],
             "kv_fork": [P] + [I64] * 4 + [P] * 3 + [I64, I64, P, I64, P, P, P, P, SZ, P],
             "kv_fork_workspace_size": [I64, C.POINTER(SZ)],
@@ -394,6 +403,45 @@ def qmm_fp8_b128(a, a_scales, w, w_scales, y=None, *, out_dtype=torch.float32, w
     return (_SERVING or _calls()).qmm_fp8_b128(a, a_scales, w, w_scales, y, out_dtype, workspace, stream)
 
 
+def qmm_fp8_b128_grouped(a, a_scales, w, w_scales, offsets, y=None, *, out_dtype=torch.float32, workspace=None,
+                         stream=None):
+    """qmm_fp8_b128 for a layer of experts: rows offsets[e] .. offsets[e + 1] - 1
+    of a [M, K] times w[e] of w [experts, N, K] (scales [experts, ceil(N / 128),
+    ceil(K / 128)]); offsets int32 [experts + 1]. Rows of y [M, N] that no expert
+    has are left as they are."""
+    return (_SERVING or _calls()).qmm_fp8_b128_grouped(a, a_scales, w, w_scales, offsets, y, out_dtype, workspace,
+                                                       stream)
+
+
+def rms_norm(x, weight=None, residual=None, out=None, residual_out=None, *, eps=1e-6, weight_offset=0.0,
+             out_dtype=None, stream=None):
+    """h / sqrt(mean(h^2) + eps) * (weight_offset + weight) of the rows h = x (+
+    residual) of x [M, K] (its and the residual's rows may lie apart), in
+    out_dtype (default: x's); weight [K], or None for a factor of 1. With a
+    residual (of x's type or float32): (out, residual_out), the latter h in the
+    residual's type, which may be the residual itself."""
+    return (_SERVING or _calls()).rms_norm(x, weight, residual, out, residual_out, eps, weight_offset, out_dtype, stream)
+
+
+def rms_norm_fp8_b128(x, weight=None, residual=None, codes=None, scales=None, residual_out=None, *, eps=1e-6,
+                      weight_offset=0.0, stream=None):
+    """rms_norm with its output as quantize_fp8_b128 gives it: (codes, scales), or
+    (codes, scales, residual_out) with a residual."""
+    return (_SERVING or _calls()).rms_norm_fp8_b128(x, weight, residual, codes, scales, residual_out, eps, weight_offset,
+                                                    stream)
+
+
+def silu_mul(gate, up, out=None, *, out_dtype=None, stream=None):
+    """up * gate / (1 + exp(-gate)) of gate, up [M, K] of one type (rows may lie
+    apart, as halves of one product's rows), in out_dtype (default: theirs)."""
+    return (_SERVING or _calls()).silu_mul(gate, up, out, out_dtype, stream)
+
+
+def silu_mul_fp8_b128(gate, up, codes=None, scales=None, *, stream=None):
+    """silu_mul with its output as quantize_fp8_b128 gives it: (codes, scales)."""
+    return (_SERVING or _calls()).silu_mul_fp8_b128(gate, up, codes, scales, stream)
+
+
 def attn_paged(q, k_cache, v_cache, page_table, q_offsets, context_lens, out=None, lse=None, *,
                max_new=None, scale=None, softcap=0.0, window=0, return_lse=False, workspace=None,
                stream=None):
@@ -421,6 +469,17 @@ def kv_append(k, v, k_cache, v_cache, slots, *, stream=None):
     [num_pages, kv_heads, page_size, head_dim], rounded to their type. slots
     int64 [tokens]: page * page_size + place of each row; negative: skipped."""
     return (_SERVING or _calls()).kv_append(k, v, k_cache, v_cache, slots, stream)
+
+
+def kv_append_rope(q, k, v, positions, inv_freq, k_cache, v_cache, slots, q_out=None, *, interleaved=False,
+                   stream=None):
+    """kv_append with keys, and queries, rotated on the way: pair i of row t of q
+    [tokens, q_heads, head_dim] (or None) and k by the angle positions[t] (int64)
+    * inv_freq[i] (float32). The pairs are the first 2 * len(inv_freq) values of a
+    head: i and i + len(inv_freq), or with interleaved 2 i and 2 i + 1. Returns
+    the rotated q, dense, in the cache's type (None without q)."""
+    return (_SERVING or _calls()).kv_append_rope(q, k, v, positions, inv_freq, k_cache, v_cache, slots, q_out, interleaved,
+                                                 stream)
 
 
 def kv_copy_pages(cache, src, dst, *, stream=None):

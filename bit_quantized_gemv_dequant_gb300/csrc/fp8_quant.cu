@@ -1,13 +1,11 @@
 // quantize_fp8_b128: one e4m3 code per value and one f32 scale per 128 values
 // of a row.
-#include <cuda_fp8.h>
-
-#include "serve_common.cuh"
+#include "fp8_code.cuh"
 
 namespace qg {
 namespace {
 
-constexpr int kBlock = 128;   // values per scale
+constexpr int kBlock = kFp8Block;
 constexpr int kThreads = 256;
 
 // scale = max |x| / 448, code = e4m3_rn(x / scale), both divisions correctly
@@ -16,39 +14,6 @@ constexpr int kThreads = 256;
 // a NaN reaches the scale. PER values per lane, which are 16 bytes where the
 // rows allow it (PER = 8 for 16-bit types), 128 / PER lanes per block; bound by
 // the bytes of x and the codes (and by latency for few rows).
-//
-// A division per value would bound the kernel instead. With r = 1 / scale
-// correctly rounded, q' = q + r (x - scale q) after one such step is within an
-// ulp of the quotient and after another the correctly rounded one (Markstein's
-// theorem); the remainders are exact as long as nothing underflows, which the
-// limits on scale see to for every quotient that does not end as code 0.
-// The codes of PER values, from -x (so that a zero keeps its sign through the
-// steps).
-template <int PER>
-__device__ __forceinline__ void encode(const float (&minus_x)[PER], float scale, uint32_t (&code)[PER / 4]) {
-    float2 q[PER / 2];
-    const bool plain = scale > 0x1p-80f && scale < 0x1p80f && (__float_as_uint(scale) & 0x7FFFFFu) != 0x7FFFFFu;
-    if (plain) {
-        const float rcp = __frcp_rn(scale);
-        const float2 mr = make_float2(-rcp, -rcp), s2 = make_float2(scale, scale);
-#pragma unroll
-        for (int i = 0; i < PER / 2; ++i) {
-            const float2 mx = make_float2(minus_x[2 * i], minus_x[2 * i + 1]);
-            q[i] = __fmul2_rn(mx, mr);
-            q[i] = __ffma2_rn(__ffma2_rn(s2, q[i], mx), mr, q[i]);
-            q[i] = __ffma2_rn(__ffma2_rn(s2, q[i], mx), mr, q[i]);
-        }
-    } else {  // far from 1, infinite, NaN, or a significand of ones
-#pragma unroll
-        for (int i = 0; i < PER / 2; ++i)
-            q[i] = make_float2(__fdiv_rn(minus_x[2 * i], -scale), __fdiv_rn(minus_x[2 * i + 1], -scale));
-    }
-#pragma unroll
-    for (int i = 0; i < PER / 4; ++i)
-        code[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(q[2 * i], __NV_SATFINITE, __NV_E4M3) |
-                  (uint32_t)__nv_cvt_float2_to_fp8x2(q[2 * i + 1], __NV_SATFINITE, __NV_E4M3) << 16;
-}
-
 template <class T, int PER, bool VEC, int kDeep>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(const T* __restrict__ x, long long stride, uint8_t* __restrict__ codes,
@@ -111,10 +76,9 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int i = kLanes / 2; i; i >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
         }
-        float scale = __fdiv_rn(__uint_as_float(top), 448.f);
-        if (scale == 0.f) scale = 1.f;
+        const float scale = fp8_scale(top);
         uint32_t code[PER / 4];
-        encode<PER>(v, scale, code);
+        fp8_encode<PER>(v, scale, code);
         if (at_m[d] >= M) continue;
         uint8_t* out = codes + (long long)at_m[d] * K + at_k[d];
         if (VEC) {

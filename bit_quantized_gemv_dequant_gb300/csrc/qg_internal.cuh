@@ -342,6 +342,54 @@ struct LogprobArgs {
 };
 int logprobs_launch(const DevCtx& dc, const LogprobArgs& a, cudaStream_t s);
 
+// Row norms and gates (rms_norm.cu, silu_mul.cu). scales set: codes go to y.
+struct NormArgs {
+    const void *x, *res, *w;  // res, w: may be null
+    void *y, *res_out;
+    float* scales;
+    long long x_stride, res_stride, res_out_stride;
+    int x_dtype, res_dtype, w_dtype, y_dtype;
+    long long M, K;
+    float eps, offset;
+};
+int norm_launch(const NormArgs& a, cudaStream_t s);
+struct GateArgs {
+    const void *gate, *up;
+    void* y;
+    float* scales;
+    long long gate_stride, up_stride;
+    int x_dtype, y_dtype;
+    long long M, K;
+};
+int gate_launch(const GateArgs& a, cudaStream_t s);
+
+// Rotation by position on the way into a paged cache (kv_rope.cu).
+struct RopeArgs {
+    const void *q, *k, *v;  // q: may be null, hq is 0 then
+    long long q_stride, k_stride, v_stride;
+    int x_dtype, cache_dtype;
+    const int64_t *positions, *slots;
+    const float* inv_freq;
+    void *q_out, *k_cache, *v_cache;
+    long long tokens, num_pages;
+    int hq, hkv, d, rot, page_size;
+    bool interleaved;
+};
+int kv_append_rope_launch(const DevCtx& dc, const RopeArgs& a, cudaStream_t s);
+
+// fp8 products of rows grouped by expert (fp8_grouped.cu).
+struct GroupedArgs {
+    const uint8_t* a;
+    const float* sa;
+    const uint8_t* w;
+    const float* sw;
+    const int32_t* offsets;
+    void* y;
+    int y_dtype;
+    long long M, E, N, K;
+};
+int fp8_grouped_launch(const DevCtx& dc, const GroupedArgs& a, void* ws, size_t ws_bytes, cudaStream_t s);
+
 // Record a CUDA error for qg_last_cuda_error() and return QG_ERR_CUDA.
 int cuda_fail(cudaError_t e);
 

@@ -1,0 +1,125 @@
+// Rows in units of eight values, for the kernels that pass over rows once: 16
+// bytes of a 16-bit type, twice that of f32.
+#pragma once
+
+#include "serve_common.cuh"
+
+namespace qg {
+
+template <class T>
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
+
+// The values p[0 .. 8), of which `left` are inside the row (VEC: all or none, and
+// p on a 16-byte boundary); those that are not are 0.
+template <class T, bool VEC>
+__device__ __forceinline__ Raw8<T> load8(const T* p, int left) {
+    Raw8<T> r;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            r.w[i] = left > 0 ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
+    } else {
+        uint32_t u[2 * sizeof(T)];
+#pragma unroll
+        for (int i = 0; i < 2 * (int)sizeof(T); ++i) u[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= left) break;
+            if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(p[i]);
+            else u[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + i) << (16 * (i % 2));
+        }
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+    }
+    return r;
+}
+
+template <class T>
+__device__ __forceinline__ void to_f32(const Raw8<T>& r, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[4 * i] = __uint_as_float(r.w[i].x);
+            v[4 * i + 1] = __uint_as_float(r.w[i].y);
+            v[4 * i + 2] = __uint_as_float(r.w[i].z);
+            v[4 * i + 3] = __uint_as_float(r.w[i].w);
+        }
+    } else {
+        const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2<T>(u[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// p[0 .. min(8, left)) = v; VEC as above.
+template <class T, bool VEC>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8], int left) {
+    if constexpr (VEC) {
+        if (left <= 0) return;
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(p) =
+                make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+// The same for a type known at run time, at element `at` of an array.
+template <bool VEC>
+__device__ __forceinline__ void store8(void* p, long long at, int dtype, const float (&v)[8], int left) {
+    if (dtype == QG_F32) store8<float, VEC>(static_cast<float*>(p) + at, v, left);
+    else if (dtype == QG_F16) store8<__half, VEC>(static_cast<__half*>(p) + at, v, left);
+    else store8<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16*>(p) + at, v, left);
+}
+
+// Eight codes, PER of them inside the row as above (VEC: on an 8-byte boundary).
+template <bool VEC>
+__device__ __forceinline__ void store_codes8(uint8_t* p, const uint32_t (&code)[2], int left) {
+    if constexpr (VEC) {
+        if (left > 0) *reinterpret_cast<uint2*>(p) = make_uint2(code[0], code[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = (uint8_t)(code[i / 4] >> (8 * (i % 4)));
+    }
+}
+
+// Whether rows of `width` values that lie `stride` elements apart can be moved in
+// units of eight.
+inline bool in_eights(const void* p, long long stride, long long width, int elem_bytes) {
+    return width % 8 == 0 && (stride * elem_bytes) % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+}
+
+inline int type_bytes(int dtype) { return dtype == QG_F32 ? 4 : 2; }
+
+// A launch that may start while the kernel before it ends (it waits for it with
+// griddepcontrol.wait before it touches memory).
+template <class... P, class... A>
+int launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = may_overlap() ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e == cudaSuccess ? QG_OK : cuda_fail(e);
+}
+
+}  // namespace qg

@@ -1,6 +1,6 @@
-// C-ABI entry points of the serving operators (block-scaled fp8 product,
-// attention over a paged cache, upkeep of its pages, log probabilities):
-// argument validation, then dispatch. As in qg_api.cu every check happens
+// C-ABI entry points of the serving operators (block-scaled fp8 products, norms
+// and gates, attention over a paged cache, upkeep of its pages, log
+// probabilities): argument validation, then dispatch. As in qg_api.cu every check happens
 // before anything is enqueued. Index arrays live on the device and are checked
 // by the kernels that read them.
 #include <cuda_runtime.h>
@@ -95,6 +95,42 @@ int attn_shape(AttnArgs* a, int64_t tokens, int64_t batch, int64_t max_new, int6
     return QG_OK;
 }
 
+// What rms_norm and rms_norm_fp8_b128 have in common.
+int check_norm(const NormArgs& a, const Region (&out)[3], int64_t* bytes_x) {
+    if (a.M < 0 || a.K <= 0 || !is_type(a.x_dtype) || !(a.eps >= 0.f) || a.offset != a.offset) return QG_ERR_INVALID_ARG;
+    if (a.M > 0 && (!a.x || !a.y || (a.res && !a.res_out))) return QG_ERR_INVALID_ARG;
+    if ((a.res && !is_type(a.res_dtype)) || (a.w && !is_type(a.w_dtype))) return QG_ERR_INVALID_ARG;
+    if (a.M > kMaxCount || a.K > kMaxCount) return QG_ERR_UNSUPPORTED;
+    if (a.res && a.res_dtype != a.x_dtype && a.res_dtype != QG_F32) return QG_ERR_UNSUPPORTED;
+    int64_t rb = 0, ob = 0;
+    if (!span(a.M, a.K, a.x_stride, size_of(a.x_dtype), bytes_x)) return QG_ERR_INVALID_ARG;
+    if (a.res && (!span(a.M, a.K, a.res_stride, size_of(a.res_dtype), &rb) ||
+                  !span(a.M, a.K, a.res_out_stride, size_of(a.res_dtype), &ob)))
+        return QG_ERR_INVALID_ARG;
+    if (!aligned(a.x, size_of(a.x_dtype)) || (a.w && !aligned(a.w, size_of(a.w_dtype))) ||
+        (a.res && (!aligned(a.res, size_of(a.res_dtype)) || !aligned(a.res_out, size_of(a.res_dtype)))))
+        return QG_ERR_MISALIGNED;
+    // The new residual may take the old one's place, and only that.
+    const bool in_place = a.res && a.res_out == a.res && a.res_out_stride == a.res_stride;
+    const Region outs[] = {out[0], out[1], {a.res ? a.res_out : nullptr, ob}};
+    const Region ins[] = {{a.x, *bytes_x}, {a.w, a.w ? a.K * size_of(a.w_dtype) : 0},
+                          {in_place ? nullptr : a.res, rb}};
+    return clash(outs, ins) ? QG_ERR_INVALID_ARG : QG_OK;
+}
+
+int check_gate(const GateArgs& a) {
+    if (a.M < 0 || a.K <= 0 || !is_type(a.x_dtype)) return QG_ERR_INVALID_ARG;
+    if (a.M > 0 && (!a.gate || !a.up || !a.y)) return QG_ERR_INVALID_ARG;
+    if (a.M > kMaxCount || a.K > kMaxCount) return QG_ERR_UNSUPPORTED;
+    int64_t gb = 0, ub = 0;
+    const int64_t es = size_of(a.x_dtype);
+    if (!span(a.M, a.K, a.gate_stride, es, &gb) || !span(a.M, a.K, a.up_stride, es, &ub)) return QG_ERR_INVALID_ARG;
+    if (!aligned(a.gate, es) || !aligned(a.up, es)) return QG_ERR_MISALIGNED;
+    const Region outs[] = {{a.y, a.M * a.K * (a.scales ? 1 : size_of(a.y_dtype))}, {a.scales, a.M * ((a.K + 127) / 128) * 4}};
+    const Region ins[] = {{a.gate, gb}, {a.up, ub}};
+    return clash(outs, ins) ? QG_ERR_INVALID_ARG : QG_OK;
+}
+
 }  // namespace
 }  // namespace qg
 
@@ -148,6 +184,99 @@ int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) 
     if (M > kMaxCount || N > kMaxCount || K > kMaxCount) return QG_ERR_UNSUPPORTED;
     *bytes = (size_t)(M + N) * (size_t)((K + 15) / 16 * 16);
     return QG_OK;
+}
+
+int qmm_fp8_b128_grouped_workspace_size(int64_t M, int64_t experts, int64_t N, int64_t K, size_t* bytes) {
+    if (!bytes) return QG_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (M < 0 || experts <= 0 || N <= 0 || K <= 0) return QG_ERR_INVALID_ARG;
+    if (M > kMaxCount || experts > 1024 || N > kMaxCount / experts || K > kMaxCount) return QG_ERR_UNSUPPORTED;
+    *bytes = (size_t)(M + experts * N) * (size_t)((K + 15) / 16 * 16);
+    return QG_OK;
+}
+
+int qmm_fp8_b128_grouped(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
+                         const int32_t* offsets, void* y, int y_dtype, int64_t M, int64_t experts, int64_t N, int64_t K,
+                         void* workspace, size_t workspace_bytes, qg_stream_t stream) {
+    size_t most = 0;
+    int rc = qmm_fp8_b128_grouped_workspace_size(M, experts, N, K, &most);
+    if (rc) return rc;
+    if (!w || !w_scales || !offsets || (M > 0 && (!a || !a_scales || !y))) return QG_ERR_INVALID_ARG;
+    if (y_dtype != QG_F32 && y_dtype != QG_BF16) return QG_ERR_INVALID_ARG;
+    if (M > kMaxBytes / 4 / N) return QG_ERR_UNSUPPORTED;
+    if (!aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(offsets, 4) || !aligned(y, size_of(y_dtype)))
+        return QG_ERR_MISALIGNED;
+    const int64_t kb = (K + 127) / 128;
+    const Region out[] = {{y, M * N * size_of(y_dtype)}};
+    const Region in[] = {{a, M * K}, {a_scales, M * kb * 4}, {w, experts * N * K},
+                         {w_scales, experts * ((N + 127) / 128) * kb * 4}, {offsets, (experts + 1) * 4}};
+    if (clash(out, in)) return QG_ERR_INVALID_ARG;
+    if (workspace && !aligned(workspace, 16)) return QG_ERR_MISALIGNED;
+    if (M == 0) return QG_OK;
+    const DevCtx* dc = nullptr;
+    rc = device_ctx(&dc);
+    if (rc) return rc;
+    return fp8_grouped_launch(*dc, GroupedArgs{a, a_scales, w, w_scales, offsets, y, y_dtype, M, experts, N, K},
+                              workspace, workspace ? workspace_bytes : 0, cu(stream));
+}
+
+int rms_norm(const void* x, int x_dtype, int64_t x_stride, const void* residual, int residual_dtype,
+             int64_t residual_stride, const void* weight, int weight_dtype, float weight_offset, float eps, void* y,
+             int y_dtype, void* residual_out, int64_t residual_out_stride, int64_t M, int64_t K, qg_stream_t stream) {
+    const NormArgs a{x, residual, weight, y, residual_out, nullptr, x_stride, residual_stride, residual_out_stride,
+                     x_dtype, residual_dtype, weight_dtype, y_dtype, M, K, eps, weight_offset};
+    if (!is_type(y_dtype)) return QG_ERR_INVALID_ARG;
+    if (!aligned(y, size_of(y_dtype))) return QG_ERR_MISALIGNED;
+    int64_t xb = 0;
+    const bool sane = M > 0 && K > 0 && M <= kMaxCount && K <= kMaxCount;
+    const Region out[3] = {{y, sane ? M * K * size_of(y_dtype) : 0}, {nullptr, 0}, {nullptr, 0}};
+    int rc = check_norm(a, out, &xb);
+    if (rc || M == 0) return rc;
+    const DevCtx* dc = nullptr;
+    rc = device_ctx(&dc);
+    return rc ? rc : norm_launch(a, cu(stream));
+}
+
+int rms_norm_fp8_b128(const void* x, int x_dtype, int64_t x_stride, const void* residual, int residual_dtype,
+                      int64_t residual_stride, const void* weight, int weight_dtype, float weight_offset, float eps,
+                      uint8_t* codes, float* scales, void* residual_out, int64_t residual_out_stride, int64_t M, int64_t K,
+                      qg_stream_t stream) {
+    const NormArgs a{x, residual, weight, codes, residual_out, scales, x_stride, residual_stride, residual_out_stride,
+                     x_dtype, residual_dtype, weight_dtype, QG_F32, M, K, eps, weight_offset};
+    if (M > 0 && !scales) return QG_ERR_INVALID_ARG;
+    if (!aligned(scales, 4)) return QG_ERR_MISALIGNED;
+    int64_t xb = 0;
+    const bool sane = M > 0 && K > 0 && M <= kMaxCount && K <= kMaxCount;
+    const Region out[3] = {{codes, sane ? M * K : 0}, {scales, sane ? M * ((K + 127) / 128) * 4 : 0}, {nullptr, 0}};
+    int rc = check_norm(a, out, &xb);
+    if (rc || M == 0) return rc;
+    const DevCtx* dc = nullptr;
+    rc = device_ctx(&dc);
+    return rc ? rc : norm_launch(a, cu(stream));
+}
+
+int silu_mul(const void* gate, int64_t gate_stride, const void* up, int64_t up_stride, int x_dtype, void* y, int y_dtype,
+             int64_t M, int64_t K, qg_stream_t stream) {
+    const GateArgs a{gate, up, y, nullptr, gate_stride, up_stride, x_dtype, y_dtype, M, K};
+    if (!is_type(y_dtype)) return QG_ERR_INVALID_ARG;
+    if (!aligned(y, size_of(y_dtype))) return QG_ERR_MISALIGNED;
+    int rc = check_gate(a);
+    if (rc || M == 0) return rc;
+    const DevCtx* dc = nullptr;
+    rc = device_ctx(&dc);
+    return rc ? rc : gate_launch(a, cu(stream));
+}
+
+int silu_mul_fp8_b128(const void* gate, int64_t gate_stride, const void* up, int64_t up_stride, int x_dtype,
+                      uint8_t* codes, float* scales, int64_t M, int64_t K, qg_stream_t stream) {
+    const GateArgs a{gate, up, codes, scales, gate_stride, up_stride, x_dtype, QG_F32, M, K};
+    if (M > 0 && !scales) return QG_ERR_INVALID_ARG;
+    if (!aligned(scales, 4)) return QG_ERR_MISALIGNED;
+    int rc = check_gate(a);
+    if (rc || M == 0) return rc;
+    const DevCtx* dc = nullptr;
+    rc = device_ctx(&dc);
+    return rc ? rc : gate_launch(a, cu(stream));
 }
 
 int attn_paged(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -246,6 +375,44 @@ int kv_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, 
     const AppendArgs a{k, v, k_stride, v_stride, x_dtype, cache_dtype, k_cache, v_cache, slots,
                        tokens, num_pages, (int)kv_heads, (int)head_dim, (int)page_size};
     return kv_append_launch(*dc, a, cu(stream));
+}
+
+int kv_append_rope(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                   int x_dtype, const int64_t* positions, const float* inv_freq, int64_t rotary_dim, int interleaved,
+                   void* q_out, void* k_cache, void* v_cache, int cache_dtype, const int64_t* slots, int64_t tokens,
+                   int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t num_pages, int64_t page_size,
+                   qg_stream_t stream) {
+    if (tokens < 0 || q_heads < 0 || kv_heads <= 0 || head_dim <= 0 || num_pages <= 0 || !page_size_ok(page_size) ||
+        !is_type(x_dtype) || !is_16bit(cache_dtype) || !k_cache || !v_cache || !inv_freq)
+        return QG_ERR_INVALID_ARG;
+    if (rotary_dim <= 0 || rotary_dim % 2 || rotary_dim > head_dim) return QG_ERR_INVALID_ARG;
+    if (tokens > 0 && (!k || !v || !slots || !positions || (q_heads > 0 && (!q || !q_out)))) return QG_ERR_INVALID_ARG;
+    if (head_dim % 8 || head_dim > 1024) return QG_ERR_UNSUPPORTED;
+    if (q_heads > 65535 || kv_heads > 65535 || tokens > kMaxCount || num_pages > kMaxCount ||
+        tokens > kMaxCount / std::max<int64_t>(q_heads, kv_heads) ||
+        num_pages > kMaxBytes / (kv_heads * page_size * head_dim * 2))
+        return QG_ERR_UNSUPPORTED;
+    int64_t qb = 0, kb = 0, vb = 0;
+    const int64_t row = kv_heads * head_dim, es = size_of(x_dtype);
+    if ((q_heads > 0 && !span(tokens, q_heads * head_dim, q_stride, es, &qb)) || !span(tokens, row, k_stride, es, &kb) ||
+        !span(tokens, row, v_stride, es, &vb))
+        return QG_ERR_INVALID_ARG;
+    if (!aligned(k, es) || !aligned(v, es) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 8) ||
+        !aligned(positions, 8) || !aligned(inv_freq, 4) || (q_heads > 0 && (!aligned(q, es) || !aligned(q_out, 16))))
+        return QG_ERR_MISALIGNED;
+    const int64_t cb = num_pages * page_size * row * 2;
+    const Region out[] = {{k_cache, cb}, {v_cache, cb}, {q_out, tokens * q_heads * head_dim * 2}};
+    const Region in[] = {{q, qb}, {k, kb}, {v, vb}, {slots, tokens * 8}, {positions, tokens * 8},
+                         {inv_freq, rotary_dim / 2 * 4}};
+    if (clash(out, in)) return QG_ERR_INVALID_ARG;
+    if (tokens == 0) return QG_OK;
+    const DevCtx* dc = nullptr;
+    int rc = device_ctx(&dc);
+    if (rc) return rc;
+    const RopeArgs a{q_heads > 0 ? q : nullptr, k, v, q_stride, k_stride, v_stride, x_dtype, cache_dtype, positions, slots,
+                     inv_freq, q_out, k_cache, v_cache, tokens, num_pages, (int)q_heads, (int)kv_heads, (int)head_dim,
+                     (int)rotary_dim, (int)page_size, interleaved != 0};
+    return kv_append_rope_launch(*dc, a, cu(stream));
 }
 
 int kv_copy_pages(void* cache, int64_t planes, int64_t num_pages, int64_t page_bytes,

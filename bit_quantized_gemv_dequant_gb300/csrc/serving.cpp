@@ -103,6 +103,11 @@ int code(const Tensor& t, const char* name) {
     }
 }
 
+ScalarType type_of(PyObject* o, const char* name) {
+    if (!THPDtype_Check(o)) value_error("%s must be a torch.dtype", name);
+    return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
 Tensor make(at::IntArrayRef size, ScalarType type, const Tensor& like) {
     return at::empty(size, at::TensorOptions().dtype(type).device(like.device()));
 }
@@ -284,8 +289,7 @@ PyObject* qmm_fp8_b128(PyObject* const* a) {
     shape(w, "w", {N, K});
     shape(sx, "a_scales", {M, KB});
     shape(sw, "w_scales", {(N + 127) / 128, KB});
-    if (a[4] == Py_None && !THPDtype_Check(a[5])) value_error("out_dtype must be a torch.dtype");
-    const Tensor y = a[4] == Py_None ? make({M, N}, reinterpret_cast<THPDtype*>(a[5])->scalar_type, x) : dense(a[4], "y");
+    const Tensor y = a[4] == Py_None ? make({M, N}, type_of(a[5], "out_dtype"), x) : dense(a[4], "y");
     if (a[4] != Py_None) shape(y, "y", {M, N});
     const int type = code(y, "y");
     const qg_stream_t s = stream_of(a[7]);
@@ -298,6 +302,156 @@ PyObject* qmm_fp8_b128(PyObject* const* a) {
                               M, N, K, ws.p, ws.n, s);
     });
     return wrap(y);
+}
+
+// a, a_scales, w, w_scales, offsets, y | None, out_dtype, workspace, stream
+PyObject* qmm_fp8_b128_grouped(PyObject* const* a) {
+    const Tensor& x = dense(a[0], "a", ScalarType::Float8_e4m3fn);
+    const Tensor& sx = dense(a[1], "a_scales", ScalarType::Float);
+    const Tensor& w = dense(a[2], "w", ScalarType::Float8_e4m3fn);
+    const Tensor& sw = dense(a[3], "w_scales", ScalarType::Float);
+    const Tensor& offsets = dense(a[4], "offsets", ScalarType::Int);
+    dims(x, "a", 2);
+    dims(w, "w", 3);
+    const int64_t M = x.size(0), K = x.size(1), E = w.size(0), N = w.size(1), KB = (K + 127) / 128;
+    shape(w, "w", {E, N, K});
+    shape(sx, "a_scales", {M, KB});
+    shape(sw, "w_scales", {E, (N + 127) / 128, KB});
+    shape(offsets, "offsets", {E + 1});
+    const Tensor y = a[5] == Py_None ? make({M, N}, type_of(a[6], "out_dtype"), x) : dense(a[5], "y");
+    if (a[5] != Py_None) shape(y, "y", {M, N});
+    const int type = code(y, "y");
+    const qg_stream_t s = stream_of(a[8]);
+    size_t need = 0;
+    const uintptr_t odd = (uintptr_t)K | (uintptr_t)x.data_ptr() | (uintptr_t)w.data_ptr();
+    if (odd & 15) check(qmm_fp8_b128_grouped_workspace_size(M, E, N, K, &need), "qmm_fp8_b128_grouped");
+    const Scratch ws = scratch(need, a[7], x, s);
+    call("qmm_fp8_b128_grouped", ws.enqueue, [&] {
+        return ::qmm_fp8_b128_grouped(at_of<uint8_t>(x), at_of<float>(sx), at_of<uint8_t>(w), at_of<float>(sw),
+                                      at_of<int32_t>(offsets), y.data_ptr(), type, M, E, N, K, ws.p, ws.n, s);
+    });
+    return wrap(y);
+}
+
+// The arguments that the two forms of a norm share.
+struct Norm {
+    Tensor x, res, w, res_out;
+    int64_t M, K, x_stride, res_stride = 0, out_stride = 0;
+    int type, res_type = QG_F32, w_type = QG_F32;
+    float eps, offset;
+
+    Norm(PyObject* px, PyObject* pw, PyObject* pres, PyObject* pout, PyObject* peps, PyObject* poffset) {
+        x = rows(px, "x", 2, &x_stride);
+        type = code(x, "x");
+        M = x.size(0);
+        K = x.size(1);
+        if (pw != Py_None) {
+            w = dense(pw, "weight");
+            shape(w, "weight", {K});
+            w_type = code(w, "weight");
+        }
+        if (pres != Py_None) {
+            res = rows(pres, "residual", 2, &res_stride);
+            shape(res, "residual", {M, K});
+            res_type = code(res, "residual");
+        }
+        eps = (float)number(peps);
+        offset = (float)number(poffset);
+        if (pres == Py_None) {
+            if (pout != Py_None) value_error("residual_out needs a residual");
+        } else if (pout == Py_None) {
+            res_out = make({M, K}, res.scalar_type(), x);
+            out_stride = K;
+        } else {
+            res_out = rows(pout, "residual_out", 2, &out_stride);
+            shape(res_out, "residual_out", {M, K});
+            if (res_out.scalar_type() != res.scalar_type()) value_error("residual and residual_out must be of one type");
+        }
+    }
+    static void* at(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+};
+
+// x, weight | None, residual | None, out | None, residual_out | None, eps, weight_offset, out_dtype | None, stream
+PyObject* rms_norm(PyObject* const* a) {
+    const Norm n(a[0], a[1], a[2], a[4], a[5], a[6]);
+    const Tensor y = a[3] != Py_None ? dense(a[3], "out")
+                                     : make({n.M, n.K}, a[7] == Py_None ? n.x.scalar_type() : type_of(a[7], "out_dtype"), n.x);
+    if (a[3] != Py_None) shape(y, "out", {n.M, n.K});
+    const int type = code(y, "out");
+    const qg_stream_t s = stream_of(a[8]);
+    call("rms_norm", [&] {
+        return ::rms_norm(n.x.data_ptr(), n.type, n.x_stride, n.at(n.res), n.res_type, n.res_stride, n.at(n.w), n.w_type,
+                          n.offset, n.eps, y.data_ptr(), type, n.at(n.res_out), n.out_stride, n.M, n.K, s);
+    });
+    return n.res.defined() ? tuple(y, n.res_out) : wrap(y);
+}
+
+// codes and scales of [M, K], given or new
+std::pair<Tensor, Tensor> coded(PyObject* pc, PyObject* ps, int64_t M, int64_t K, const Tensor& like) {
+    const int64_t KB = (K + 127) / 128;
+    Tensor c = pc == Py_None ? make({M, K}, ScalarType::Float8_e4m3fn, like) : dense(pc, "codes", ScalarType::Float8_e4m3fn);
+    Tensor s = ps == Py_None ? make({M, KB}, ScalarType::Float, like) : dense(ps, "scales", ScalarType::Float);
+    if (pc != Py_None) shape(c, "codes", {M, K});
+    if (ps != Py_None) shape(s, "scales", {M, KB});
+    return {std::move(c), std::move(s)};
+}
+
+// x, weight | None, residual | None, codes | None, scales | None, residual_out | None, eps, weight_offset, stream
+PyObject* rms_norm_fp8_b128(PyObject* const* a) {
+    const Norm n(a[0], a[1], a[2], a[5], a[6], a[7]);
+    const auto [codes, scales] = coded(a[3], a[4], n.M, n.K, n.x);
+    const Tensor &c = codes, &sc = scales;
+    const qg_stream_t s = stream_of(a[8]);
+    call("rms_norm_fp8_b128", [&] {
+        return ::rms_norm_fp8_b128(n.x.data_ptr(), n.type, n.x_stride, n.at(n.res), n.res_type, n.res_stride, n.at(n.w),
+                                   n.w_type, n.offset, n.eps, at_of<uint8_t>(c), at_of<float>(sc), n.at(n.res_out),
+                                   n.out_stride, n.M, n.K, s);
+    });
+    return n.res.defined() ? tuple(c, sc, n.res_out) : tuple(c, sc);
+}
+
+struct Gate {
+    Tensor gate, up;
+    int64_t M, K, gs, us;
+    int type;
+
+    Gate(PyObject* pg, PyObject* pu) {
+        gate = rows(pg, "gate", 2, &gs);
+        up = rows(pu, "up", 2, &us);
+        type = code(gate, "gate");
+        M = gate.size(0);
+        K = gate.size(1);
+        shape(up, "up", {M, K});
+        if (up.scalar_type() != gate.scalar_type()) value_error("gate and up must be of one type");
+    }
+};
+
+// gate, up, out | None, out_dtype | None, stream
+PyObject* silu_mul(PyObject* const* a) {
+    const Gate g(a[0], a[1]);
+    const Tensor y = a[2] != Py_None
+                         ? dense(a[2], "out")
+                         : make({g.M, g.K}, a[3] == Py_None ? g.gate.scalar_type() : type_of(a[3], "out_dtype"), g.gate);
+    if (a[2] != Py_None) shape(y, "out", {g.M, g.K});
+    const int type = code(y, "out");
+    const qg_stream_t s = stream_of(a[4]);
+    call("silu_mul", [&] {
+        return ::silu_mul(g.gate.data_ptr(), g.gs, g.up.data_ptr(), g.us, g.type, y.data_ptr(), type, g.M, g.K, s);
+    });
+    return wrap(y);
+}
+
+// gate, up, codes | None, scales | None, stream
+PyObject* silu_mul_fp8_b128(PyObject* const* a) {
+    const Gate g(a[0], a[1]);
+    const auto [codes, scales] = coded(a[2], a[3], g.M, g.K, g.gate);
+    const Tensor &c = codes, &sc = scales;
+    const qg_stream_t s = stream_of(a[4]);
+    call("silu_mul_fp8_b128", [&] {
+        return ::silu_mul_fp8_b128(g.gate.data_ptr(), g.gs, g.up.data_ptr(), g.us, g.type, at_of<uint8_t>(c),
+                                   at_of<float>(sc), g.M, g.K, s);
+    });
+    return tuple(c, sc);
 }
 
 // q, k_cache, v_cache, page_table, q_offsets, context_lens, out | None, lse | None,
@@ -367,6 +521,49 @@ PyObject* kv_append(PyObject* const* a) {
                            D, pages, page, s);
     });
     Py_RETURN_NONE;
+}
+
+// q | None, k, v, positions, inv_freq, k_cache, v_cache, slots, q_out | None, interleaved, stream
+PyObject* kv_append_rope(PyObject* const* a) {
+    int64_t qs = 0, ks, vs;
+    const Tensor& k = rows(a[1], "k", 3, &ks);
+    const Tensor& v = rows(a[2], "v", 3, &vs);
+    const Tensor& positions = dense(a[3], "positions", ScalarType::Long);
+    const Tensor& freq = dense(a[4], "inv_freq", ScalarType::Float);
+    const Tensor& kc = dense(a[5], "k_cache");
+    const Tensor& vc = dense(a[6], "v_cache", kc.scalar_type());
+    const Tensor& slots = dense(a[7], "slots", ScalarType::Long);
+    if (v.scalar_type() != k.scalar_type()) value_error("k and v must be of one type");
+    dims(kc, "k_cache", 4);
+    dims(freq, "inv_freq", 1);
+    const int64_t T = k.size(0), H = k.size(1), D = k.size(2), pages = kc.size(0), page = kc.size(2);
+    shape(v, "v", {T, H, D});
+    shape(kc, "k_cache", {pages, H, page, D});
+    shape(vc, "v_cache", {pages, H, page, D});
+    shape(slots, "slots", {T});
+    shape(positions, "positions", {T});
+    Tensor q, out;
+    if (a[0] != Py_None) {
+        q = rows(a[0], "q", 3, &qs);
+        if (q.scalar_type() != k.scalar_type()) value_error("q and k must be of one type");
+        shape(q, "q", {T, q.size(1), D});
+        out = a[8] == Py_None ? make({T, q.size(1), D}, kc.scalar_type(), q) : dense(a[8], "q_out", kc.scalar_type());
+        if (a[8] != Py_None) shape(out, "q_out", q.sizes());
+    } else if (a[8] != Py_None) {
+        value_error("q_out needs q");
+    }
+    const int x = code(k, "k"), c = code(kc, "k_cache");
+    const bool interleaved = truth(a[9]);
+    const qg_stream_t s = stream_of(a[10]);
+    call("kv_append_rope", [&] {
+        const bool has = q.defined();
+        return ::kv_append_rope(has ? q.data_ptr() : nullptr, k.data_ptr(), v.data_ptr(), qs, ks, vs, x,
+                                at_of<int64_t>(positions), at_of<float>(freq), 2 * freq.size(0), interleaved,
+                                has ? out.data_ptr() : nullptr, kc.data_ptr(), vc.data_ptr(), c, at_of<int64_t>(slots), T,
+                                has ? q.size(1) : 0, H, D, pages, page, s);
+    });
+    if (!q.defined()) Py_RETURN_NONE;
+    return wrap(out);
 }
 
 struct Planes {
@@ -486,7 +683,9 @@ PyObject* token_logprobs(PyObject* const* a) {
 PyMethodDef g_methods[] = {ENTRY(set_error, 1),     ENTRY(quantize_fp8_b128, 4), ENTRY(qmm_fp8_b128, 8),
                            ENTRY(attn_paged, 15),   ENTRY(kv_append, 6),         ENTRY(kv_copy_pages, 4),
                            ENTRY(kv_fork, 8),       ENTRY(kv_free, 5),           ENTRY(kv_compact, 5),
-                           ENTRY(token_logprobs, 4), {nullptr, nullptr, 0, nullptr}};
+                           ENTRY(token_logprobs, 4), ENTRY(qmm_fp8_b128_grouped, 9), ENTRY(rms_norm, 9),
+                           ENTRY(rms_norm_fp8_b128, 9), ENTRY(silu_mul, 5), ENTRY(silu_mul_fp8_b128, 5),
+                           ENTRY(kv_append_rope, 11), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

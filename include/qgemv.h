@@ -258,9 +258,10 @@ QG_API int qmm_af4_g64(const float* x, const uint32_t* plane, const uint32_t* me
                        qg_stream_t stream);
 
 /* ------------------------------------------------------------------------
- * Operators around the projections of a serving step: the product with
- * block-scaled 8-bit floating point weights, attention over a paged cache,
- * the upkeep of the cache's pages and the log probabilities of tokens. No
+ * Operators around the projections of a serving step: the products with
+ * block-scaled 8-bit floating point weights (of one layer, or of experts), the
+ * norms and gates between them, attention over a paged cache, the upkeep of
+ * the cache's pages and the log probabilities of tokens. No
  * counterpart in the source pages: additions of this library. The
  * conventions at the top of this file hold for all of them, with these
  * additions: element types are named by QG_F32 / QG_F16 / QG_BF16, strides
@@ -299,6 +300,59 @@ QG_API int qmm_fp8_b128(const uint8_t* a, const float* a_scales, const uint8_t* 
                         const float* w_scales, void* y, int y_dtype, int64_t M, int64_t N,
                         int64_t K, void* workspace, size_t workspace_bytes, qg_stream_t stream);
 QG_API int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+
+/* qmm_fp8_b128_grouped: the products of a layer of experts. Rows offsets[e] ..
+ * offsets[e + 1] - 1 of a [M, K] are those of expert e (none is fine), whose
+ * weight is w[e] of w [experts, N, K], with w_scales [experts, ceil(N / 128),
+ * ceil(K / 128)]; y [M, N] and everything else as in qmm_fp8_b128, the error
+ * bound too. offsets is int32 [experts + 1], from 0 up to M. Rows before
+ * offsets[0] and at or after offsets[experts] are left alone; an expert whose
+ * range is none (outside of 0 .. M, or backwards) has no rows and is recorded.
+ * M = 0 is fine, experts <= 1024, experts * N <= 2^31 - 2^14. The kernel is
+ * chosen by M / experts; any spread of the rows is right. The workspace is
+ * needed for the same reason as there: calls with K % 16 == 0 and 16-byte
+ * aligned a and w need none. */
+QG_API int qmm_fp8_b128_grouped(const uint8_t* a, const float* a_scales, const uint8_t* w,
+                                const float* w_scales, const int32_t* offsets, void* y, int y_dtype,
+                                int64_t M, int64_t experts, int64_t N, int64_t K, void* workspace,
+                                size_t workspace_bytes, qg_stream_t stream);
+QG_API int qmm_fp8_b128_grouped_workspace_size(int64_t M, int64_t experts, int64_t N, int64_t K,
+                                               size_t* bytes);
+
+/* What lies between two products of a layer. M = 0 is fine for all of them.
+ *
+ * rms_norm: of each row of x [M, K] (x_dtype, rows x_stride elements apart)
+ *   h = x + residual (x alone if residual is NULL)
+ *   y = h / sqrt(mean(h^2) + eps) * (weight_offset + weight)
+ * in f32 (squares and their sum too: rows of values past 2^63 / sqrt(K)
+ * overflow), with one rounding to y [M, K] of y_dtype. weight [K] may be
+ * NULL: a factor of 1 then, weight_offset or not. With a residual (of
+ * x_dtype or f32, rows residual_stride apart), residual_out gets h rounded to
+ * its type; it may be the residual itself, with the same stride, and must not
+ * overlap it otherwise. eps >= 0; a row of zeros with eps = 0 gives NaN. A
+ * NaN or an infinity in a row reaches all of its y.
+ * rms_norm_fp8_b128: the same, with y as quantize_fp8_b128 stores it: codes
+ * [M, K] and scales [M, ceil(K / 128)] of the f32 values.
+ *
+ * silu_mul: y = up * gate / (1 + exp(-gate)) of gate, up [M, K] (x_dtype,
+ * each with a row stride: halves of one product's rows, or the two outputs of
+ * qgemv_dual_q4_0), in f32 with one rounding to y_dtype; results below 2^-119
+ * may be 0. silu_mul_fp8_b128: the same as codes and scales. */
+QG_API int rms_norm(const void* x, int x_dtype, int64_t x_stride, const void* residual,
+                    int residual_dtype, int64_t residual_stride, const void* weight,
+                    int weight_dtype, float weight_offset, float eps, void* y, int y_dtype,
+                    void* residual_out, int64_t residual_out_stride, int64_t M, int64_t K,
+                    qg_stream_t stream);
+QG_API int rms_norm_fp8_b128(const void* x, int x_dtype, int64_t x_stride, const void* residual,
+                             int residual_dtype, int64_t residual_stride, const void* weight,
+                             int weight_dtype, float weight_offset, float eps, uint8_t* codes,
+                             float* scales, void* residual_out, int64_t residual_out_stride,
+                             int64_t M, int64_t K, qg_stream_t stream);
+QG_API int silu_mul(const void* gate, int64_t gate_stride, const void* up, int64_t up_stride,
+                    int x_dtype, void* y, int y_dtype, int64_t M, int64_t K, qg_stream_t stream);
+QG_API int silu_mul_fp8_b128(const void* gate, int64_t gate_stride, const void* up,
+                             int64_t up_stride, int x_dtype, uint8_t* codes, float* scales,
+                             int64_t M, int64_t K, qg_stream_t stream);
 
 /* The paged cache of one layer: k_cache and v_cache are [num_pages,
  * kv_heads, page_size, head_dim] of one 16-bit type, 16-byte aligned.
@@ -356,6 +410,19 @@ QG_API int attn_paged_workspace_size(int64_t tokens, int64_t batch, int64_t max_
  * QG_BF16), to slot slots[t] = page * page_size + place of one layer's
  * k_cache / v_cache. A negative slot skips its row. Slots must differ.
  *
+ * kv_append_rope: kv_append with the rotation by position on the way, of q
+ * too. The first rotary_dim values of each head of q and k are pairs: (i, i +
+ * rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0. Pair i of row t is
+ * turned by the angle positions[t] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * in f32 from the exact angle (for any position below 2^31 of either sign, to
+ * 2^-23 of a turn's sine), the rest of a head is not turned. q [tokens,
+ * q_heads, head_dim] (x_dtype, rows q_stride apart) goes to q_out, dense, in
+ * cache_dtype; with q_heads = 0 there is none. k and v go to slots[t] as in
+ * kv_append; rows with a negative slot get their q_out all the same.
+ * inv_freq: f32 [rotary_dim / 2], finite. rotary_dim is even and at most
+ * head_dim, head_dim a multiple of 8 and at most 1024.
+ *
  * kv_copy_pages: page dst[i] = page src[i] in every plane, i < n. No page may
  * be both a source and a destination, and destinations must differ. Pairs
  * with a negative member are skipped.
@@ -385,6 +452,12 @@ QG_API int kv_append(const void* k, const void* v, int64_t k_stride, int64_t v_s
                      void* k_cache, void* v_cache, int cache_dtype, const int64_t* slots,
                      int64_t tokens, int64_t kv_heads, int64_t head_dim, int64_t num_pages,
                      int64_t page_size, qg_stream_t stream);
+QG_API int kv_append_rope(const void* q, const void* k, const void* v, int64_t q_stride,
+                          int64_t k_stride, int64_t v_stride, int x_dtype, const int64_t* positions,
+                          const float* inv_freq, int64_t rotary_dim, int interleaved, void* q_out,
+                          void* k_cache, void* v_cache, int cache_dtype, const int64_t* slots,
+                          int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                          int64_t num_pages, int64_t page_size, qg_stream_t stream);
 QG_API int kv_copy_pages(void* cache, int64_t planes, int64_t num_pages, int64_t page_bytes,
                          const int32_t* src, const int32_t* dst, int64_t n, qg_stream_t stream);
 QG_API int kv_fork(void* cache, int64_t planes, int64_t num_pages, int64_t page_bytes,
