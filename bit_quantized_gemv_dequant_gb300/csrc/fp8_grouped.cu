@@ -12,6 +12,7 @@ namespace {
 constexpr int kGTile = 64;    // rows of a and of w per tile
 constexpr int kGChunk = 32;   // k per step
 constexpr int kGThreads = 256;
+constexpr int kFewRows = 64;  // per expert on average, for the kernel of few rows
 using GGroups = fp8::Groups<kGTile, 1>;
 
 __device__ __forceinline__ float e4m3_f32(uint8_t c) {
@@ -24,17 +25,17 @@ __device__ __forceinline__ float e4m3_f32(uint8_t c) {
 template <class TY>
 __global__ void __launch_bounds__(kGThreads)
     general_kernel(const GroupedArgs a, const int KB, unsigned* err) {
-    extern __shared__ uint8_t smem[];
-    GGroups& groups = *reinterpret_cast<GGroups*>(smem);
+    extern __shared__ long long list[];
     __shared__ float as[kGChunk][kGTile + 4];
     __shared__ float ws[kGChunk][kGTile + 4];
-    const int E = (int)a.E, M = (int)a.M, N = (int)a.N, K = (int)a.K, nt = (N - 1) / kGTile + 1;
-    if (threadIdx.x < 32) groups.build(a.offsets, E, M, nt, err);
+    GGroups groups(list, (int)a.E);
+    const int M = (int)a.M, N = (int)a.N, K = (int)a.K, nt = (N - 1) / kGTile + 1;
+    if (threadIdx.x < 32) groups.build(a.offsets, M, nt, err);
     __syncthreads();
     TY* y = static_cast<TY*>(a.y);
     const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
-    for (long long t = blockIdx.x; t < groups.first[E]; t += gridDim.x) {
-        const GGroups::Tile g = groups.find(t, E);
+    for (long long t = blockIdx.x; t < groups.first[a.E]; t += gridDim.x) {
+        const GGroups::Tile g = groups.find(t);
         const long long m0 = g.m0, n0 = (long long)g.n_tile * kGTile, end = g.m0 + g.rows;
         const uint8_t* w = a.w + (long long)g.e * N * K;
         const float* sw = a.sw + ((long long)g.e * ((N - 1) / 128 + 1) + n0 / 128) * KB;
@@ -84,13 +85,35 @@ __global__ void __launch_bounds__(kGThreads)
 
 template <class TY>
 int general_launch(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
-    general_kernel<TY><<<(unsigned)dc.num_sms * 4, kGThreads, sizeof(GGroups), s>>>(a, (int)((a.K + 127) / 128), dc.err);
+    general_kernel<TY><<<(unsigned)dc.num_sms * 4, kGThreads, GGroups::bytes(a.E), s>>>(a, (int)((a.K + 127) / 128), dc.err);
     return launched();
 }
 
 }  // namespace
 
-int fp8_grouped_launch(const DevCtx& dc, const GroupedArgs& a, void* ws, size_t ws_bytes, cudaStream_t s) {
+int fp8_grouped_launch(const DevCtx& dc, const GroupedArgs& args, void* ws, size_t ws_bytes, cudaStream_t s) {
+    GroupedArgs a = args;
+    const long long pitch = (a.K + 15) / 16 * 16;
+    auto fits = [&](const uint8_t* p) { return a.K == pitch && reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    bool tma = fits(a.a) && fits(a.w);
+    if (!tma && pitch <= 0x7FFFFFFF && ws_bytes >= (size_t)((a.M + a.E * a.N) * pitch)) {
+        // Zeros after the end of a row add nothing, and the blocks of 128 are the same.
+        uint8_t* p = static_cast<uint8_t*>(ws);
+        int rc = QG_OK;
+        if (!fits(a.w)) {
+            rc = fp8::pad_rows(dc, a.w, p, a.E * a.N, a.K, pitch, s);
+            a.w = p;
+            p += a.E * a.N * pitch;
+        }
+        if (rc == QG_OK && !fits(args.a)) {
+            rc = fp8::pad_rows(dc, a.a, p, a.M, a.K, pitch, s);
+            a.a = p;
+        }
+        if (rc) return rc;
+        a.K = pitch;
+        tma = true;
+    }
+    if (tma) return a.M <= kFewRows * a.E ? fp8::launch_grouped_few(dc, a, s) : fp8::launch_grouped_tile(dc, a, s);
     return a.y_dtype == QG_F32 ? general_launch<float>(dc, a, s) : general_launch<__nv_bfloat16>(dc, a, s);
 }
 

@@ -110,13 +110,17 @@ __global__ void __launch_bounds__(kPadThreads)
     }
 }
 
-int pad_launch(const DevCtx& dc, const uint8_t* src, uint8_t* dst, long long rows, long long K, long long pitch,
-               cudaStream_t s) {
+}  // namespace
+
+int fp8::pad_rows(const DevCtx& dc, const uint8_t* src, uint8_t* dst, long long rows, long long K, long long pitch,
+                  cudaStream_t s) {
     const long long ctas = (rows * (pitch / 16) + kPadThreads - 1) / kPadThreads;
     pad_kernel<<<(unsigned)(ctas < dc.num_sms * 16LL ? ctas : dc.num_sms * 16LL), kPadThreads, 0, s>>>(
         src, dst, rows, (int)K, (int)pitch);
     return launched();
 }
+
+namespace {
 
 template <class TY>
 int general_launch(const Fp8Args& a, cudaStream_t s) {
@@ -141,12 +145,12 @@ int fp8_mm_launch(const DevCtx& dc, const Fp8Args& args, void* ws, size_t ws_byt
         uint8_t* p = static_cast<uint8_t*>(ws);
         int rc = QG_OK;
         if (!fits(a.w)) {
-            rc = pad_launch(dc, a.w, p, a.N, a.K, pitch, s);
+            rc = fp8::pad_rows(dc, a.w, p, a.N, a.K, pitch, s);
             a.w = p;
             p += a.N * pitch;
         }
         if (rc == QG_OK && !fits(args.a)) {
-            rc = pad_launch(dc, a.a, p, a.M, a.K, pitch, s);
+            rc = fp8::pad_rows(dc, a.a, p, a.M, a.K, pitch, s);
             a.a = p;
         }
         if (rc) return rc;
