@@ -12,7 +12,6 @@ namespace {
 constexpr int kGTile = 64;    // rows of a and of w per tile
 constexpr int kGChunk = 32;   // k per step
 constexpr int kGThreads = 256;
-constexpr int kFewRows = 64;  // per expert on average, for the kernel of few rows
 using GGroups = fp8::Groups<kGTile, 1>;
 
 __device__ __forceinline__ float e4m3_f32(uint8_t c) {
@@ -33,9 +32,10 @@ __global__ void __launch_bounds__(kGThreads)
     if (threadIdx.x < 32) groups.build(a.offsets, M, nt, err);
     __syncthreads();
     TY* y = static_cast<TY*>(a.y);
+    GGroups::Tile g{};
     const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
     for (long long t = blockIdx.x; t < groups.first[a.E]; t += gridDim.x) {
-        const GGroups::Tile g = groups.find(t);
+        groups.find(t, g);
         const long long m0 = g.m0, n0 = (long long)g.n_tile * kGTile, end = g.m0 + g.rows;
         const uint8_t* w = a.w + (long long)g.e * N * K;
         const float* sw = a.sw + ((long long)g.e * ((N - 1) / 128 + 1) + n0 / 128) * KB;
@@ -89,6 +89,17 @@ int general_launch(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
     return launched();
 }
 
+// Which kernel, by the rows that an expert has on average: at 32 the kernel of few rows
+// takes 93 us of 32 experts, N = K = 4096, and the other one 100; at 48 107 and 104, at
+// 64 133 and 112. Up to 64 it is also taken where it leaves fewer SMs idle, since it
+// splits K for its last tiles (9 experts of 34 rows, N = 2200, K = 5200).
+bool few_rows(const DevCtx& dc, const GroupedArgs& a) {
+    if (a.M <= 32 * a.E) return true;
+    if (a.M > 64 * a.E) return false;
+    const long long pairs = std::max(1, dc.num_sms / 2), tiles = (a.N + 255) / 256 * a.E;
+    return 5 * fp8::grouped_few_chain(dc, a) < 4 * ((tiles + pairs - 1) / pairs) * ((a.K + 127) / 128);
+}
+
 }  // namespace
 
 int fp8_grouped_launch(const DevCtx& dc, const GroupedArgs& args, void* ws, size_t ws_bytes, cudaStream_t s) {
@@ -113,7 +124,7 @@ int fp8_grouped_launch(const DevCtx& dc, const GroupedArgs& args, void* ws, size
         a.K = pitch;
         tma = true;
     }
-    if (tma) return a.M <= kFewRows * a.E ? fp8::launch_grouped_few(dc, a, s) : fp8::launch_grouped_tile(dc, a, s);
+    if (tma) return few_rows(dc, a) ? fp8::launch_grouped_few(dc, a, s) : fp8::launch_grouped_tile(dc, a, s);
     return a.y_dtype == QG_F32 ? general_launch<float>(dc, a, s) : general_launch<__nv_bfloat16>(dc, a, s);
 }
 

@@ -29,10 +29,12 @@ constexpr int kBN = 64;
 constexpr int kThreads = 384, kEpi = 256;
 constexpr int kStages = 7, kStage = 16384 + kBN * 128;
 constexpr int kBufs = 8;
+constexpr int kJoin = 10;      // what joining the parts of a tile takes, in k blocks
 constexpr int kOwn = kBN / 2;  // rows of a per epilogue thread
 constexpr int kPartOff = kStages * kStage;
+constexpr int kPitch = scale_pitch(kBN);
 constexpr int kScaleOff = kPartOff + kBN * 128 * 4;
-constexpr int kBarOff = kScaleOff + kSets * kSetBlocks * kBN * 4;
+constexpr int kBarOff = kScaleOff + kSets * kSetBlocks * kPitch * 4;
 constexpr int kBars = 2 * kStages + 2 * kBufs + 2 * kSets + 3;
 constexpr int kGroupOff = kBarOff + 8 * kBars + 8;
 using FewGroups = Groups<kBN, 16>;
@@ -94,8 +96,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = warp_number(), lane = threadIdx.x & 31;
     const int split = (int)gridDim.x, rank = (int)blockIdx.x;
-    const int b0 = (int)((long long)p.KB * rank / split), b1 = (int)((long long)p.KB * (rank + 1) / split);
-    const int nb = b1 - b0;
 
     if (threadIdx.x == 64) {
         for (int i = 0; i < kStages; ++i) {
@@ -130,14 +130,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t tmem = *slot;
     const long long tiles = groups.first[p.E];
-    const long long first = blockIdx.y, step = gridDim.y;
+    FewGroups::Tile g{};
+    // This CTA's jobs: tiles of its own, all of K, as long as there are enough for all
+    // CTAs, then shares of the rest, one tile per cluster at a time.
+    const long long ctas = (long long)split * gridDim.y, own = blockIdx.y * (long long)split + rank;
+    const long long whole = quotient(split > 1 ? tiles : tiles + ctas - 1 - own, ctas);
+    int b0 = 0, b1 = p.KB;
+    auto job = [&](long long i) {
+        long long t = i * ctas + own;
+        if (i >= whole) {
+            t = split > 1 ? whole * ctas + (i - whole) * gridDim.y + blockIdx.y : tiles;
+            b0 = (int)((long long)p.KB * rank / split);
+            b1 = (int)((long long)p.KB * (rank + 1) / split);
+        }
+        if (t >= tiles) return false;
+        groups.find(t, g);
+        return true;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
             int i = 0;
             bool ok = true;
-            for (long long t = first; t < tiles && ok; t += step) {
-                const FewGroups::Tile g = groups.find(t);
+            for (long long t = 0; ok && job(t); ++t) {
                 const int parts = (g.rows + 15) / 16;
                 for (int b = b0; b < b1; ++b, ++i) {
                     const int st = i % kStages;
@@ -161,10 +176,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
         int st = 0, tb = 0;
         uint32_t ph = 0, tph = 0;
-        bool ok = true;
-        for (long long t = first; t < tiles && ok; t += step) {
-            const uint32_t desc = f8_idesc(128, (groups.find(t).rows + 15) / 16 * 16);
-            for (int i = 0; i < nb; ++i) {
+        bool ok = true, any = false;
+        for (long long t = 0; ok && job(t); ++t) {
+            const uint32_t desc = f8_idesc(128, (g.rows + 15) / 16 * 16);
+            for (int b = b0; b < b1; ++b) {
+                any = true;
                 if (!warp_bar_wait(full(st), ph) || !warp_bar_wait(t_empty(tb), tph ^ 1)) {
                     if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
                     ok = false;
@@ -189,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (first < tiles) {
+        if (any) {
             if (elect_one()) tc_commit(done);
             __syncwarp();
             if (!warp_bar_wait(done, 0) && lane == 0) report_error(p.err, DEVERR_WAIT_DRAIN);
@@ -199,16 +215,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         int set = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (long long t = first; t < tiles && ok; t += step) {
-            const FewGroups::Tile g = groups.find(t);
+        for (long long t = 0; ok && job(t); ++t) {
             const float* sw = p.sw + ((long long)g.e * ((p.N + 127) / 128) + g.n_tile) * p.KB;
-            for (int i = 0; i < nb; i += kSetBlocks) {
+            for (int b = b0; b < b1; b += kSetBlocks) {
                 if (!warp_bar_wait(s_empty(set), ph ^ 1)) {
                     if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
                     ok = false;
                     break;
                 }
-                load_scales<kBN>(scales + set * (kSetBlocks * kBN), p, sw, g.m0, g.rows, b0 + i, min(kSetBlocks, nb - i), tid);
+                load_scales<kBN>(scales + set * (kSetBlocks * kPitch), p, sw, g.m0, g.rows, b, min(kSetBlocks, b1 - b), tid);
                 mbar_arrive(s_full(set));
                 if (++set == kSets) {
                     set = 0;
@@ -227,18 +242,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && lane == 0) report_error(p.err, code);
             ok = false;
         };
-        for (long long t = first; t < tiles; t += step) {
-            const FewGroups::Tile g = groups.find(t);
+        for (long long t = 0; job(t); ++t) {
             float2 acc[kOwn / 2];
 #pragma unroll
             for (int i = 0; i < kOwn / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            for (int i0 = 0; i0 < nb; i0 += kSetBlocks) {
+            for (int i0 = b0; i0 < b1; i0 += kSetBlocks) {
                 if (ok && !warp_bar_wait(s_full(set), sph)) lost(DEVERR_TC_WAIT);
-                const int nk = min(kSetBlocks, nb - i0);
+                const int nk = min(kSetBlocks, b1 - i0);
                 for (int b = 0; b < nk; ++b) {
                     if (ok && !warp_bar_wait(t_full(tb), tph)) lost(DEVERR_TC_WAIT);
                     tc_fence_after();
-                    const float4* sc = reinterpret_cast<const float4*>(scales + (set * kSetBlocks + b) * kBN + own0);
+                    const float4* sc = reinterpret_cast<const float4*>(scales + (set * kSetBlocks + b) * kPitch + own0);
                     uint32_t r[2][16];
                     const bool low = own0 < g.rows, high = own0 + 16 < g.rows;
                     if (low) tmem_ld16_async(at + tb * kBN, r[0]);
@@ -275,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const long long n = g.n_tile * 128LL + row;
-            if (split == 1) {
+            if (t < whole) {
                 if (n < p.N) {
 #pragma unroll
                     for (int c = 0; c < kOwn; ++c)
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             float* part = reinterpret_cast<float*>(smem + kPartOff);  // [row of a][row of w]
-            if (t != first && ok && !cluster_bar_wait(p_empty, pph ^ 1)) lost(DEVERR_TC_WAIT);
+            if (t > whole && ok && !cluster_bar_wait(p_empty, pph ^ 1)) lost(DEVERR_TC_WAIT);
 #pragma unroll
             for (int c = 0; c < kOwn; ++c)
                 if (own0 + c < g.rows) part[(own0 + c) * 128 + row] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
@@ -325,6 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+struct FewPlan {
+    const int* room;
+    int split;
+    long long chain;  // k blocks one after the other
+};
+
 // How many clusters of i CTAs the GPU holds at once, asked once per kernel and
 // device.
 template <class TY>
@@ -354,25 +374,40 @@ int cluster_room(const DevCtx& dc, const int** room) {
     return error[dc.device] == cudaSuccess ? QG_OK : cuda_fail(error[dc.device]);
 }
 
+// The size of the clusters: the one with the fewest k blocks one after the other if
+// the rows are spread over as many experts as there can be.
+template <class TY>
+int plan(const DevCtx& dc, const GroupedArgs& a, FewPlan* p) {
+    const int rc = cluster_room<TY>(dc, &p->room);
+    if (rc) return rc;
+    const long long kb = (a.K + 127) / 128, tiles = (a.N + 127) / 128 * std::min(a.M, a.E);
+    p->split = 0;
+    for (int i = 1; i < 9 && (i == 1 || kb >= 2 * i); ++i) {
+        if (p->room[i] < 1) continue;
+        const long long ctas = (long long)i * p->room[i], rest = tiles % ctas;
+        const long long shares = (rest + p->room[i] - 1) / p->room[i];
+        const long long chain = tiles / ctas * kb + shares * (i == 1 ? kb : (kb + i - 1) / i + kJoin);
+        if (p->split == 0 || chain * 100 < p->chain * 96) {
+            p->chain = chain;
+            p->split = i;
+        }
+    }
+    return p->split ? QG_OK : QG_ERR_UNSUPPORTED;
+}
+
 template <class TY>
 int launch(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
-    const int* room = nullptr;
-    int rc = cluster_room<TY>(dc, &room);
+    FewPlan pl;
+    int rc = plan<TY>(dc, a, &pl);
     CUtensorMap mw, ma;
     if (rc == QG_OK) rc = weight_map(&mw, a);
     if (rc == QG_OK) rc = code_map(&ma, a.a, a.M, a.K, 16);
     if (rc) return rc;
-    // The largest split of K, two k blocks per CTA at least, whose clusters all run at
-    // once if the rows are spread over as many experts as there can be.
-    const long long kb = (a.K + 127) / 128, nt = (a.N + 127) / 128;
-    const long long tiles = nt * (std::min(a.M, a.E) + a.M / kBN);  // at most
-    int split = 1;
-    for (int i = 2; i < 9 && kb >= 2 * i; ++i)
-        if (nt * std::min(a.M, a.E) <= room[i]) split = i;
-    if (room[split] < 1) return QG_ERR_UNSUPPORTED;
+    const int split = pl.split, *room = pl.room;
+    const long long kb = (a.K + 127) / 128, most = (a.N + 127) / 128 * (std::min(a.M, a.E) + a.M / kBN);
     const GroupedParams p{a.sa, a.sw, a.offsets, a.y, (int)a.M, (int)a.E, (int)a.N, (int)kb, dc.err};
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)split, (unsigned)std::min<long long>(tiles, room[split]));
+    cfg.gridDim = dim3((unsigned)split, (unsigned)std::min<long long>(most, room[split]));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem_bytes(a.E);
     cfg.stream = s;
@@ -392,6 +427,11 @@ int launch(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
 
 int launch_grouped_few(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
     return a.y_dtype == QG_F32 ? launch<float>(dc, a, s) : launch<__nv_bfloat16>(dc, a, s);
+}
+
+long long grouped_few_chain(const DevCtx& dc, const GroupedArgs& a) {
+    FewPlan p;
+    return plan<float>(dc, a, &p) == QG_OK ? p.chain : 0x7FFFFFFFFFFFFFFFLL;
 }
 
 int weight_map(CUtensorMap* m, const GroupedArgs& a) {

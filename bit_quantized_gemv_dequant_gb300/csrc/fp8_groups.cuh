@@ -9,6 +9,31 @@ namespace fp8 {
 
 constexpr int kMaxExperts = 1024;
 
+// The number of expert e's rows, and the first of them. A range that is none
+// (outside of 0 .. M or backwards) is empty and recorded.
+__device__ __forceinline__ int rows_of(const int32_t* offsets, int e, int M, int* first, unsigned* err) {
+    const int lo = offsets[e], hi = offsets[e + 1];
+    *first = lo;
+    if (lo >= 0 && hi <= M && hi >= lo) return hi - lo;
+    report_error(err, DEVERR_INDEX);
+    return 0;
+}
+
+// a / b for a >= 0 and b > 0, in 32 bits where they do: several times shorter.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
+}
+
+// The sum of v over this lane and those below it.
+__device__ __forceinline__ long long warp_prefix(long long v) {
+#pragma unroll
+    for (int i = 1; i < 32; i *= 2) {
+        const long long below = __shfl_up_sync(0xFFFFFFFFu, v, i);
+        if ((threadIdx.x & 31) >= (unsigned)i) v += below;
+    }
+    return v;
+}
+
 // offsets[e] .. offsets[e + 1] - 1 are expert e's rows. Only the device knows
 // them, so each block finds the tiles of all experts by itself: an expert with n
 // rows has ceil(n / BN) chunks of rows, as even as whole STEPs allow, times nt
@@ -31,8 +56,7 @@ struct Groups {
         int e, n_tile, m0, rows;  // rows m0 .. m0 + rows - 1 of a
     };
 
-    // By one whole warp. Ranges that are none (outside of 0 .. M or backwards) count
-    // as empty and are recorded.
+    // By one whole warp.
     __device__ void build(const int32_t* offsets, int M, int nt, unsigned* err) {
         const int lane = threadIdx.x & 31;
         long long base = 0;
@@ -40,20 +64,12 @@ struct Groups {
             const int e = e0 + lane;
             int lo = 0, n = 0;
             if (e < E) {
-                lo = offsets[e];
-                const int hi = offsets[e + 1];
-                if (lo < 0 || hi > M || hi < lo) report_error(err, DEVERR_INDEX);
-                else n = hi - lo;
+                n = rows_of(offsets, e, M, &lo, err);
                 begin[e] = lo;
                 rows[e] = n;
             }
             const long long tiles = (long long)((n + BN - 1) / BN) * nt;
-            long long sum = tiles;
-#pragma unroll
-            for (int i = 1; i < 32; i *= 2) {
-                const long long below = __shfl_up_sync(0xFFFFFFFFu, sum, i);
-                if (lane >= i) sum += below;
-            }
+            const long long sum = warp_prefix(tiles);
             if (e < E) first[e] = base + sum - tiles;
             base += __shfl_sync(0xFFFFFFFFu, sum, 31);
         }
@@ -61,17 +77,20 @@ struct Groups {
         __syncwarp();
     }
 
-    // Tile t < first[E].
-    __device__ Tile find(long long t) const {
-        int e = 0;  // the last expert whose first tile is at most t: it has some
-        for (int i = kMaxExperts / 2; i; i /= 2)
-            if (e + i < E && first[e + i] <= t) e += i;
-        const int n = rows[e], chunks = (n + BN - 1) / BN;
-        const long long at = t - first[e];
-        const int n_tile = at <= 0x7FFFFFFF ? (int)at / chunks : (int)(at / chunks);
-        const int c = (int)(at - (long long)n_tile * chunks);
+    // Tile t < first[E], from one before it (or Tile{}).
+    __device__ void find(long long t, Tile& g) const {
+        if (first[g.e + 1] <= t) {  // the last expert whose first tile is at most t: it has some
+            ++g.e;
+            for (int i = 1 << (31 - __clz(E)); i; i /= 2)
+                if (g.e + i < E && first[g.e + i] <= t) g.e += i;
+        }
+        const int n = rows[g.e], chunks = (n + BN - 1) / BN;
+        const long long at = t - first[g.e];
+        g.n_tile = (int)quotient(at, chunks);
+        const int c = (int)(at - (long long)g.n_tile * chunks);
         const int each = ((n + chunks - 1) / chunks + STEP - 1) / STEP * STEP;
-        return Tile{e, n_tile, begin[e] + c * each, min(each, n - c * each)};
+        g.m0 = begin[g.e] + c * each;
+        g.rows = min(each, n - c * each);
     }
 };
 
@@ -86,28 +105,29 @@ struct GroupedParams {
 
 // Scales come through shared memory in sets of kSetBlocks k blocks, of which
 // kSets are under way: [k block][row of a] with w's scale of the tile's 128 weight
-// rows multiplied in. Two warps of 32 bring them (rows of a by thread, whose
-// blocks lie beside each other), running ahead of the products.
+// rows multiplied in. Two warps bring them, running ahead of the products. Eight
+// lanes read the k blocks of a row, which lie beside each other; the pitch puts
+// what a warp writes (8 blocks of 4 rows) into 32 banks.
 constexpr int kSetBlocks = 8, kSets = 4;
+constexpr int scale_pitch(int BN) { return BN + 4; }
 
 // One set: k blocks b .. b + n - 1 of the rows m0 .. m0 + rows - 1, by 64 threads.
 template <int BN>
 __device__ __forceinline__ void load_scales(float* set, const GroupedParams& p, const float* sw, int m0, int rows, int b,
                                             int n, int tid) {
-    float f[kSetBlocks];
+    const int i = tid % 8, m1 = tid / 8;
+    if (i >= n) return;
+    const float f = __ldg(sw + b + i);
+    const float* sa = p.sa + (long long)m0 * p.KB + b + i;
+    float* to = set + i * scale_pitch(BN);
+#pragma unroll 1
+    for (int j = 0; j < rows; j += 64) {
+        float v[8];
 #pragma unroll
-    for (int i = 0; i < kSetBlocks; ++i) f[i] = i < n ? __ldg(sw + b + i) : 0.f;
+        for (int k = 0; k < 8; ++k) v[k] = j + k * 8 + m1 < rows ? __ldg(sa + (long long)(j + k * 8 + m1) * p.KB) : 0.f;
 #pragma unroll
-    for (int j = 0; j < BN; j += 64) {
-        const int m = j + tid;
-        if (m < rows) {
-            const float* sa = p.sa + (long long)(m0 + m) * p.KB + b;
-            float v[kSetBlocks];
-#pragma unroll
-            for (int i = 0; i < kSetBlocks; ++i) v[i] = i < n ? __ldg(sa + i) : 0.f;
-#pragma unroll
-            for (int i = 0; i < kSetBlocks; ++i) set[i * BN + m] = v[i] * f[i];
-        }
+        for (int k = 0; k < 8; ++k)
+            if (j + k * 8 + m1 < rows) to[j + k * 8 + m1] = v[k] * f;
     }
 }
 
@@ -123,6 +143,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 int weight_map(CUtensorMap* m, const GroupedArgs& a);
 
 int launch_grouped_few(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s);
+// The k blocks that a CTA of launch_grouped_few takes one after the other, if no expert has more than 64 rows.
+long long grouped_few_chain(const DevCtx& dc, const GroupedArgs& a);
 int launch_grouped_tile(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s);
 
 }  // namespace fp8

@@ -90,5 +90,8 @@ int pad_rows(const DevCtx& dc, const uint8_t* src, uint8_t* dst, long long rows,
 // A 2-D map of rows x cols e4m3 codes, boxes of box_rows x 128, 128-byte swizzle.
 int code_map(CUtensorMap* m, const uint8_t* p, long long rows, long long cols, int box_rows);
 
+// y [rows, cols] of f32 or bf16 in boxes of 32 rows x 128 bytes, 128-byte swizzle (fp8_tile.cu).
+int out_map(CUtensorMap* m, void* y, int dtype, long long rows, long long cols);
+
 }  // namespace fp8
 }  // namespace qg

@@ -333,22 +333,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// y in boxes of 32 rows x 128 bytes.
-template <class TY>
-int out_map(CUtensorMap* m, const Fp8Args& a) {
-    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-    int rc = encoder(&encode);
-    if (rc) return rc;
-    const cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.M};
-    const cuuint64_t strides[1] = {(cuuint64_t)a.N * sizeof(TY)};
-    const cuuint32_t box[2] = {128 / sizeof(TY), 32}, es[2] = {1, 1};
-    return encode(m, sizeof(TY) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.y, dims,
-                  strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? QG_OK
-               : QG_ERR_UNSUPPORTED;
-}
-
 template <class TY>
 int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     static int configured[64] = {0};
@@ -369,7 +353,7 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     if (rc == QG_OK) rc = code_map(&mw, a.w, a.N, a.K, kBN / 2);
     // TMA stores want rows of y on 16-byte boundaries
     const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.N * sizeof(TY) % 16 == 0;
-    if (rc == QG_OK && vec) rc = out_map<TY>(&my, a);
+    if (rc == QG_OK && vec) rc = out_map(&my, a.y, a.y_dtype, a.M, a.N);
     if (rc) return rc;
     const Params p{a.sa, a.sw, a.y, (int)a.M, (int)a.N, (int)((a.K + 127) / 128), vec, dc.err};
     const long long tiles = ((a.M + 2 * kBM - 1) / (2 * kBM)) * ((a.N + kBN - 1) / kBN);
@@ -391,6 +375,21 @@ int launch(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+int out_map(CUtensorMap* m, void* y, int dtype, long long rows, long long cols) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    int rc = encoder(&encode);
+    if (rc) return rc;
+    const unsigned size = dtype == QG_F32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols * size};
+    const cuuint32_t box[2] = {128 / size, 32}, es[2] = {1, 1};
+    return encode(m, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, y, dims, strides, box,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QG_OK
+               : QG_ERR_UNSUPPORTED;
+}
 
 int launch_tile(const DevCtx& dc, const Fp8Args& a, cudaStream_t s) {
     return a.y_dtype == QG_F32 ? launch<float>(dc, a, s) : launch<__nv_bfloat16>(dc, a, s);
