@@ -41,23 +41,76 @@ __device__ __forceinline__ float2 cos_sin(uint64_t fraction) {
     return make_float2(c, s);
 }
 
+constexpr int kThreads = 256;
 constexpr int kAngles = 256;  // angles of a block's tokens, if it has several
 constexpr int kTokens = 8;    // tokens of a block at most
 
-// A block of (D / 8) x rows threads takes `per` tokens: their angles into shared
-// memory (one for all heads), then eight values of a head per thread, the heads of
-// q, k and v one after the other. Bound by the bytes of q, k and v, once each.
+// A block takes `per` tokens: their angles into shared memory (one for all heads),
+// then the heads of q, k and v of all its tokens one after the other, a head by the
+// threads of one threadIdx.y. Bound by the bytes of q, k and v, once each, next to
+// instruction issue; a thread has the loads of kBatch heads under way, the first
+// ones while the angles are worked out.
+//
+// PAIRED: 16 values of a head per thread, both members of eight pairs (or two runs
+// of eight that are not turned), so a pair's angle is read and its place worked out
+// once: 8192 tokens, 32 and 8 heads of 128, bf16, took 57 us with eight values per
+// thread, whose partners were loaded a second time. It needs D a multiple of 16 and
+// pairs that lie apart by a multiple of eight; other heads are turned value by value.
+//
 // Angle i of a token lies at chunk (i % 8) / 2, place i / 8: threads beside each
 // other, whose values are beside each other, read 16-byte words beside each other.
-template <class TX, class TC, bool VEC, bool INTER>
-__global__ void __launch_bounds__(1024) rope_kernel(const RopeArgs a, const int per, unsigned* err) {
+template <class TX, class TC, bool VEC, bool INTER, bool PAIRED>
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a, const int per, unsigned* err) {
+    constexpr int kRuns = PAIRED ? 2 : 1;  // of eight values per thread and head
+    constexpr int kBatch = sizeof(TX) == 4 ? 2 : 3;
     extern __shared__ float2 angles[];  // [per][4][places][2]
     const int n = a.rot / 2, places = (n + 7) / 8;
     const long long t0 = (long long)blockIdx.x * per;
     const int tokens = (int)min((long long)per, a.tokens - t0);
     const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
+    const int D = a.d, heads = a.hq + 2 * a.hkv, x = threadIdx.x;
+    const int log_page = 31 - __clz(a.page_size);
+    // Where this thread's runs begin: threads below n / 8 have the pairs that lie apart.
+    const bool apart = PAIRED && !INTER && x < n / 8;
+    const int d0 = !PAIRED || apart ? x * 8 : x * 16, d1 = apart ? d0 + n : d0 + 8;
+
+    struct Head {
+        const TX* src;
+        int t, h;  // h: over the heads of q, k and v; t = tokens: none
+    };
+    int t = 0, h = threadIdx.y;  // of the next head
+    auto next = [&] {
+        while (h >= heads && t < tokens) {
+            h -= heads;
+            ++t;
+        }
+        Head r{nullptr, t, h};
+        const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
+        const int skip = is_q ? 0 : is_k ? a.hq : a.hq + a.hkv;
+        r.src = static_cast<const TX*>(is_q ? a.q : is_k ? a.k : a.v) +
+                (t0 + t) * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) + (h - skip) * D;
+        h += blockDim.y;
+        return r;
+    };
+    Head head[kBatch];
+    Raw8<TX> raw[kBatch][kRuns];
+    auto load = [&] {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            head[i] = next();
+            if (head[i].t >= tokens) continue;
+            raw[i][0] = load8<TX, VEC>(head[i].src + d0, 8);
+            if constexpr (PAIRED) raw[i][1] = load8<TX, VEC>(head[i].src + d1, 8);
+        }
+    };
+    // (cos, sin) of pairs p and p + 1, p even
+    auto two_angles = [&](int t, int p) {
+        return reinterpret_cast<const float4*>(angles)[(t * 4 + p % 8 / 2) * places + p / 8];
+    };
+
     fp8::pdl_wait();
     fp8::pdl_trigger();
+    load();
     for (int i = tid; i < tokens * n; i += threads) {
         const int t = i / n, j = i - t * n;
         angles[((t * 4 + j % 8 / 2) * places + j / 8) * 2 + j % 2] =
@@ -65,76 +118,78 @@ __global__ void __launch_bounds__(1024) rope_kernel(const RopeArgs a, const int 
     }
     __syncthreads();
 
-    const int d0 = threadIdx.x * 8, D = a.d;
-    const int log_page = 31 - __clz(a.page_size);
-    const int heads = a.hq + 2 * a.hkv;
-    for (int t = 0; t < tokens; ++t) {
-        const int64_t slot = a.slots[t0 + t];
-        const int64_t page = slot >> log_page;
-        const bool bad = page >= a.num_pages;
-        if (bad && tid == 0) report_error(err, DEVERR_INDEX);
-        for (int h = threadIdx.y; h < heads; h += blockDim.y) {
-            const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
-            const int head = is_q ? h : is_k ? h - a.hq : h - a.hq - a.hkv;
-            const TX* src = static_cast<const TX*>(is_q ? a.q : is_k ? a.k : a.v) +
-                            (t0 + t) * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) + (long long)head * D;
-            float x[8], y[8];
-            to_f32(load8<TX, VEC>(src + d0, 8), x);
-            if ((is_q || is_k) && d0 < a.rot) {
-                if constexpr (INTER) {
+    for (; head[0].t < tokens; load()) {
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2) {  // pairs p and p + 1
-                        const int p = d0 / 2 + i;
-                        const float4 v = p < n ? reinterpret_cast<const float4*>(angles)[(t * 4 + p % 8 / 2) * places + p / 8]
-                                               : make_float4(1.f, 0.f, 1.f, 0.f);
-                        y[2 * i] = fmaf(x[2 * i + 1], -v.y, x[2 * i] * v.x);
-                        y[2 * i + 1] = fmaf(x[2 * i], v.y, x[2 * i + 1] * v.x);
-                        y[2 * i + 2] = fmaf(x[2 * i + 3], -v.w, x[2 * i + 2] * v.z);
-                        y[2 * i + 3] = fmaf(x[2 * i + 2], v.w, x[2 * i + 3] * v.z);
-                    }
+        for (int b = 0; b < kBatch; ++b) {
+            const int t = head[b].t, h = head[b].h;
+            if (t >= tokens) break;
+            float y[kRuns][8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (d0 + i >= a.rot) y[i] = x[i];
-                } else if (n % 8 == 0) {  // all eight are first members of their pairs, or all second ones
-                    const bool second = d0 >= n;
-                    const int p0 = second ? d0 - n : d0;
-                    float o[8];
-                    to_f32(load8<TX, VEC>(src + (second ? p0 : d0 + n), 8), o);
-                    const float4* cs = reinterpret_cast<const float4*>(angles) + t * 4 * places + p0 / 8;
+            for (int r = 0; r < kRuns; ++r) to_f32(raw[b][r], y[r]);
+            if (h >= a.hq + a.hkv) {
+            } else if (INTER) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 v = cs[i * places];
-                        const float s0 = second ? v.y : -v.y, s1 = second ? v.w : -v.w;
-                        y[2 * i] = fmaf(o[2 * i], s0, x[2 * i] * v.x);
-                        y[2 * i + 1] = fmaf(o[2 * i + 1], s1, x[2 * i + 1] * v.z);
-                    }
-                } else {
+                for (int r = 0; r < kRuns; ++r)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int d = d0 + i;
-                        y[i] = x[i];
-                        if (d < a.rot) {
-                            const bool second = d >= n;
-                            const int p = second ? d - n : d;
-                            const float2 cs = angles[((t * 4 + p % 8 / 2) * places + p / 8) * 2 + p % 2];
-                            const float o = to_f32(src[second ? p : d + n]);
-                            y[i] = fmaf(o, second ? cs.y : -cs.y, x[i] * cs.x);
+                    for (int i = 0; i < 8; i += 4) {
+                        const int p = (d0 + r * 8 + i) / 2;
+                        if (p >= n) continue;
+                        const float4 v = two_angles(t, p);
+                        const float* f = &y[r][i];
+                        const float o[4] = {fmaf(f[1], -v.y, f[0] * v.x), fmaf(f[0], v.y, f[1] * v.x),
+                                            fmaf(f[3], -v.w, f[2] * v.z), fmaf(f[2], v.w, f[3] * v.z)};
+                        y[r][i] = o[0];
+                        y[r][i + 1] = o[1];
+                        if (p + 1 < n) {
+                            y[r][i + 2] = o[2];
+                            y[r][i + 3] = o[3];
                         }
+                    }
+            } else if constexpr (PAIRED) {
+                if (apart) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const float4 v = two_angles(t, d0 + i);
+                        const float2 c = make_float2(v.x, v.z), s = make_float2(v.y, v.w);
+                        const float2 p = make_float2(y[0][i], y[0][i + 1]), q = make_float2(y[1][i], y[1][i + 1]);
+                        const float2 u = __ffma2_rn(make_float2(-q.x, -q.y), s, __fmul2_rn(p, c));
+                        const float2 w = __ffma2_rn(p, s, __fmul2_rn(q, c));
+                        y[0][i] = u.x;
+                        y[0][i + 1] = u.y;
+                        y[1][i] = w.x;
+                        y[1][i + 1] = w.y;
                     }
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = x[i];
+                for (int i = 0; i < 8; ++i) {
+                    const int d = d0 + i;
+                    if (d < a.rot) {
+                        const bool second = d >= n;
+                        const int p = second ? d - n : d;
+                        const float2 cs = angles[((t * 4 + p % 8 / 2) * places + p / 8) * 2 + p % 2];
+                        const float o = to_f32(head[b].src[second ? p : d + n]);
+                        y[0][i] = fmaf(o, second ? cs.y : -cs.y, y[0][i] * cs.x);
+                    }
+                }
             }
             TC* dst;
-            if (is_q) {
-                dst = static_cast<TC*>(a.q_out) + ((t0 + t) * a.hq + head) * D;
+            if (h < a.hq) {
+                dst = static_cast<TC*>(a.q_out) + ((t0 + t) * a.hq + h) * D;
             } else {
-                if (slot < 0 || bad) continue;
+                const int64_t slot = a.slots[t0 + t], page = slot >> log_page;
+                if (slot < 0) continue;
+                if (page >= a.num_pages) {
+                    report_error(err, DEVERR_INDEX);
+                    continue;
+                }
+                const bool is_k = h < a.hq + a.hkv;
+                const int at = h - a.hq - (is_k ? 0 : a.hkv);
                 dst = static_cast<TC*>(is_k ? a.k_cache : a.v_cache) +
-                      ((page * a.hkv + head) * a.page_size + (slot & (a.page_size - 1))) * D;
+                      ((page * a.hkv + at) * a.page_size + (slot & (a.page_size - 1))) * D;
             }
-            store8<TC, true>(dst + d0, y, 8);
+            store8<TC, true>(dst + d0, y[0], 8);
+            if constexpr (PAIRED) store8<TC, true>(dst + d1, y[1], 8);
         }
     }
 }
@@ -142,7 +197,9 @@ __global__ void __launch_bounds__(1024) rope_kernel(const RopeArgs a, const int 
 }  // namespace
 
 int kv_append_rope_launch(const DevCtx& dc, const RopeArgs& a, cudaStream_t s) {
-    const int cols = a.d / 8, rows = std::max(1, 256 / cols), n = a.rot / 2;
+    const int n = a.rot / 2;
+    const bool paired = a.d % 16 == 0 && (a.interleaved || n % 8 == 0);
+    const int cols = a.d / (paired ? 16 : 8), rows = std::max(1, kThreads / cols);
     // Enough tokens for an angle per thread, but first a block for every SM.
     const long long per = std::max<long long>(
         1, std::min<long long>(std::min(kAngles / n, kTokens), (a.tokens + dc.num_sms - 1) / dc.num_sms));
@@ -157,8 +214,14 @@ int kv_append_rope_launch(const DevCtx& dc, const RopeArgs& a, cudaStream_t s) {
         return by_type(a.cache_dtype, [&](auto tc) {
             using TC = decltype(tc);
             if constexpr (sizeof(TC) == 2) {
-                auto kern = a.interleaved ? (vec ? rope_kernel<TX, TC, true, true> : rope_kernel<TX, TC, false, true>)
-                                          : (vec ? rope_kernel<TX, TC, true, false> : rope_kernel<TX, TC, false, false>);
+                auto pick = [&](auto inter, auto pairs) {
+                    constexpr bool I = decltype(inter)::value, P = decltype(pairs)::value;
+                    return vec ? rope_kernel<TX, TC, true, I, P> : rope_kernel<TX, TC, false, I, P>;
+                };
+                using Yes = std::true_type;
+                using No = std::false_type;
+                auto kern = a.interleaved ? (paired ? pick(Yes{}, Yes{}) : pick(Yes{}, No{}))
+                                          : (paired ? pick(No{}, Yes{}) : pick(No{}, No{}));
                 return launch_after(kern, dim3((unsigned)grid), dim3(cols, rows), smem, s, a, (int)per, dc.err);
             } else {
                 return (int)QG_ERR_INVALID_ARG;

@@ -46,9 +46,7 @@ __global__ void __launch_bounds__(1024)
     const int step = threads * 8;
     float h[kHeld][8], sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < kHeld; ++c) {
-        load_h(tid * 8 + c * step, h[c]);
-    }
+    for (int c = 0; c < kHeld; ++c) load_h(tid * 8 + c * step, h[c]);
 #pragma unroll
     for (int c = 0; c < kHeld; ++c)
 #pragma unroll

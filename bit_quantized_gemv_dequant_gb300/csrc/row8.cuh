@@ -21,17 +21,21 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int left) {
         for (int i = 0; i < (int)sizeof(T) / 2; ++i)
             r.w[i] = left > 0 ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
     } else {
-        uint32_t u[2 * sizeof(T)];
-#pragma unroll
-        for (int i = 0; i < 2 * (int)sizeof(T); ++i) u[i] = 0;
+        uint32_t u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (i >= left) break;
-            if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(p[i]);
-            else u[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + i) << (16 * (i % 2));
+            u[i] = 0;
+            if (i < left) {
+                if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(p[i]);
+                else u[i] = *reinterpret_cast<const uint16_t*>(p + i);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+        if constexpr (sizeof(T) == 4) {
+            r.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+            r.w[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        } else {
+            r.w[0] = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+        }
     }
     return r;
 }
@@ -84,7 +88,7 @@ __device__ __forceinline__ void store8(void* p, long long at, int dtype, const f
     else store8<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16*>(p) + at, v, left);
 }
 
-// Eight codes, PER of them inside the row as above (VEC: on an 8-byte boundary).
+// Eight codes (VEC: on an 8-byte boundary).
 template <bool VEC>
 __device__ __forceinline__ void store_codes8(uint8_t* p, const uint32_t (&code)[2], int left) {
     if constexpr (VEC) {
