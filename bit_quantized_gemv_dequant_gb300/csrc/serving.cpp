@@ -6,9 +6,12 @@
 // through ctypes, of which the two launches are 7.
 #include <Python.h>
 
+#include <ATen/Context.h>
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -108,8 +111,15 @@ ScalarType type_of(PyObject* o, const char* name) {
     return reinterpret_cast<THPDtype*>(o)->scalar_type;
 }
 
+// A new tensor on like's device, as at::empty makes it, without its way through the
+// dispatcher (half of the time that a new output takes). A program that asks for
+// uninitialized memory to be filled gets at::empty.
 Tensor make(at::IntArrayRef size, ScalarType type, const Tensor& like) {
-    return at::empty(size, at::TensorOptions().dtype(type).device(like.device()));
+    if (at::globalContext().deterministicAlgorithms())
+        return at::empty(size, at::TensorOptions().dtype(type).device(like.device()));
+    const c10::cuda::OptionalCUDAGuard guard(like.device());
+    return at::detail::empty_generic(size, c10::cuda::CUDACachingAllocator::get(),
+                                     c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
 }
 
 template <class T = void>
