@@ -63,7 +63,7 @@ template <class TX, class TC, bool VEC, bool INTER, bool PAIRED>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a, const int per, unsigned* err) {
     constexpr int kRuns = PAIRED ? 2 : 1;  // of eight values per thread and head
     constexpr int kBatch = sizeof(TX) == 4 ? 2 : 3;
-    extern __shared__ float2 angles[];  // [per][4][places][2]
+    extern __shared__ __align__(16) float2 angles[];  // [per][4][places][2]
     const int n = a.rot / 2, places = (n + 7) / 8;
     const long long t0 = (long long)blockIdx.x * per;
     const int tokens = (int)min((long long)per, a.tokens - t0);
