@@ -43,7 +43,7 @@ __device__ __forceinline__ float2 cos_sin(uint64_t fraction) {
 
 constexpr int kThreads = 256;
 constexpr int kAngles = 256;  // angles of a block's tokens, if it has several
-constexpr int kTokens = 8;    // tokens of a block at most
+constexpr int kTokens = 2;    // tokens of a block at most
 
 // A block takes `per` tokens: their angles into shared memory (one for all heads),
 // then the heads of q, k and v of all its tokens one after the other, a head by the
@@ -62,7 +62,7 @@ constexpr int kTokens = 8;    // tokens of a block at most
 template <class TX, class TC, bool VEC, bool INTER, bool PAIRED>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a, const int per, unsigned* err) {
     constexpr int kRuns = PAIRED ? 2 : 1;  // of eight values per thread and head
-    constexpr int kBatch = sizeof(TX) == 4 ? 2 : 3;
+    constexpr int kBatch = 2;
     extern __shared__ __align__(16) float2 angles[];  // [per][4][places][2]
     const int n = a.rot / 2, places = (n + 7) / 8;
     const long long t0 = (long long)blockIdx.x * per;

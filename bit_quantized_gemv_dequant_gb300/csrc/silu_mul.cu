@@ -9,7 +9,7 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPer = 16;                      // values per thread
 constexpr int kLanes = kFp8Block / kPer;      // threads per scale
 constexpr int kUnits = kThreads / kLanes;     // scales per block

@@ -1,11 +1,14 @@
 """A decoder served from a paged cache, with this library's operators end to end.
 
-The model is small and random: two layers of 8 query heads on 2 key heads, block-scaled fp8 projections, a Q4_K
-output matrix. What it does is what a server does in every step:
+The model is small and random: two layers of 8 query heads on 2 key heads, block-scaled fp8 projections, four
+experts of which each token has two, a Q4_K output matrix. What it does is what a server does in every step:
 
+    rms_norm_fp8_b128, rms_norm       the residual stream's additions and norms, in codes for the products
     quantize_fp8_b128, qmm_fp8_b128   the projections of the step's tokens
-    kv_append                         their keys and values into their pages
+    kv_append_rope                    queries and keys turned by their positions, keys and values into their pages
     attn_paged                        prompts and single tokens of all sequences in one call
+    qmm_fp8_b128_grouped,             the experts' products, rows in the order of the experts,
+    silu_mul_fp8_b128                 and the gate between them
     qgemv_q4_k, token_logprobs        logits, the probability of the tokens that came, the alternatives
     kv_fork, kv_free, kv_compact      continuations of a sequence, its end, and a packed cache
 
@@ -24,6 +27,7 @@ import bit_quantized_gemv_dequant_gb300 as qg  # noqa: E402
 from bit_quantized_gemv_dequant_gb300 import synth  # noqa: E402
 
 LAYERS, HIDDEN, HEADS, KV_HEADS, DIM, VOCAB, PAGE = 2, 512, 8, 2, 64, 1024, 16
+EXPERTS, WIDE = 4, 384
 
 
 def fp8_weight(w):
@@ -33,6 +37,11 @@ def fp8_weight(w):
     scales = blocks.abs().amax((1, 3)) / 448.0
     codes = (blocks / scales[:, None, :, None]).view(n, k).to(torch.float8_e4m3fn)
     return codes, scales.contiguous()
+
+
+def experts(w):
+    """The same of all experts' weights [experts, N, K]."""
+    return tuple(torch.stack(t) for t in zip(*[fp8_weight(e) for e in w]))
 
 
 class Model:
@@ -46,6 +55,10 @@ class Model:
         width = (HEADS + 2 * KV_HEADS) * DIM
         self.qkv = [fp8_weight(normal(width, HIDDEN) * HIDDEN**-0.5) for _ in range(LAYERS)]
         self.out = [fp8_weight(normal(HIDDEN, HEADS * DIM) * HIDDEN**-0.5) for _ in range(LAYERS)]
+        self.norms = [torch.rand(HIDDEN, generator=g, device="cuda") + 0.5 for _ in range(2 * LAYERS + 1)]
+        self.up = [experts(normal(EXPERTS, 2 * WIDE, HIDDEN) * HIDDEN**-0.5) for _ in range(LAYERS)]
+        self.down = [experts(normal(EXPERTS, HIDDEN, WIDE) * WIDE**-0.5) for _ in range(LAYERS)]
+        self.inv_freq = 10000.0 ** (-torch.arange(0, DIM, 2, device="cuda") / DIM)
         self.head = torch.from_numpy(synth.q4_k_case(seed + 1, VOCAB, HIDDEN, 1)["w"]).cuda()
 
 
@@ -54,8 +67,19 @@ def linear(x, weight):
     return qg.qmm_fp8_b128(codes, scales, *weight)
 
 
-def norm(x):
-    return x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-6)
+def feed_forward(model, layer, codes, scales, tokens):
+    """Each token's two experts. (A trained model's router would choose them; here the token itself does.)"""
+    first = (tokens + layer) % EXPERTS
+    chosen = torch.stack([first, (first + 1 + tokens // EXPERTS % (EXPERTS - 1)) % EXPERTS], 1).flatten()
+    order = torch.argsort(chosen, stable=True)
+    ends = torch.bincount(chosen, minlength=EXPERTS).cumsum(0)
+    offsets = torch.cat([ends.new_zeros(1), ends]).to(torch.int32)
+    rows = order // 2
+    codes, scales = codes.view(torch.uint8)[rows].view(codes.dtype), scales[rows]
+    wide = qg.qmm_fp8_b128_grouped(codes, scales, *model.up[layer], offsets)
+    codes, scales = qg.silu_mul_fp8_b128(wide[:, :WIDE], wide[:, WIDE:])
+    narrow = qg.qmm_fp8_b128_grouped(codes, scales, *model.down[layer], offsets)
+    return narrow[torch.argsort(order)].view(len(tokens), 2, HIDDEN).sum(1)
 
 
 class Cache:
@@ -73,18 +97,20 @@ class Cache:
         return self.table.shape[0] - 1
 
     def grow(self, counts):
-        """Pages for counts[r] more tokens of each row, the lowest free ones; slots of the new tokens, row by row."""
+        """Pages for counts[r] more tokens of each row, the lowest free ones; slots and positions of the new tokens, row by
+        row."""
         table, lens, refs = self.table.cpu(), self.lens.cpu(), self.refs.cpu()
-        free, slots = iter((refs == 0).nonzero().flatten().tolist()), []
+        free, slots, positions = iter((refs == 0).nonzero().flatten().tolist()), [], []
         for r, n in enumerate(counts):
             for t in range(int(lens[r]), int(lens[r]) + n):
                 if table[r, t // PAGE] < 0:
                     page = next(free)
                     table[r, t // PAGE], refs[page] = page, 1
                 slots.append(int(table[r, t // PAGE]) * PAGE + t % PAGE)
+                positions.append(t)
             lens[r] += n
         self.table, self.lens, self.refs = table.cuda(), lens.cuda(), refs.cuda()
-        return torch.tensor(slots, dtype=torch.int64, device="cuda")
+        return torch.tensor(slots, device="cuda"), torch.tensor(positions, device="cuda")
 
     def fork(self, parents):
         parents = torch.tensor(parents, dtype=torch.int32, device="cuda")
@@ -106,17 +132,24 @@ class Cache:
 def step(model, cache, new):
     """Logits after each of the new tokens: new[r] lists those of row r (none is fine)."""
     counts = [len(t) for t in new]
-    slots = cache.grow(counts)
+    slots, positions = cache.grow(counts)
     offsets = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
-    x = model.embed[torch.tensor([t for row in new for t in row], device="cuda")]
+    tokens = torch.tensor([t for row in new for t in row], device="cuda")
+    x = model.embed[tokens]  # the residual stream
+    codes, scales = qg.rms_norm_fp8_b128(x, model.norms[0])
     for layer in range(LAYERS):
-        qkv = linear(norm(x), model.qkv[layer]).view(len(x), HEADS + 2 * KV_HEADS, DIM)
+        qkv = qg.qmm_fp8_b128(codes, scales, *model.qkv[layer]).view(len(x), HEADS + 2 * KV_HEADS, DIM)
         k_cache, v_cache = cache.planes[2 * layer], cache.planes[2 * layer + 1]
-        qg.kv_append(qkv[:, HEADS:HEADS + KV_HEADS], qkv[:, HEADS + KV_HEADS:], k_cache, v_cache, slots)
-        heads = qg.attn_paged(qkv[:, :HEADS].to(torch.bfloat16), k_cache, v_cache, cache.table, offsets, cache.lens,
-                              max_new=max(counts))
-        x = x + linear(heads.view(len(x), HEADS * DIM), model.out[layer])
-    return qg.qgemv_q4_k(model.head, norm(x).contiguous(), N=VOCAB)
+        q = qg.kv_append_rope(qkv[:, :HEADS], qkv[:, HEADS:HEADS + KV_HEADS], qkv[:, HEADS + KV_HEADS:], positions,
+                              model.inv_freq, k_cache, v_cache, slots)
+        heads = qg.attn_paged(q, k_cache, v_cache, cache.table, offsets, cache.lens, max_new=max(counts))
+        out = linear(heads.view(len(x), HEADS * DIM), model.out[layer])
+        codes, scales, x = qg.rms_norm_fp8_b128(out, model.norms[2 * layer + 1], x)
+        out = feed_forward(model, layer, codes, scales, tokens)
+        if layer + 1 < LAYERS:
+            codes, scales, x = qg.rms_norm_fp8_b128(out, model.norms[2 * layer + 2], x)
+    last, _ = qg.rms_norm(out, model.norms[-1], x)
+    return qg.qgemv_q4_k(model.head, last, N=VOCAB)
 
 
 def next_logprobs(logits, tokens):
