@@ -10,6 +10,13 @@ namespace qg {
 
 constexpr int kFp8Block = 128;   // values per scale
 
+// The largest magnitude of three, NaN above infinity.
+__device__ __forceinline__ float fp8_largest(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // The scale of a block whose largest |x| has the bits `top`.
 __device__ __forceinline__ float fp8_scale(unsigned top) {
     const float scale = __fdiv_rn(__uint_as_float(top), 448.f);

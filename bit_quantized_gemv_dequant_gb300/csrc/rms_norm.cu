@@ -32,13 +32,26 @@ __global__ void __launch_bounds__(1024)
     fp8::pdl_wait();
     fp8::pdl_trigger();
 
+    // Rows that do not lie in eights go through a warp's kilobyte of shared memory.
+    extern __shared__ __align__(16) uint32_t tiles[];
+    uint32_t* tile = tiles + (threadIdx.x / 32) * 256;
+    const int lane8 = (threadIdx.x & 31) * 8;
+    auto load = [&](auto* p, int k, int left, float (&v)[8]) {  // p[k .. k + 8), a warp's threads together
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+        if constexpr (VEC) to_f32(load8<T, true>(p + k, left), v);
+        else load8_warp(p + k - lane8, left + lane8, tile, v);
+    };
+    auto store = [&](auto* p, int k, int left, const float (&v)[8]) {
+        using T = std::remove_pointer_t<decltype(p)>;
+        if constexpr (VEC) store8<T, true>(p + k, v, left);
+        else store8_warp(p + k - lane8, v, left + lane8, tile);
+    };
     auto load_h = [&](int k, float (&h)[8]) {
-        const int left = live ? K - k : 0;
-        const Raw8<TX> xr = load8<TX, VEC>(x + k, left);
-        to_f32(xr, h);
+        const int left = live ? K - k : -lane8;
+        load(x, k, left, h);
         if (has_res) {
             float f[8];
-            to_f32(load8<TR, VEC>(r + k, left), f);
+            load(r, k, left, f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[i] += f[i];
         }
@@ -51,9 +64,9 @@ __global__ void __launch_bounds__(1024)
     for (int c = 0; c < kHeld; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(h[c][i], h[c][i], sum);
-    for (int k = tid * 8 + kHeld * step; k < K; k += step) {
+    for (int k0 = kHeld * step; k0 < K; k0 += step) {
         float f[8];
-        load_h(k, f);
+        load_h(k0 + tid * 8, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
     }
@@ -67,42 +80,44 @@ __global__ void __launch_bounds__(1024)
         for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
     }
     // correctly rounded division and root: rows of few values are as exact as long ones
-    const float s = __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, (float)K) + a.eps));
+    const float root = __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, (float)K) + a.eps));
+    const float s = FP8 ? -root : root;  // codes are made from -y
 
     auto finish = [&](int k, const float (&f)[8]) {
-        const int left = live ? K - k : 0;
-        if (has_res) store8<TR, VEC>(r_out + k, f, left);
+        const int left = live ? K - k : -lane8;
+        if (has_res) store(r_out, k, left, f);
         float y[8];
+        const float s0 = VEC && left <= 0 ? 0.f : s;  // (behind the row's end f is 0 and s may be infinite)
         if (a.w) {
             float w[8];
-            const int wl = K - k;
-            if (a.w_dtype == QG_F32) to_f32(load8<float, VEC>(static_cast<const float*>(a.w) + k, wl), w);
-            else if (a.w_dtype == QG_F16) to_f32(load8<__half, VEC>(static_cast<const __half*>(a.w) + k, wl), w);
-            else to_f32(load8<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(a.w) + k, wl), w);
+            with_type(a.w_dtype, [&](auto t) { load(static_cast<const decltype(t)*>(a.w), k, K - k, w); });
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = f[i] * s * (w[i] + a.offset);
+            for (int i = 0; i < 8; ++i) y[i] = f[i] * s0 * (w[i] + a.offset);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = f[i] * s;
+            for (int i = 0; i < 8; ++i) y[i] = f[i] * s0;
         }
         if constexpr (FP8) {
-            unsigned top = 0;
-            float minus[8];
+            if constexpr (!VEC) {  // what lies behind the row's end is 0 whatever s is
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // what lies behind the row's end is 0 whatever s is
-                minus[i] = i < left ? -y[i] : 0.f;
-                top = max(top, __float_as_uint(minus[i]) & 0x7FFFFFFFu);
+                for (int i = 0; i < 8; ++i)
+                    if (i >= left) y[i] = 0.f;
             }
+            float most = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) most = fp8_largest(most, y[i], y[i + 1]);
+            unsigned top = __float_as_uint(most) & 0x7FFFFFFFu;
 #pragma unroll
             for (int i = 8; i; i >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
             const float scale = fp8_scale(top);
             uint32_t code[2];
-            fp8_encode<8>(minus, scale, code);
-            store_codes8<VEC>(static_cast<uint8_t*>(a.y) + m * K + k, code, left);
+            fp8_encode<8>(y, scale, code);
+            uint8_t* to = static_cast<uint8_t*>(a.y) + m * K + k;
+            if constexpr (VEC) store_codes8<true>(to, code, left);
+            else store_codes8_warp(to - lane8, code, left + lane8, tile);
             if (tid % 16 == 0 && left > 0) a.scales[m * ((K + 127) / 128) + k / 128] = scale;
         } else {
-            store8<VEC>(a.y, m * K + k, a.y_dtype, y, left);
+            with_type(a.y_dtype, [&](auto t) { store(static_cast<decltype(t)*>(a.y) + m * K, k, left, y); });
         }
     };
 #pragma unroll
@@ -127,7 +142,7 @@ int launch(const NormArgs& a, cudaStream_t s) {
     const long long grid = (a.M + block / threads - 1) / (block / threads);
     if (grid > 0x7FFFFFFFLL) return QG_ERR_UNSUPPORTED;
     return launch_after(vec ? norm_kernel<TX, TR, FP8, true> : norm_kernel<TX, TR, FP8, false>, dim3((unsigned)grid),
-                        dim3(block), 0, s, a, (int)a.K, threads);
+                        dim3(block), vec ? 0 : block * 32, s, a, (int)a.K, threads);
 }
 
 template <class TX, class TR>

@@ -100,6 +100,53 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, const uint32_t (&code)[
     }
 }
 
+// The same for a warp's 256 values that lie anywhere: 32 places beside each other at a
+// time, by way of 1 KB of shared memory (`tile`, the warp's own). p is the place of
+// its first value, `left` how many of the row there are from there on. Of 37 rows of
+// 5201 f32 values value by value took rms_norm 7.1 us.
+template <class T>
+__device__ __forceinline__ void load8_warp(const T* p, int left, uint32_t* tile, float (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i * 32 + lane < left ? to_f32(p[i * 32 + lane]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tile[i * 32 + lane] = __float_as_uint(f[i]);
+    __syncwarp();
+    Raw8<float> r;
+    r.w[0] = reinterpret_cast<const uint4*>(tile)[2 * lane];
+    r.w[1] = reinterpret_cast<const uint4*>(tile)[2 * lane + 1];
+    to_f32(r, v);
+    __syncwarp();
+}
+template <class T>
+__device__ __forceinline__ void store8_warp(T* p, const float (&v)[8], int left, uint32_t* tile) {
+    const int lane = threadIdx.x & 31;
+    store8<float, true>(reinterpret_cast<float*>(tile) + 8 * lane, v, 8);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i * 32 + lane < left) p[i * 32 + lane] = from_f32<T>(__uint_as_float(tile[i * 32 + lane]));
+    __syncwarp();
+}
+__device__ __forceinline__ void store_codes8_warp(uint8_t* p, const uint32_t (&code)[2], int left, uint32_t* tile) {
+    const int lane = threadIdx.x & 31;
+    reinterpret_cast<uint2*>(tile)[lane] = make_uint2(code[0], code[1]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i * 32 + lane < left) p[i * 32 + lane] = reinterpret_cast<const uint8_t*>(tile)[i * 32 + lane];
+    __syncwarp();
+}
+
+// f(T{}) for an element type known at run time, in a kernel.
+template <class F>
+__device__ __forceinline__ void with_type(int dtype, F&& f) {
+    if (dtype == QG_F32) f(float{});
+    else if (dtype == QG_F16) f(__half{});
+    else f(__nv_bfloat16{});
+}
+
 // Whether rows of `width` values that lie `stride` elements apart can be moved in
 // units of eight.
 inline bool in_eights(const void* p, long long stride, long long width, int elem_bytes) {

@@ -43,13 +43,6 @@ __device__ __forceinline__ float2 gated(float2 g, float2 u) {
     return __fmul2_rn(__fmul2_rn(g, make_float2(reciprocal_approx(d.x), reciprocal_approx(d.y))), u);
 }
 
-// The largest magnitude of three, NaN above infinity.
-__device__ __forceinline__ float largest(float a, float b, float c) {
-    float d;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // Sixteen values per thread, eight threads per scale. Bound by the bytes of g, u and
 // y next to instruction issue: with a library's exponential and a division per value
 // and eight values per thread 4096 x 12288 bf16 to codes took 58.7 us.
@@ -90,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(const GateArgs a, const 
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) most = largest(most, y[h][i], y[h][i + 1]);
+            for (int i = 0; i < 8; i += 2) most = fp8_largest(most, y[h][i], y[h][i + 1]);
         unsigned top = __float_as_uint(most) & 0x7FFFFFFFu;
 #pragma unroll
         for (int i = kLanes / 2; i; i >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
