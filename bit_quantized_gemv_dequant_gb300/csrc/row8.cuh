@@ -12,8 +12,9 @@ struct Raw8 {
 };
 
 // The values p[0 .. 8), of which `left` are inside the row (VEC: all or none, and
-// p on a 16-byte boundary); those that are not are 0.
-template <class T, bool VEC>
+// p on a 16-byte boundary); those that are not are 0. Without VEC they may lie STEP
+// apart, so that threads beside each other read places beside each other.
+template <class T, bool VEC, int STEP = 1>
 __device__ __forceinline__ Raw8<T> load8(const T* p, int left) {
     Raw8<T> r;
     if constexpr (VEC) {
@@ -25,9 +26,9 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int left) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             u[i] = 0;
-            if (i < left) {
-                if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(p[i]);
-                else u[i] = *reinterpret_cast<const uint16_t*>(p + i);
+            if (i * STEP < left) {
+                if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(p[i * STEP]);
+                else u[i] = *reinterpret_cast<const uint16_t*>(p + i * STEP);
             }
         }
         if constexpr (sizeof(T) == 4) {
@@ -62,7 +63,7 @@ __device__ __forceinline__ void to_f32(const Raw8<T>& r, float (&v)[8]) {
 }
 
 // p[0 .. min(8, left)) = v; VEC as above.
-template <class T, bool VEC>
+template <class T, bool VEC, int STEP = 1>
 __device__ __forceinline__ void store8(T* p, const float (&v)[8], int left) {
     if constexpr (VEC) {
         if (left <= 0) return;
@@ -76,27 +77,19 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int left) {
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = from_f32<T>(v[i]);
+            if (i * STEP < left) p[i * STEP] = from_f32<T>(v[i]);
     }
 }
 
-// The same for a type known at run time, at element `at` of an array.
-template <bool VEC>
-__device__ __forceinline__ void store8(void* p, long long at, int dtype, const float (&v)[8], int left) {
-    if (dtype == QG_F32) store8<float, VEC>(static_cast<float*>(p) + at, v, left);
-    else if (dtype == QG_F16) store8<__half, VEC>(static_cast<__half*>(p) + at, v, left);
-    else store8<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16*>(p) + at, v, left);
-}
-
 // Eight codes (VEC: on an 8-byte boundary).
-template <bool VEC>
+template <bool VEC, int STEP = 1>
 __device__ __forceinline__ void store_codes8(uint8_t* p, const uint32_t (&code)[2], int left) {
     if constexpr (VEC) {
         if (left > 0) *reinterpret_cast<uint2*>(p) = make_uint2(code[0], code[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = (uint8_t)(code[i / 4] >> (8 * (i % 4)));
+            if (i * STEP < left) p[i * STEP] = (uint8_t)(code[i / 4] >> (8 * (i % 4)));
     }
 }
 
