@@ -22,9 +22,14 @@ namespace {
 //   warps 4-11  take the accumulators into registers, times both scales (f32):
 //               thread = row of w, and 32 of the 64 rows of a
 //
-// With a split the parts of a tile meet in shared memory over the cluster, each CTA
-// adding up its share of the rows of a in the order of the split: the result does
-// not depend on timing.
+// 256 rows on 64 experts, N = K = 4096, bf16: 153 us, 6.7 TB/s. 8 rows on 8 of them, N =
+// 4096, K = 2048: 17.0 us, 4.0 TB/s: 256 tiles on 152 SMs, the second round as slow as
+// the first; 3 us until the first k block is there.
+//
+// Tiles that do not fill a round of all CTAs are shared, by K, over a cluster (9
+// experts of 34 rows, N = 2200, K = 5200: 27.5 us, 35 without). Its parts meet in
+// shared memory over the cluster, each CTA adding up its share of the rows of a in the
+// order of the split: the result does not depend on timing.
 constexpr int kBN = 64;
 constexpr int kThreads = 384, kEpi = 256;
 constexpr int kStages = 7, kStage = 16384 + kBN * 128;

@@ -43,7 +43,7 @@ __device__ __forceinline__ float2 cos_sin(uint64_t fraction) {
 
 constexpr int kThreads = 256;
 constexpr int kAngles = 256;  // angles of a block's tokens, if it has several
-constexpr int kTokens = 2;    // tokens of a block at most
+constexpr int kTokens = 2;    // tokens of a block at most (36.8 us; one 50.7, up to eight 37.4)
 
 // A block takes `per` tokens: their angles into shared memory (one for all heads),
 // then the heads of q, k and v of all its tokens one after the other, a head by the
@@ -53,8 +53,8 @@ constexpr int kTokens = 2;    // tokens of a block at most
 //
 // PAIRED: 16 values of a head per thread, both members of eight pairs (or two runs
 // of eight that are not turned), so a pair's angle is read and its place worked out
-// once: 8192 tokens, 32 and 8 heads of 128, bf16, took 57 us with eight values per
-// thread, whose partners were loaded a second time. It needs D a multiple of 16 and
+// once: 8192 tokens, 32 and 8 heads of 128, bf16: 36.8 us, 5.5 TB/s; 57 us with eight
+// values per thread, whose partners were loaded a second time. It needs D a multiple of 16 and
 // pairs that lie apart by a multiple of eight; other heads are turned value by value.
 //
 // Angle i of a token lies at chunk (i % 8) / 2, place i / 8: threads beside each

@@ -44,8 +44,8 @@ __device__ __forceinline__ float2 gated(float2 g, float2 u) {
 }
 
 // Sixteen values per thread, eight threads per scale. Bound by the bytes of g, u and
-// y next to instruction issue: with a library's exponential and a division per value
-// and eight values per thread 4096 x 12288 bf16 to codes took 58.7 us.
+// y next to instruction issue (72 % of all slots): 4096 x 12288 bf16 to codes 42.5 us,
+// 6.0 TB/s; with a library's exponential and division and eight values per thread 58.7.
 template <class T, bool FP8, bool VEC>
 __global__ void __launch_bounds__(kThreads) gate_kernel(const GateArgs a, const int K, const int KB) {
     constexpr int kSign = FP8 ? -1 : 1;

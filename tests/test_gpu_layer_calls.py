@@ -329,3 +329,26 @@ def test_wide_codes_and_scales():
         c = Experts(61, counts, 384, 1024)
         c.a, c.sa = codes_like(g, *c.a.shape), scales_like(g, *c.sa.shape)
         c.check(c.run())
+
+
+def test_first_calls_of_a_process_are_captured():
+    """No call before the capture: what a kernel's first call sets up and asks for is allowed there."""
+    code = """
+import sys, torch
+sys.path[:0] = ["tests", "."]
+import bit_quantized_gemv_dequant_gb300 as qg
+import test_gpu_layer_calls as t
+m, few, many, odd = t.Layer(1), t.Experts(2, [3, 9], 256, 512), t.Experts(3, [300, 520], 256, 512), t.Experts(4, [3, 9], 40, 250)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = m.step(), few.run(), many.run(), odd.run()
+graph.replay()
+torch.cuda.synchronize()
+got = {k: v.clone() for k, v in out[0].items()}, [v.clone() for v in out[1:]]
+assert t.same(got[0], m.step()) and all(torch.equal(a, b) for a, b in zip(got[1], (few.run(), many.run(), odd.run())))
+assert qg.device_error() == 0
+print("done")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["done"], (r.returncode, r.stdout, r.stderr[-2000:])
