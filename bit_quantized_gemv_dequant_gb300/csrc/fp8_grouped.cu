@@ -108,11 +108,12 @@ int fp8_grouped_launch(const DevCtx& dc, const GroupedArgs& args, void* ws, size
     auto fits = [&](const uint8_t* p) { return a.K == pitch && reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     bool tma = fits(a.a) && fits(a.w);
     if (!tma && pitch <= 0x7FFFFFFF && ws_bytes >= (size_t)((a.M + a.E * a.N) * pitch)) {
-        // Zeros after the end of a row add nothing, and the blocks of 128 are the same.
+        // Zeros after the end of a row add nothing, and the blocks of 128 are the same. Of w
+        // only the experts that have rows are copied.
         uint8_t* p = static_cast<uint8_t*>(ws);
         int rc = QG_OK;
         if (!fits(a.w)) {
-            rc = fp8::pad_rows(dc, a.w, p, a.E * a.N, a.K, pitch, s);
+            rc = fp8::pad_rows(dc, a.w, p, a.E * a.N, a.K, pitch, s, a.offsets, a.N);
             a.w = p;
             p += a.E * a.N * pitch;
         }

@@ -75,15 +75,37 @@ __global__ void __launch_bounds__(kGThreads)
 // dst[r][c] = src[r][c] for c < K, 0 up to the pitch (a multiple of 16); src's
 // rows start at any byte. 16 bytes per thread, from the five aligned words that
 // hold them; where those are not all inside src, byte by byte.
-constexpr int kPadThreads = 256;
+constexpr int kPadThreads = 256, kMaxGroups = 1024;
 __global__ void __launch_bounds__(kPadThreads)
-    pad_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, long long rows, int K, int pitch) {
+    pad_kernel(const uint8_t* __restrict__ src, uint8_t* __restrict__ dst, long long rows, int K, int pitch,
+               const int32_t* __restrict__ offsets, int group) {
+    __shared__ short used[kMaxGroups];
+    __shared__ int count;
+    if (offsets) {  // the groups that have something
+        if (threadIdx.x < 32) {
+            int n = 0;
+            for (int g0 = 0; g0 < (int)(rows / group); g0 += 32) {
+                const int g = g0 + threadIdx.x;
+                const bool some = g < (int)(rows / group) && offsets[g] < offsets[g + 1];
+                const unsigned mask = __ballot_sync(0xFFFFFFFFu, some);
+                if (some) used[n + __popc(mask & ((1u << threadIdx.x) - 1u))] = (short)g;
+                n += __popc(mask);
+            }
+            if (threadIdx.x == 0) count = n;
+        }
+        __syncthreads();
+    }
+    const long long some_rows = offsets ? (long long)count * group : rows;
     const int per = pitch / 16;
     const uintptr_t begin = reinterpret_cast<uintptr_t>(src), end = begin + rows * K;
-    for (long long i = (long long)blockIdx.x * kPadThreads + threadIdx.x; i < rows * per;
+    for (long long i = (long long)blockIdx.x * kPadThreads + threadIdx.x; i < some_rows * per;
          i += (long long)gridDim.x * kPadThreads) {
-        const long long r = i < 0x7FFFFFFF ? (int)i / per : i / per;
+        long long r = i < 0x7FFFFFFF ? (int)i / per : i / per;
         const int c = (int)(i - r * per) * 16, n = min(16, K - c);
+        if (offsets) {
+            const int g = (int)((uint32_t)r / (uint32_t)group);
+            r += (long long)(used[g] - g) * group;
+        }
         const uintptr_t at = begin + r * K + c, word = at & ~(uintptr_t)3;
         const int shift = (int)(at - word) * 8;
         uint32_t v[5];
@@ -113,10 +135,10 @@ __global__ void __launch_bounds__(kPadThreads)
 }  // namespace
 
 int fp8::pad_rows(const DevCtx& dc, const uint8_t* src, uint8_t* dst, long long rows, long long K, long long pitch,
-                  cudaStream_t s) {
+                  cudaStream_t s, const int32_t* offsets, long long group) {
     const long long ctas = (rows * (pitch / 16) + kPadThreads - 1) / kPadThreads;
     pad_kernel<<<(unsigned)(ctas < dc.num_sms * 16LL ? ctas : dc.num_sms * 16LL), kPadThreads, 0, s>>>(
-        src, dst, rows, (int)K, (int)pitch);
+        src, dst, rows, (int)K, (int)pitch, offsets, (int)group);
     return launched();
 }
 

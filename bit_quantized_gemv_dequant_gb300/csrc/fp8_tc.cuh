@@ -84,8 +84,10 @@ bool swap_is_shorter(const DevCtx& dc, const Fp8Args& a);
 int launch_tile(const DevCtx& dc, const Fp8Args& a, cudaStream_t s);
 
 // dst = src's rows of K bytes, which start at any byte, with zeros up to the pitch, a
-// multiple of 16 (fp8_mm.cu).
-int pad_rows(const DevCtx& dc, const uint8_t* src, uint8_t* dst, long long rows, long long K, long long pitch, cudaStream_t s);
+// multiple of 16 (fp8_mm.cu). With offsets, which say what groups of rows are for, those
+// of a group that has nothing (offsets[g] .. offsets[g + 1] - 1) are left out.
+int pad_rows(const DevCtx& dc, const uint8_t* src, uint8_t* dst, long long rows, long long K, long long pitch, cudaStream_t s,
+             const int32_t* offsets = nullptr, long long group = 0);
 
 // A 2-D map of rows x cols e4m3 codes, boxes of box_rows x 128, 128-byte swizzle.
 int code_map(CUtensorMap* m, const uint8_t* p, long long rows, long long cols, int box_rows);
