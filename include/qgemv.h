@@ -415,8 +415,8 @@ QG_API int attn_paged_workspace_size(int64_t tokens, int64_t batch, int64_t max_
  * rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0. Pair i of row t is
  * turned by the angle positions[t] * inv_freq[i]:
  *   (a, b) -> (a cos - b sin, b cos + a sin),
- * in f32 from the exact angle (for any position below 2^31 of either sign, to
- * 2^-23 of a turn's sine), the rest of a head is not turned. q [tokens,
+ * in f32 from the exact angle (for positions below 2^31, of either sign); the
+ * rest of a head is not turned. q [tokens,
  * q_heads, head_dim] (x_dtype, rows q_stride apart) goes to q_out, dense, in
  * cache_dtype; with q_heads = 0 there is none. k and v go to slots[t] as in
  * kv_append; rows with a negative slot get their q_out all the same.
