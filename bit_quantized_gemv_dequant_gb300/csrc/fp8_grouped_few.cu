@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                load_scales<kBN>(scales + set * (kSetBlocks * kPitch), p, sw, g.m0, g.rows, b, min(kSetBlocks, b1 - b), tid);
+                load_scales<kBN, 8>(scales + set * (kSetBlocks * kPitch), p, sw, nullptr, g.m0, g.rows, b, min(kSetBlocks, b1 - b), tid);
                 mbar_arrive(s_full(set));
                 if (++set == kSets) {
                     set = 0;

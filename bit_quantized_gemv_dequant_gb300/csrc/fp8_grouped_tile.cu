@@ -20,11 +20,12 @@ namespace {
 //   of every eight columns, and needs 32 scales per k block. (With a row and all 128
 //   columns it would need 128, and shared memory is busy with the operands. 16 lanes
 //   at a time is half of what tensor memory delivers: uniform chunks of 256 rows
-//   take 294 us like that and 246 as M, 16384 rows on 32 experts, N = K = 4096.)
+//   take 294 us like that and 243 as M, 16384 rows on 32 experts, N = K = 4096.)
 //
 // A k block of a whole chunk takes about 970 cycles (512 of products; the round trip
 // of accumulators and their promotion), of one of 64 rows 640. 16384 rows unevenly on
-// 32 experts: 306 to 316 us, 1.74 to 1.80 PFLOP/s, SM clock 2030 MHz at the power limit.
+// 32 experts: 299 to 313 us, 1.76 to 1.84 PFLOP/s, SM clock 1950 to 2040 MHz at the power
+// limit.
 //
 //   warps 0-7    epilogue; 216 registers each, which warps 8-11 give up
 //   warp 8       TMA producer, whose copies complete on the first CTA's barrier
@@ -292,10 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float* to = scales + set * (kSetBlocks * kPitch);
                     const int n = min(kSetBlocks, p.KB - b);
                     if (g.rows == kBN) {  // [half of the columns][this CTA's 128 rows]
-                        load_scales<kBN>(to, p, halves[0], g.m0 + rank * kBM, kBM, b, n, tid);
-                        load_scales<kBN>(to + kBM, p, halves[1], g.m0 + rank * kBM, kBM, b, n, tid);
+                        load_scales<kBN, 16, kBM>(to, p, halves[0], halves[1], g.m0 + rank * kBM, kBM, b, n, tid);
                     } else {
-                        load_scales<kBN>(to, p, own, g.m0, g.rows, b, n, tid);
+                        load_scales<kBN, 16>(to, p, own, nullptr, g.m0, g.rows, b, n, tid);
                     }
                     mbar_arrive(s_full(set));
                     if (++set == kTileSets) {

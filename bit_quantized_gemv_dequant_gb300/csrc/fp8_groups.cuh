@@ -111,23 +111,30 @@ struct GroupedParams {
 constexpr int kSetBlocks = 8, kSets = 4;
 constexpr int scale_pitch(int BN) { return BN + 4; }
 
-// One set: k blocks b .. b + n - 1 of the rows m0 .. m0 + rows - 1, by 64 threads.
-template <int BN>
-__device__ __forceinline__ void load_scales(float* set, const GroupedParams& p, const float* sw, int m0, int rows, int b,
-                                            int n, int tid) {
+// One set: k blocks b .. b + n - 1 of the rows m0 .. m0 + rows - 1, by 64 threads, with
+// the factors of one block of w's rows, or of two (the second one's products from
+// column kSecond on). 8 LOADS rows are under way at a time: loads are slow beside the
+// operands' (many rows per expert: 305 us with 64 rows at a time and a reading of sa for
+// each of two factors, 299 with 128 rows and one).
+template <int BN, int LOADS, int kSecond = 0>
+__device__ __forceinline__ void load_scales(float* set, const GroupedParams& p, const float* sw, const float* sw2, int m0,
+                                            int rows, int b, int n, int tid) {
     const int i = tid % 8, m1 = tid / 8;
     if (i >= n) return;
-    const float f = __ldg(sw + b + i);
+    const float f = __ldg(sw + b + i), f2 = kSecond ? __ldg(sw2 + b + i) : 0.f;
     const float* sa = p.sa + (long long)m0 * p.KB + b + i;
     float* to = set + i * scale_pitch(BN);
 #pragma unroll 1
-    for (int j = 0; j < rows; j += 64) {
-        float v[8];
+    for (int j = m1; j < rows; j += 8 * LOADS) {
+        float v[LOADS];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = j + k * 8 + m1 < rows ? __ldg(sa + (long long)(j + k * 8 + m1) * p.KB) : 0.f;
+        for (int k = 0; k < LOADS; ++k) v[k] = j + k * 8 < rows ? __ldg(sa + (long long)(j + k * 8) * p.KB) : 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (j + k * 8 + m1 < rows) to[j + k * 8 + m1] = v[k] * f;
+        for (int k = 0; k < LOADS; ++k)
+            if (j + k * 8 < rows) {
+                to[j + k * 8] = v[k] * f;
+                if (kSecond) to[kSecond + j + k * 8] = v[k] * f2;
+            }
     }
 }
 
