@@ -12,7 +12,7 @@ namespace {
 // half of both operands in its shared memory, and two epilogue warpgroups bring
 // the accumulator of the k block before into registers meanwhile. An expert's rows
 // are cut into chunks of 256 and one of what is left:
-// - 256 rows of a are the M side: a thread of the epilogue has a row of a and 128
+// - 256 rows of a, or nearly, are the M side: a thread of the epilogue has a row of a and 128
 //   columns in one block of w's scales, so one factor per k block.
 // - Fewer are the N side, which comes in steps of 32, and w is M: 140 rows take
 //   160 / 256 of the products' time. Each column has a scale of its own then, so the
@@ -24,7 +24,7 @@ namespace {
 //
 // A k block of a whole chunk takes about 970 cycles (512 of products; the round trip
 // of accumulators and their promotion), of one of 64 rows 640. 16384 rows unevenly on
-// 32 experts: 299 to 313 us, 1.76 to 1.84 PFLOP/s, SM clock 1950 to 2040 MHz at the power
+// 32 experts: 296 to 310 us, 1.77 to 1.86 PFLOP/s, SM clock 1950 to 2040 MHz at the power
 // limit.
 //
 //   warps 0-7    epilogue; 216 registers each, which warps 8-11 give up
@@ -35,6 +35,7 @@ constexpr int kThreads = 384;
 constexpr int kRegisters = 256 * 216 + 128 * 72;  // what setmaxnreg hands out
 constexpr int kBM = 128, kBN = 256;               // rows of w per CTA, rows of a per pair
 constexpr int kStep = 32;                         // of the columns of a chunk that is not whole
+constexpr int kWhole = 192;
 constexpr int kStages = 5;
 constexpr int kStage = (kBM + kBN / 2) * 128;     // per CTA
 constexpr int kTileSets = 2;                       // of scales under way
@@ -48,6 +49,11 @@ using TileGroups = Groups<kBN, kBN>;
 constexpr int smem_bytes(long long E) { return 1024 + kGroupOff + TileGroups::bytes(E); }
 static_assert(smem_bytes(kMaxExperts) <= 227 * 1024, "shared memory");
 static_assert(kGroupOff % 8 == 0, "tile numbers are 8 bytes");
+
+// Whether a chunk's rows are the M side: a whole one's, or nearly (215 rows take 1080
+// cycles per k block as N, 970 as M). 16384 rows unevenly on 32 experts: 296 us with the
+// border at 192, 297 at 160, 301 at 128, 300 with 256 rows alone.
+__device__ __forceinline__ bool is_whole(int rows) { return rows > kWhole; }
 
 // The address of shared memory `addr` in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
@@ -214,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (long long t = first; t < tiles && ok; t += step) {
                 groups.find(t, g);
-                const int half = (g.rows + kStep - 1) / kStep * (kStep / 2);  // of the columns: each CTA holds its own
+                // of the rows of a: each CTA holds its own
+                const int half = is_whole(g.rows) ? kBM : (g.rows + kStep - 1) / kStep * (kStep / 2);
                 const int boxes = (half + 31) / 32, bytes = 2 * (kBM * 128 + boxes * 4096);  // both CTAs'
                 const int n0 = (2 * g.n_tile + rank) * kBM, m0 = g.m0 + rank * half;
                 for (int b = 0; b < p.KB; ++b, ++i) {
@@ -242,9 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (long long t = first; t < tiles && ok; t += step) {
                 groups.find(t, g);
-                const int rows = g.rows;
-                const uint32_t desc = f8_idesc(2 * kBM, (rows + kStep - 1) / kStep * kStep);
-                const uint64_t dm = rows == kBN ? da : dw, dn = rows == kBN ? dw : da;
+                const bool whole = is_whole(g.rows);
+                const uint32_t desc = f8_idesc(2 * kBM, whole ? kBN : (g.rows + kStep - 1) / kStep * kStep);
+                const uint64_t dm = whole ? da : dw, dn = whole ? dw : da;
                 for (int b = 0; b < p.KB; ++b) {
                     if (!warp_bar_wait(full(st), ph) || !warp_bar_wait(t_empty(tb), tph ^ 1)) {
                         if (lane == 0) report_error(p.err, DEVERR_TC_WAIT);
@@ -292,8 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float* to = scales + set * (kSetBlocks * kPitch);
                     const int n = min(kSetBlocks, p.KB - b);
-                    if (g.rows == kBN) {  // [half of the columns][this CTA's 128 rows]
-                        load_scales<kBN, 16, kBM>(to, p, halves[0], halves[1], g.m0 + rank * kBM, kBM, b, n, tid);
+                    if (is_whole(g.rows)) {  // [half of the columns][this CTA's rows]
+                        load_scales<kBN, 16, kBM>(to, p, halves[0], halves[1], g.m0 + rank * kBM,
+                                                  min(kBM, g.rows - rank * kBM), b, n, tid);
                     } else {
                         load_scales<kBN, 16>(to, p, own, nullptr, g.m0, g.rows, b, n, tid);
                     }
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (long long t = first; t < tiles; t += step) {
             groups.find(t, g);
-            if (g.rows == kBN) {
+            if (is_whole(g.rows)) {
                 const int half = warp / 4, row = (warp & 3) * 32 + lane;
                 const uint32_t at = lanes + half * 128;
                 float2 acc[64];
@@ -364,10 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sph ^= 1;
                     }
                 }
-                const int m = g.m0 + rank * kBM + (warp & 3) * 32;
+                const int m = g.m0 + rank * kBM + (warp & 3) * 32, mine = g.m0 + g.rows - m;  // rows from m on
                 const long long n0 = g.n_tile * (2LL * kBM) + half * 128;
                 const uint32_t stage = base + kOutOff + warp * 4096;
-                if (vec) {
+                if (vec && mine >= 32) {
                     constexpr int kPer = 128 / sizeof(TY);  // columns of a 128-byte row
 #pragma unroll
                     for (int c = 0; c < 128; c += kPer) {
@@ -395,11 +403,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                         }
                     }
-                } else {
+                } else if (lane < mine) {
                     TY* to = y + (long long)(m + lane) * p.N + n0;
+                    constexpr int kPer = 16 / sizeof(TY);
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (n0 + c < p.N) to[c] = from_f32<TY>(c & 1 ? acc[c / 2].y : acc[c / 2].x);
+                    for (int c = 0; c < 128; c += kPer) {
+                        const float2* v = acc + c / 2;
+                        if (vec) {
+                            uint4 o;
+                            if constexpr (sizeof(TY) == 4)
+                                o = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                                               __float_as_uint(v[1].y));
+                            else
+                                o = make_uint4(pack2<TY>(v[0].x, v[0].y), pack2<TY>(v[1].x, v[1].y),
+                                               pack2<TY>(v[2].x, v[2].y), pack2<TY>(v[3].x, v[3].y));
+                            if (n0 + c < p.N) *reinterpret_cast<uint4*>(to + c) = o;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kPer; ++i)
+                                if (n0 + c + i < p.N) to[c + i] = from_f32<TY>(i & 1 ? v[i / 2].y : v[i / 2].x);
+                        }
+                    }
                 }
                 continue;
             }
