@@ -27,15 +27,15 @@ __global__ void __launch_bounds__(kGThreads)
     extern __shared__ long long list[];
     __shared__ float as[kGChunk][kGTile + 4];
     __shared__ float ws[kGChunk][kGTile + 4];
-    GGroups groups(list, (int)a.E);
     const int M = (int)a.M, N = (int)a.N, K = (int)a.K, nt = (N - 1) / kGTile + 1;
+    GGroups groups(list, (int)a.E);
     if (threadIdx.x < 32) groups.build(a.offsets, M, nt, err);
     __syncthreads();
     TY* y = static_cast<TY*>(a.y);
     GGroups::Tile g{};
     const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
     for (long long t = blockIdx.x; t < groups.first[a.E]; t += gridDim.x) {
-        groups.find(t, g);
+        groups.find(t, nt, g);
         const long long m0 = g.m0, n0 = (long long)g.n_tile * kGTile, end = g.m0 + g.rows;
         const uint8_t* w = a.w + (long long)g.e * N * K;
         const float* sw = a.sw + ((long long)g.e * ((N - 1) / 128 + 1) + n0 / 128) * KB;

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             b1 = (int)((long long)p.KB * (rank + 1) / split);
         }
         if (t >= tiles) return false;
-        groups.find(t, g);
+        groups.find(t, (p.N + 127) / 128, g);
         return true;
     };
 

@@ -24,7 +24,7 @@ namespace {
 //
 // A k block of a whole chunk takes about 970 cycles (512 of products; the round trip
 // of accumulators and their promotion), of one of 64 rows 640. 16384 rows unevenly on
-// 32 experts: 296 to 310 us, 1.77 to 1.86 PFLOP/s, SM clock 1950 to 2040 MHz at the power
+// 32 experts: 290 to 303 us, 1.81 to 1.90 PFLOP/s, SM clock 1950 to 2040 MHz at the power
 // limit.
 //
 //   warps 0-7    epilogue; 216 registers each, which warps 8-11 give up
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i = 0;
             bool ok = true;
             for (long long t = first; t < tiles && ok; t += step) {
-                groups.find(t, g);
+                groups.find(t, (p.N + 2 * kBM - 1) / (2 * kBM), g);
                 // of the rows of a: each CTA holds its own
                 const int half = is_whole(g.rows) ? kBM : (g.rows + kStep - 1) / kStep * (kStep / 2);
                 const int boxes = (half + 31) / 32, bytes = 2 * (kBM * 128 + boxes * 4096);  // both CTAs'
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t ph = 0, tph = 0;
             bool ok = true;
             for (long long t = first; t < tiles && ok; t += step) {
-                groups.find(t, g);
+                groups.find(t, (p.N + 2 * kBM - 1) / (2 * kBM), g);
                 const bool whole = is_whole(g.rows);
                 const uint32_t desc = f8_idesc(2 * kBM, whole ? kBN : (g.rows + kStep - 1) / kStep * kStep);
                 const uint64_t dm = whole ? da : dw, dn = whole ? dw : da;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t ph = 0;
             bool ok = true;
             for (long long t = first; t < tiles && ok; t += step) {
-                groups.find(t, g);
+                groups.find(t, (p.N + 2 * kBM - 1) / (2 * kBM), g);
                 // rows of w that are not there: any scales that are
                 const float* sw = p.sw + (long long)g.e * nt128 * p.KB;
                 const float* own = sw + (long long)min(2 * g.n_tile + rank, nt128 - 1) * p.KB;
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) arrive_cluster(empty0 + 8u * buf);
         };
         for (long long t = first; t < tiles; t += step) {
-            groups.find(t, g);
+            groups.find(t, (p.N + 2 * kBM - 1) / (2 * kBM), g);
             if (is_whole(g.rows)) {
                 const int half = warp / 4, row = (warp & 3) * 32 + lane;
                 const uint32_t at = lanes + half * 128;
