@@ -352,3 +352,31 @@ print("done")
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.split() == ["done"], (r.returncode, r.stdout, r.stderr[-2000:])
+
+
+@pytest.mark.parametrize("M,K", [(200001, 3), (70000, 8), (3, 300000), (1, 1000003)])
+def test_tall_and_wide(M, K):
+    x = torch.randn(M, K, generator=rng(70), device="cuda").bfloat16()
+    w = torch.rand(K, generator=rng(71), device="cuda") + 0.5
+    y, r = qg.rms_norm(x, w, x, out_dtype=torch.float32)
+    norms.check(y, norms.ref(x, w, x, 1e-6, 0.0), K)
+    assert torch.equal(r, x + x)
+    coded_is(*qg.rms_norm_fp8_b128(x, w, x)[:2], y)
+    y = qg.silu_mul(x, x, out_dtype=torch.float32)
+    gates.check(y, x, x)
+    coded_is(*qg.silu_mul_fp8_b128(x, x), y)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(100003, 1, 1, 8), (2, 65535, 3, 8), (3, 1, 300, 48)])
+def test_many_tokens_and_many_heads(T, Hq, Hkv, D):
+    rope.Case(72, T, Hq, Hkv, D, 64, "bf16", "bf16").check()
+    rope.Case(73, T, Hq, Hkv, D, 64, "f32", "f16", rot=D // 2).check(True)
+
+
+@pytest.mark.parametrize("counts,N,K", [([40] * 1000 + [0] * 24, 1, 16), ([129] * 300, 257, 144), ([1] * 700, 3, 100), ([100003], 8, 16)])
+def test_many_rows_and_narrow_weights(counts, N, K):
+    c = Experts(74, counts, N, K, 1, 1)
+    y = c.full("f32")
+    c.run(y=y)
+    c.check(y, list(range(0, len(counts), 37)))
+    assert (y[0] == 7).all() and (y[-1] == 7).all() and qg.device_error() == 0
