@@ -41,88 +41,71 @@ __device__ __forceinline__ float2 cos_sin(uint64_t fraction) {
     return make_float2(c, s);
 }
 
-constexpr int kThreads = 256;
-constexpr int kAngles = 256;  // angles of a block's tokens, if it has several
-constexpr int kTokens = 2;    // tokens of a block at most (36.8 us; one 50.7, up to eight 37.4)
+constexpr int kThreads = 128;
 
-// A block takes `per` tokens: their angles into shared memory (one for all heads),
-// then the heads of q, k and v of all its tokens one after the other, a head by the
-// threads of one threadIdx.y. Bound by the bytes of q, k and v, once each, next to
-// instruction issue; a thread has the loads of kBatch heads under way, the first
-// ones while the angles are worked out.
+// A block takes a token: its angles into shared memory (one for all heads), then the
+// heads of q, k and v one after the other, a head by the threads of one threadIdx.y.
+// Bound by the bytes of q, k and v, once each, next to instruction issue; a thread has
+// the loads of kBatch heads under way, the first ones while the angles are worked out.
 //
 // PAIRED: 16 values of a head per thread, both members of eight pairs (or two runs
 // of eight that are not turned), so a pair's angle is read and its place worked out
-// once: 8192 tokens, 32 and 8 heads of 128, bf16: 36.8 us, 5.5 TB/s; 57 us with eight
-// values per thread, whose partners were loaded a second time. It needs D a multiple of 16 and
+// once: 8192 tokens, 32 and 8 heads of 128, bf16: 34.1 us, 5.9 TB/s; 57 with eight values
+// per thread, whose partners were loaded a second time. It needs D a multiple of 16 and
 // pairs that lie apart by a multiple of eight; other heads are turned value by value.
 //
-// Angle i of a token lies at chunk (i % 8) / 2, place i / 8: threads beside each
-// other, whose values are beside each other, read 16-byte words beside each other.
+// Angle i lies at chunk (i % 8) / 2, place i / 8: threads beside each other, whose values
+// are beside each other, read 16-byte words beside each other.
 template <class TX, class TC, bool VEC, bool INTER, bool PAIRED>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a, const int per, unsigned* err) {
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeArgs a, unsigned* err) {
     constexpr int kRuns = PAIRED ? 2 : 1;  // of eight values per thread and head
-    constexpr int kBatch = 2;
-    extern __shared__ __align__(16) float2 angles[];  // [per][4][places][2]
+    constexpr int kBatch = sizeof(TX) == 4 ? 2 : 3;
+    extern __shared__ __align__(16) float2 angles[];  // [4][places][2]
     const int n = a.rot / 2, places = (n + 7) / 8;
-    const long long t0 = (long long)blockIdx.x * per;
-    const int tokens = (int)min((long long)per, a.tokens - t0);
+    const long long t = blockIdx.x;
     const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
     const int D = a.d, heads = a.hq + 2 * a.hkv, x = threadIdx.x;
-    const int log_page = 31 - __clz(a.page_size);
     // Where this thread's runs begin: threads below n / 8 have the pairs that lie apart.
     const bool apart = PAIRED && !INTER && x < n / 8;
     const int d0 = !PAIRED || apart ? x * 8 : x * 16, d1 = apart ? d0 + n : d0 + 8;
 
-    struct Head {
-        const TX* src;
-        int t, h;  // h: over the heads of q, k and v; t = tokens: none
-    };
-    int t = 0, h = threadIdx.y;  // of the next head
-    auto next = [&] {
-        while (h >= heads && t < tokens) {
-            h -= heads;
-            ++t;
-        }
-        Head r{nullptr, t, h};
+    // Head h of those of q, k and v.
+    auto source = [&](int h) {
         const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
         const int skip = is_q ? 0 : is_k ? a.hq : a.hq + a.hkv;
-        r.src = static_cast<const TX*>(is_q ? a.q : is_k ? a.k : a.v) +
-                (t0 + t) * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) + (h - skip) * D;
-        h += blockDim.y;
-        return r;
+        return static_cast<const TX*>(is_q ? a.q : is_k ? a.k : a.v) +
+               t * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) + (h - skip) * D;
     };
-    Head head[kBatch];
     Raw8<TX> raw[kBatch][kRuns];
-    auto load = [&] {
+    auto load = [&](int h0) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            head[i] = next();
-            if (head[i].t >= tokens) continue;
-            raw[i][0] = load8<TX, VEC>(head[i].src + d0, 8);
-            if constexpr (PAIRED) raw[i][1] = load8<TX, VEC>(head[i].src + d1, 8);
+            const int h = h0 + i * blockDim.y;
+            if (h >= heads) continue;
+            const TX* src = source(h);
+            raw[i][0] = load8<TX, VEC>(src + d0, 8);
+            if constexpr (PAIRED) raw[i][1] = load8<TX, VEC>(src + d1, 8);
         }
     };
     // (cos, sin) of pairs p and p + 1, p even
-    auto two_angles = [&](int t, int p) {
-        return reinterpret_cast<const float4*>(angles)[(t * 4 + p % 8 / 2) * places + p / 8];
-    };
+    auto two_angles = [&](int p) { return reinterpret_cast<const float4*>(angles)[p % 8 / 2 * places + p / 8]; };
 
     fp8::pdl_wait();
     fp8::pdl_trigger();
-    load();
-    for (int i = tid; i < tokens * n; i += threads) {
-        const int t = i / n, j = i - t * n;
-        angles[((t * 4 + j % 8 / 2) * places + j / 8) * 2 + j % 2] =
-            cos_sin(turn_fraction(a.inv_freq[j]) * (uint64_t)a.positions[t0 + t]);
-    }
+    load(threadIdx.y);
+    const int64_t slot = a.slots[t], page = slot >> (31 - __clz(a.page_size));
+    const bool none = slot < 0 || page >= a.num_pages;
+    const long long place = (page * a.hkv * a.page_size + (slot & (a.page_size - 1))) * D;  // of head 0
+    for (int j = tid; j < n; j += threads)
+        angles[(j % 8 / 2 * places + j / 8) * 2 + j % 2] = cos_sin(turn_fraction(a.inv_freq[j]) * (uint64_t)a.positions[t]);
+    if (tid == 0 && page >= a.num_pages) report_error(err, DEVERR_INDEX);
     __syncthreads();
 
-    for (; head[0].t < tokens; load()) {
+    for (int h0 = threadIdx.y; h0 < heads; h0 += kBatch * blockDim.y, load(h0)) {
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int t = head[b].t, h = head[b].h;
-            if (t >= tokens) break;
+            const int h = h0 + b * blockDim.y;
+            if (h >= heads) break;
             float y[kRuns][8];
 #pragma unroll
             for (int r = 0; r < kRuns; ++r) to_f32(raw[b][r], y[r]);
@@ -134,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a, con
                     for (int i = 0; i < 8; i += 4) {
                         const int p = (d0 + r * 8 + i) / 2;
                         if (p >= n) continue;
-                        const float4 v = two_angles(t, p);
+                        const float4 v = two_angles(p);
                         const float* f = &y[r][i];
                         const float o[4] = {fmaf(f[1], -v.y, f[0] * v.x), fmaf(f[0], v.y, f[1] * v.x),
                                             fmaf(f[3], -v.w, f[2] * v.z), fmaf(f[2], v.w, f[3] * v.z)};
@@ -149,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a, con
                 if (apart) {
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
-                        const float4 v = two_angles(t, d0 + i);
+                        const float4 v = two_angles(d0 + i);
                         const float2 c = make_float2(v.x, v.z), s = make_float2(v.y, v.w);
                         const float2 p = make_float2(y[0][i], y[0][i + 1]), q = make_float2(y[1][i], y[1][i + 1]);
                         const float2 u = __ffma2_rn(make_float2(-q.x, -q.y), s, __fmul2_rn(p, c));
@@ -161,32 +144,27 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a, con
                     }
                 }
             } else {
+                const TX* src = source(h);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int d = d0 + i;
                     if (d < a.rot) {
                         const bool second = d >= n;
                         const int p = second ? d - n : d;
-                        const float2 cs = angles[((t * 4 + p % 8 / 2) * places + p / 8) * 2 + p % 2];
-                        const float o = to_f32(head[b].src[second ? p : d + n]);
+                        const float2 cs = angles[(p % 8 / 2 * places + p / 8) * 2 + p % 2];
+                        const float o = to_f32(src[second ? p : d + n]);
                         y[0][i] = fmaf(o, second ? cs.y : -cs.y, y[0][i] * cs.x);
                     }
                 }
             }
             TC* dst;
             if (h < a.hq) {
-                dst = static_cast<TC*>(a.q_out) + ((t0 + t) * a.hq + h) * D;
+                dst = static_cast<TC*>(a.q_out) + (t * a.hq + h) * D;
             } else {
-                const int64_t slot = a.slots[t0 + t], page = slot >> log_page;
-                if (slot < 0) continue;
-                if (page >= a.num_pages) {
-                    report_error(err, DEVERR_INDEX);
-                    continue;
-                }
+                if (none) continue;
                 const bool is_k = h < a.hq + a.hkv;
-                const int at = h - a.hq - (is_k ? 0 : a.hkv);
-                dst = static_cast<TC*>(is_k ? a.k_cache : a.v_cache) +
-                      ((page * a.hkv + at) * a.page_size + (slot & (a.page_size - 1))) * D;
+                const long long at = h - a.hq - (is_k ? 0 : a.hkv);
+                dst = static_cast<TC*>(is_k ? a.k_cache : a.v_cache) + place + at * a.page_size * D;
             }
             store8<TC, true>(dst + d0, y[0], 8);
             if constexpr (PAIRED) store8<TC, true>(dst + d1, y[1], 8);
@@ -200,12 +178,7 @@ int kv_append_rope_launch(const DevCtx& dc, const RopeArgs& a, cudaStream_t s) {
     const int n = a.rot / 2;
     const bool paired = a.d % 16 == 0 && (a.interleaved || n % 8 == 0);
     const int cols = a.d / (paired ? 16 : 8), rows = std::max(1, kThreads / cols);
-    // Enough tokens for an angle per thread, but first a block for every SM.
-    const long long per = std::max<long long>(
-        1, std::min<long long>(std::min(kAngles / n, kTokens), (a.tokens + dc.num_sms - 1) / dc.num_sms));
-    const long long grid = (a.tokens + per - 1) / per;
-    if (grid > 0x7FFFFFFFLL) return QG_ERR_UNSUPPORTED;
-    const size_t smem = (size_t)per * ((n + 7) / 8) * 64;
+    const size_t smem = (size_t)((n + 7) / 8) * 64;
     return by_type(a.x_dtype, [&](auto tx) {
         using TX = decltype(tx);
         const int es = sizeof(TX);
@@ -222,7 +195,7 @@ int kv_append_rope_launch(const DevCtx& dc, const RopeArgs& a, cudaStream_t s) {
                 using No = std::false_type;
                 auto kern = a.interleaved ? (paired ? pick(Yes{}, Yes{}) : pick(Yes{}, No{}))
                                           : (paired ? pick(No{}, Yes{}) : pick(No{}, No{}));
-                return launch_after(kern, dim3((unsigned)grid), dim3(cols, rows), smem, s, a, (int)per, dc.err);
+                return launch_after(kern, dim3((unsigned)a.tokens), dim3(cols, rows), smem, s, a, dc.err);
             } else {
                 return (int)QG_ERR_INVALID_ARG;
             }
