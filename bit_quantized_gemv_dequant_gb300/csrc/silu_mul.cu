@@ -25,13 +25,21 @@ __device__ __forceinline__ float reciprocal_approx(float x) {
     return y;
 }
 
+__device__ __forceinline__ float least_of(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f;  // log2 e = their sum
+
 // y = u g / (1 + e^-g) for two values at a time (SIGN = -1: -y). e^-g = 2^t (1 + s
 // ln2), where t + s = -g log2 e: t is rounded, and its remainder s, which grows with
-// g, is not lost. From g = -88 on the result is 0; of -infinity it is NaN, as the
-// quotient is. An infinite g has no remainder: the minimum drops the NaN.
+// g, is not lost. From g = -87.3 on the quotient is below the normal numbers and becomes
+// 0 (see gated_far); of -infinity it is NaN. An infinite g has no remainder: the minimum
+// drops the NaN.
 template <int SIGN>
 __device__ __forceinline__ float2 gated(float2 g, float2 u) {
-    constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f;  // log2 e = their sum
     constexpr float kLn2 = SIGN * 0x1.62e43p-1f, kOne = SIGN;
     const float2 minus = make_float2(-kLog2e, -kLog2e), one = make_float2(kOne, kOne), t = __fmul2_rn(g, minus);
     float2 s = __ffma2_rn(g, minus, make_float2(-t.x, -t.y));
@@ -43,11 +51,46 @@ __device__ __forceinline__ float2 gated(float2 g, float2 u) {
     return __fmul2_rn(__fmul2_rn(g, make_float2(reciprocal_approx(d.x), reciprocal_approx(d.y))), u);
 }
 
+// y for kFarthest < g < kFar, where 1 + e^-g is e^-g: u g e^g, half of whose exponent
+// comes before u and half after it, since u may be as large as e^g is small. e^g = 2^-4k
+// 2^-r (1 - s ln2), where 4k + r + s = -g log2 e. Below kFarthest nothing is left of the
+// largest u.
+constexpr float kFar = -87.f, kFarthest = -340.f;
+template <int SIGN>
+__device__ __forceinline__ float gated_far(float g, float u) {
+    const float t = g * -kLog2e, k = rintf(t * 0.25f);
+    const float s = fmaf(g, -kRest, fmaf(g, -kLog2e, -t));
+    float e = exp2_approx(fmaf(k, 4.f, -t));
+    e = fmaf(e, s * -0x1.62e43p-1f, e);
+    const float q = __int_as_float((127 - (int)k) << 23);
+    return g * (SIGN * e) * q * q * u * q * q;
+}
+
+// The values of a thread of gate_kernel whose gates are that small, read again one by one:
+// what the rare path needs it works out anew, and takes few registers from the other one.
+template <class T, int SIGN, int RUN, int STEP>
+__device__ __noinline__ void again(float* y, const GateArgs& a, long long unit, int lane, int apart) {
+    const long long KB = (a.K + kFp8Block - 1) / kFp8Block, m = unit / KB;
+    const int k = (int)(unit - m * KB) * kFp8Block + lane * apart, left = m < a.M ? (int)a.K - k : 0;
+    const T* gate = static_cast<const T*>(a.gate) + m * a.gate_stride + k;
+    const T* up = static_cast<const T*>(a.up) + m * a.up_stride + k;
+#pragma unroll 1
+    for (int i = 0; i < kPer; ++i) {
+        const int at = i / 8 * RUN + i % 8 * STEP;
+        if (at >= left) continue;
+        const float g = to_f32(gate[at]);
+        if (g < kFar && g > kFarthest) y[i] = gated_far<SIGN>(g, to_f32(up[at]));
+    }
+}
+
 // Sixteen values per thread, eight threads per scale. Bound by the bytes of g, u and
-// y next to instruction issue (72 % of all slots): 4096 x 12288 bf16 to codes 42.5 us,
-// 6.0 TB/s; with a library's exponential and division and eight values per thread 58.7.
+// y next to instruction issue (72 % of all slots): 4096 x 12288 bf16 to codes 44.3 us,
+// 5.7 TB/s, 1.3 of which are the look for gates below kFar (46.2 without a limit on
+// registers, whose blocks are fewer); with a library's exponential and division and eight
+// values per thread 58.7.
 template <class T, bool FP8, bool VEC>
-__global__ void __launch_bounds__(kThreads) gate_kernel(const GateArgs a, const int K, const int KB) {
+__global__ void __launch_bounds__(kThreads, VEC ? 16 : 8)
+    gate_kernel(const __grid_constant__ GateArgs a, const int K, const int KB) {
     constexpr int kSign = FP8 ? -1 : 1;
     const int lane = threadIdx.x % kLanes;
     const long long units = (long long)a.M * KB, unit = (long long)blockIdx.x * kUnits + threadIdx.x / kLanes;
@@ -55,8 +98,8 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(const GateArgs a, const 
     const long long m = units <= 0xFFFF0000ll ? (uint32_t)unit / (uint32_t)KB : unit / KB;
     // A thread has two runs of eight values: beside each other, or of f32 (whose runs are
     // two loads each) one in each half of the block: 4096 x 8192 f32 57.9 us, and 71 beside
-    // each other; bf16 29.7 beside each other, 30.7 apart. Values of rows that do not lie
-    // in eights are eight apart, so that threads read places beside each other.
+    // each other; bf16 30.8 beside each other, 1.0 more apart. Values of rows that do not
+    // lie in eights are eight apart, so that threads read places beside each other.
     constexpr int kStep = VEC ? 1 : kLanes, kRun = VEC && sizeof(T) == 2 ? 8 : kFp8Block / 2;
     const int k = (int)(unit - m * KB) * kFp8Block + lane * (!VEC ? 1 : kRun == 8 ? 16 : 8), left = unit < units ? K - k : 0;
     const T* gate = static_cast<const T*>(a.gate) + m * a.gate_stride + k;
@@ -70,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(const GateArgs a, const 
         gr[h] = load8<T, VEC, kStep>(gate + kRun * h, left - kRun * h);
         ur[h] = load8<T, VEC, kStep>(up + kRun * h, left - kRun * h);
     }
-    float y[2][8];
+    float y[2][8], least = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float g[8];
@@ -78,10 +121,19 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(const GateArgs a, const 
         to_f32(ur[h], y[h]);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
+            least = least_of(least, g[i], g[i + 1]);
             const float2 v = gated<kSign>(make_float2(g[i], g[i + 1]), make_float2(y[h][i], y[h][i + 1]));
             y[h][i] = v.x;
             y[h][i + 1] = v.y;
         }
+    }
+    if (least < kFar) {
+        float z[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) z[i] = y[i / 8][i % 8];
+        again<T, kSign, kRun, kStep>(z, a, unit, lane, !VEC ? 1 : kRun == 8 ? 16 : 8);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) y[i / 8][i % 8] = z[i];
     }
     if constexpr (FP8) {
         float most = 0.f;

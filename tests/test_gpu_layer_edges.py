@@ -1,0 +1,58 @@
+"""The operators between a layer's products where their values or operands lie at an edge: gates whose quotient alone is
+below f32."""
+import pytest
+import torch
+
+import bit_quantized_gemv_dequant_gb300 as qg
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+HALF = {torch.float32: 0.0, torch.float16: 2.0**-11, torch.bfloat16: 2.0**-8}
+TINY = {torch.float32: 2.0**-149, torch.float16: 2.0**-25, torch.bfloat16: 2.0**-134}
+
+
+def gate_bound(want, out):
+    """5 units of 2^-23, as for every gate, and half a step of the output's type; what is below 2^-119 may be 0."""
+    lost = torch.where(want.abs() < 2.0**-119, want.abs(), torch.zeros_like(want))
+    return want.abs() * (5 * 2.0**-23 + HALF[out]) + lost + TINY[out]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [4096, 4099])
+def test_small_gates_of_large_values(x, out, K):
+    """Gates from -300 to -60, times values of every size up to f32's largest: the product is an ordinary number where the
+    gate alone is not."""
+    g = torch.linspace(-300, -60, K, device="cuda").to(DTYPES[x])
+    exponents = [-100, -30, 0, 20, 60, 100, 120, 127]
+    gate = g.repeat(2 * len(exponents), 1)
+    up = torch.rand(gate.shape, generator=torch.Generator("cuda").manual_seed(K), device="cuda") * 0.99 + 1
+    up *= torch.exp2(torch.tensor(exponents * 2, device="cuda").float())[:, None]
+    up[len(exponents):] *= -1
+    up = up.to(DTYPES[x])
+    y = qg.silu_mul(gate, up, out_dtype=DTYPES[out])
+    a, b = gate.double(), up.double()
+    want = b * a / (1 + torch.exp(-a))
+    assert (want.abs() > 2.0**-100).sum() > 10000
+    bad = (y.double() - want).abs() > gate_bound(want, y.dtype)
+    assert not bad.any(), (int(bad.sum()), [(float(gate[tuple(i)]), float(up[tuple(i)]), float(y[tuple(i)])) for i in bad.nonzero()[:3]])
+    codes, scales = qg.silu_mul_fp8_b128(gate, up)
+    same = qg.quantize_fp8_b128(qg.silu_mul(gate, up, out_dtype=torch.float32))
+    assert torch.equal(codes.view(torch.uint8), same[0].view(torch.uint8)) and torch.equal(scales, same[1])
+
+
+def test_small_gates_among_others():
+    """A row's result is the same whether or not its neighbours have small gates."""
+    g = torch.Generator("cuda").manual_seed(1)
+    gate = torch.randn(64, 1024, generator=g, device="cuda") * 4
+    up = torch.randn(64, 1024, generator=g, device="cuda")
+    y = qg.silu_mul(gate, up)
+    at = torch.rand(64, 1024, generator=g, device="cuda") < 0.05
+    z = qg.silu_mul(torch.where(at, torch.full_like(gate, -90.0), gate), torch.where(at, torch.full_like(up, 1e38), up))
+    assert torch.equal(z[~at], y[~at])
+    want = 1e38 * -90.0 * float(torch.exp(torch.tensor(-90.0, dtype=torch.float64)))
+    assert (z[at].double() / want - 1).abs().max() < 5 * 2.0**-23 + 2.0**-24  # (1e38 is rounded)
+    odd = torch.tensor([[float("-inf"), -100.0, -100.0, float("nan"), -3e38, -2000.0, -90.0]], device="cuda")
+    y = qg.silu_mul(odd, torch.tensor([[1.0, float("inf"), float("nan"), 1.0, 3e38, 3e38, 0.0]], device="cuda"))[0]
+    assert torch.isnan(y[[0, 2, 3]]).all() and y[1] == float("-inf") and (y[4:] == 0).all()
