@@ -33,11 +33,11 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
     return bits >> 31 ? 0 - r : r;
 }
 
-// Cosine and sine of a fraction of a turn (2^-64 each). The nearest of +-1/2 turn
-// as f32: 2^-24 of the angle, and 2^-33 of a turn where it is small.
+// Cosine and sine of a fraction of a turn (2^-64 each), as the f32 nearest to its number of
+// half turns between -1 and 1: 2^-24 of the angle, however small it is.
 __device__ __forceinline__ float2 cos_sin(uint64_t fraction) {
     float s, c;
-    sincospif((float)(int32_t)(fraction >> 32) * 0x1p-31f, &s, &c);
+    sincospif(__ll2float_rn((int64_t)fraction) * 0x1p-63f, &s, &c);
     return make_float2(c, s);
 }
 

@@ -1,5 +1,5 @@
 """The operators between a layer's products where their values or operands lie at an edge: gates whose quotient alone is
-below f32."""
+below f32, angles far below a step of the usual ones."""
 import pytest
 import torch
 
@@ -56,3 +56,28 @@ def test_small_gates_among_others():
     odd = torch.tensor([[float("-inf"), -100.0, -100.0, float("nan"), -3e38, -2000.0, -90.0]], device="cuda")
     y = qg.silu_mul(odd, torch.tensor([[1.0, float("inf"), float("nan"), 1.0, 3e38, 3e38, 0.0]], device="cuda"))[0]
     assert torch.isnan(y[[0, 2, 3]]).all() and y[1] == float("-inf") and (y[4:] == 0).all()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D", [64, 40])
+def test_small_angles(D, inter):
+    """Pairs (a, 0) at angles down to 2^-29, of both signs: the second value is a times the sine, whose relative error is that
+    of the angle in f32 (2^-24), of the sine (2 units of 2^-23) and of the product (2^-24), 6 x 2^-24, next to the angle's 2^-64
+    of a turn per position and half a step of the output."""
+    n = D // 2
+    freq = torch.exp2(-torch.linspace(4, 29, n, device="cuda")).contiguous()
+    positions = torch.tensor([1, -1, 3, -3, 1000, -1000, 0], device="cuda")
+    T = positions.numel()
+    q = torch.zeros(T, 2, D, device="cuda")
+    first, second = (slice(0, D, 2), slice(1, D, 2)) if inter else (slice(0, n), slice(n, D))
+    angle = positions.double()[:, None] * freq.double()
+    a = torch.exp2(-torch.floor(torch.log2(angle.abs() + 2.0**-40)))  # a power of two: the result is about 1
+    q[:, :, first] = a.float()[:, None]
+    kc, vc = (torch.zeros(2, 2, 8, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    out = qg.kv_append_rope(q, q, q, positions, freq, kc, vc, torch.arange(T, device="cuda"), interleaved=inter)
+    sine = angle.sin() * a
+    bound = sine.abs() * (6 * 2.0**-24 + HALF[torch.float16]) + a * positions.abs()[:, None] * 2.0**-61
+    for heads in (out, kc[0, :, :T].transpose(0, 1)):
+        bad = (heads[:, :, second].double() - sine[:, None]).abs() > bound[:, None]
+        assert not bad.any(), (int(bad.sum()), bad.nonzero()[:3].tolist())
+    assert qg.device_error() == 0
