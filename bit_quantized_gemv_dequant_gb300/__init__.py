@@ -408,7 +408,9 @@ def qmm_fp8_b128_grouped(a, a_scales, w, w_scales, offsets, y=None, *, out_dtype
     """qmm_fp8_b128 for a layer of experts: rows offsets[e] .. offsets[e + 1] - 1
     of a [M, K] times w[e] of w [experts, N, K] (scales [experts, ceil(N / 128),
     ceil(K / 128)]); offsets int32 [experts + 1]. Rows of y [M, N] that no expert
-    has are left as they are."""
+    has are left as they are. With K % 16 != 0, or a weight that does not begin on 16
+    bytes, the scratch that stays with the stream is as large as all weights: lay them
+    out with rows of a multiple of 16 bytes, or pass a workspace."""
     return (_SERVING or _calls()).qmm_fp8_b128_grouped(a, a_scales, w, w_scales, offsets, y, out_dtype, workspace,
                                                        stream)
 

@@ -107,7 +107,8 @@ int fp8_grouped_launch(const DevCtx& dc, const GroupedArgs& args, void* ws, size
     const long long pitch = (a.K + 15) / 16 * 16;
     auto fits = [&](const uint8_t* p) { return a.K == pitch && reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     bool tma = fits(a.a) && fits(a.w);
-    if (!tma && pitch <= 0x7FFFFFFF && ws_bytes >= (size_t)((a.M + a.E * a.N) * pitch)) {
+    const size_t need = (size_t)((fits(a.a) ? 0 : a.M) + (fits(a.w) ? 0 : a.E * a.N)) * (size_t)pitch;
+    if (!tma && pitch <= 0x7FFFFFFF && ws_bytes >= need) {
         // Zeros after the end of a row add nothing, and the blocks of 128 are the same. Of w
         // only the experts that have rows are copied.
         uint8_t* p = static_cast<uint8_t*>(ws);

@@ -332,9 +332,14 @@ PyObject* qmm_fp8_b128_grouped(PyObject* const* a) {
     if (a[5] != Py_None) shape(y, "y", {M, N});
     const int type = code(y, "y");
     const qg_stream_t s = stream_of(a[8]);
-    size_t need = 0;
-    const uintptr_t odd = (uintptr_t)K | (uintptr_t)x.data_ptr() | (uintptr_t)w.data_ptr();
-    if (odd & 15) check(qmm_fp8_b128_grouped_workspace_size(M, E, N, K, &need), "qmm_fp8_b128_grouped");
+    // scratch for what cannot be read as it is: all weights are many times the rows
+    size_t need = 0, of_w = 0;
+    const bool odd_x = ((uintptr_t)K | (uintptr_t)x.data_ptr()) & 15, odd_w = ((uintptr_t)K | (uintptr_t)w.data_ptr()) & 15;
+    if (odd_x || odd_w) {
+        check(qmm_fp8_b128_grouped_workspace_size(M, E, N, K, &need), "qmm_fp8_b128_grouped");
+        check(qmm_fp8_b128_grouped_workspace_size(0, E, N, K, &of_w), "qmm_fp8_b128_grouped");
+        need = odd_x ? (odd_w ? need : need - of_w) : of_w;
+    }
     const Scratch ws = scratch(need, a[7], x, s);
     call("qmm_fp8_b128_grouped", ws.enqueue, [&] {
         return ::qmm_fp8_b128_grouped(at_of<uint8_t>(x), at_of<float>(sx), at_of<uint8_t>(w), at_of<float>(sw),

@@ -311,7 +311,9 @@ QG_API int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* 
  * M = 0 is fine, experts <= 1024, experts * N <= 2^31 - 2^14. The kernel is
  * chosen by M / experts; any spread of the rows is right. The workspace is
  * needed for the same reason as there: calls with K % 16 == 0 and 16-byte
- * aligned a and w need none. */
+ * aligned a and w need none, and where K % 16 == 0 and one of them is not
+ * aligned, M * K bytes are enough for a, or experts * N * K for w. Only the
+ * weights of experts that have rows are copied into it. */
 QG_API int qmm_fp8_b128_grouped(const uint8_t* a, const float* a_scales, const uint8_t* w,
                                 const float* w_scales, const int32_t* offsets, void* y, int y_dtype,
                                 int64_t M, int64_t experts, int64_t N, int64_t K, void* workspace,

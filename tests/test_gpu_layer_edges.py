@@ -1,5 +1,5 @@
 """The operators between a layer's products where their values or operands lie at an edge: gates whose quotient alone is
-below f32, angles far below a step of the usual ones."""
+below f32, angles far below a step of the usual ones, operands of which one is unaligned."""
 import pytest
 import torch
 
@@ -81,3 +81,50 @@ def test_small_angles(D, inter):
         bad = (heads[:, :, second].double() - sine[:, None]).abs() > bound[:, None]
         assert not bad.any(), (int(bad.sum()), bad.nonzero()[:3].tolist())
     assert qg.device_error() == 0
+
+
+def experts(seed, rows, E, N, K):
+    g = torch.Generator("cuda").manual_seed(seed)
+
+    def codes(*shape):
+        return (torch.randn(*shape, generator=g, device="cuda") * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+
+    a, w = codes(rows, K), codes(E, N, K)
+    sa = torch.rand(rows, -(-K // 128), generator=g, device="cuda") + 0.5
+    sw = torch.rand(E, -(-N // 128), -(-K // 128), generator=g, device="cuda") + 0.5
+    offsets = torch.linspace(0, rows, E + 1, device="cuda").to(torch.int32)
+    return a, sa, w, sw, offsets
+
+
+def shifted(t, by):
+    flat = torch.empty(t.numel() + by, dtype=torch.uint8, device="cuda")[by:]
+    flat.copy_(t.view(torch.uint8).flatten())
+    return flat.view(t.dtype).view(t.shape)
+
+
+@pytest.mark.parametrize("rows", [9, 700])
+def test_scratch_is_for_what_is_unaligned(rows):
+    """One unaligned operand takes a copy of itself alone, and the products are those of aligned ones, bit by bit."""
+    E, N, K = 6, 520, 1024
+    a, sa, w, sw, offsets = experts(rows, rows, E, N, K)
+    want = qg.qmm_fp8_b128_grouped(a, sa, w, sw, offsets)
+    for x, y, need in ((shifted(a, 1), w, rows * K), (a, shifted(w, 4), E * N * K),
+                       (shifted(a, 8), shifted(w, 3), (rows + E * N) * K)):
+        guarded = torch.full((need + 64,), 0x7F, dtype=torch.uint8, device="cuda")
+        got = qg.qmm_fp8_b128_grouped(x, sa, y, sw, offsets, workspace=guarded[:need])
+        assert torch.equal(got, want) and (guarded[need:] == 0x7F).all()
+    assert qg.device_error() == 0
+
+
+def test_scratch_of_a_call_without_workspace():
+    E, N, K, rows = 16, 1024, 4096, 40
+    a, sa, w, sw, offsets = experts(1, rows, E, N, K)
+    want = qg.qmm_fp8_b128_grouped(a, sa, w, sw, offsets)
+    x, out = shifted(a, 1), torch.empty_like(want)
+    with torch.cuda.stream(torch.cuda.Stream()):  # one that has no scratch yet
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        qg.qmm_fp8_b128_grouped(x, sa, w, sw, offsets, out)
+        torch.cuda.synchronize()
+        assert torch.cuda.memory_allocated() - before <= rows * K + 1024
+    assert torch.equal(out, want)
