@@ -2,8 +2,6 @@
 // weight, e4m3 codes and scales as in qmm_fp8_b128.
 #include <cuda_fp8.h>
 
-#include <algorithm>
-
 #include "fp8_groups.cuh"
 
 namespace qg {
@@ -89,15 +87,14 @@ int general_launch(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
     return launched();
 }
 
-// Which kernel, by the rows that an expert has on average: at 32 the kernel of few rows
-// takes 93 us of 32 experts, N = K = 4096, and the other one 100; at 48 107 and 104, at
-// 64 133 and 112. Up to 64 it is also taken where it leaves fewer SMs idle, since it
-// splits K for its last tiles (9 experts of 34 rows, N = 2200, K = 5200).
-bool few_rows(const DevCtx& dc, const GroupedArgs& a) {
-    if (a.M <= 32 * a.E) return true;
-    if (a.M > 64 * a.E) return false;
-    const long long pairs = std::max(1, dc.num_sms / 2), tiles = (a.N + 255) / 256 * a.E;
-    return 5 * fp8::grouped_few_chain(dc, a) < 4 * ((tiles + pairs - 1) / pairs) * ((a.K + 127) / 128);
+// On the tensor cores: by the kernel of few rows per expert, or that of many.
+int tensor_launch(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
+    if (!fp8::may_be_few(a.M, a.E)) return fp8::launch_grouped_tile(dc, a, s);
+    fp8::FewPlan plan;
+    const int rc = fp8::plan_grouped_few(dc, a, &plan);
+    if (rc) return rc;
+    return fp8::takes_few(plan, dc.num_sms, a.M, a.E, a.N, a.K) ? fp8::launch_grouped_few(dc, a, plan, s)
+                                                                : fp8::launch_grouped_tile(dc, a, s);
 }
 
 }  // namespace
@@ -126,7 +123,7 @@ int fp8_grouped_launch(const DevCtx& dc, const GroupedArgs& args, void* ws, size
         a.K = pitch;
         tma = true;
     }
-    if (tma) return few_rows(dc, a) ? fp8::launch_grouped_few(dc, a, s) : fp8::launch_grouped_tile(dc, a, s);
+    if (tma) return tensor_launch(dc, a, s);
     return a.y_dtype == QG_F32 ? general_launch<float>(dc, a, s) : general_launch<__nv_bfloat16>(dc, a, s);
 }
 

@@ -34,7 +34,6 @@ constexpr int kBN = 64;
 constexpr int kThreads = 384, kEpi = 256;
 constexpr int kStages = 7, kStage = 16384 + kBN * 128;
 constexpr int kBufs = 8;
-constexpr int kJoin = 10;      // what joining the parts of a tile takes, in k blocks
 constexpr int kOwn = kBN / 2;  // rows of a per epilogue thread
 constexpr int kPartOff = kStages * kStage;
 constexpr int kPitch = scale_pitch(kBN);
@@ -344,12 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-struct FewPlan {
-    const int* room;
-    int split;
-    long long chain;  // k blocks one after the other
-};
-
 // How many clusters of i CTAs the GPU holds at once, asked once per kernel and
 // device.
 template <class TY>
@@ -379,36 +372,14 @@ int cluster_room(const DevCtx& dc, const int** room) {
     return error[dc.device] == cudaSuccess ? QG_OK : cuda_fail(error[dc.device]);
 }
 
-// The size of the clusters: the one with the fewest k blocks one after the other if
-// the rows are spread over as many experts as there can be.
 template <class TY>
-int plan(const DevCtx& dc, const GroupedArgs& a, FewPlan* p) {
-    const int rc = cluster_room<TY>(dc, &p->room);
-    if (rc) return rc;
-    const long long kb = (a.K + 127) / 128, tiles = (a.N + 127) / 128 * std::min(a.M, a.E);
-    p->split = 0;
-    for (int i = 1; i < 9 && (i == 1 || kb >= 2 * i); ++i) {
-        if (p->room[i] < 1) continue;
-        const long long ctas = (long long)i * p->room[i], rest = tiles % ctas;
-        const long long shares = (rest + p->room[i] - 1) / p->room[i];
-        const long long chain = tiles / ctas * kb + shares * (i == 1 ? kb : (kb + i - 1) / i + kJoin);
-        if (p->split == 0 || chain * 100 < p->chain * 96) {
-            p->chain = chain;
-            p->split = i;
-        }
-    }
-    return p->split ? QG_OK : QG_ERR_UNSUPPORTED;
-}
-
-template <class TY>
-int launch(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
-    FewPlan pl;
-    int rc = plan<TY>(dc, a, &pl);
+int launch(const DevCtx& dc, const GroupedArgs& a, int split, cudaStream_t s) {
+    const int* room;
+    int rc = cluster_room<TY>(dc, &room);
     CUtensorMap mw, ma;
     if (rc == QG_OK) rc = weight_map(&mw, a);
     if (rc == QG_OK) rc = code_map(&ma, a.a, a.M, a.K, 16);
     if (rc) return rc;
-    const int split = pl.split, *room = pl.room;
     const long long kb = (a.K + 127) / 128, most = (a.N + 127) / 128 * (std::min(a.M, a.E) + a.M / kBN);
     const GroupedParams p{a.sa, a.sw, a.offsets, a.y, (int)a.M, (int)a.E, (int)a.N, (int)kb, dc.err};
     cudaLaunchConfig_t cfg{};
@@ -430,13 +401,15 @@ int launch(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int launch_grouped_few(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
-    return a.y_dtype == QG_F32 ? launch<float>(dc, a, s) : launch<__nv_bfloat16>(dc, a, s);
+int plan_grouped_few(const DevCtx& dc, const GroupedArgs& a, FewPlan* plan) {
+    const int* room;
+    const int rc = a.y_dtype == QG_F32 ? cluster_room<float>(dc, &room) : cluster_room<__nv_bfloat16>(dc, &room);
+    if (rc == QG_OK) *plan = few_plan(room, a.M, a.E, a.N, a.K);
+    return rc;
 }
 
-long long grouped_few_chain(const DevCtx& dc, const GroupedArgs& a) {
-    FewPlan p;
-    return plan<float>(dc, a, &p) == QG_OK ? p.chain : 0x7FFFFFFFFFFFFFFFLL;
+int launch_grouped_few(const DevCtx& dc, const GroupedArgs& a, const FewPlan& plan, cudaStream_t s) {
+    return a.y_dtype == QG_F32 ? launch<float>(dc, a, plan.split, s) : launch<__nv_bfloat16>(dc, a, plan.split, s);
 }
 
 int weight_map(CUtensorMap* m, const GroupedArgs& a) {

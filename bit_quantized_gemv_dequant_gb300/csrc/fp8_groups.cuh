@@ -2,6 +2,7 @@
 // tiles, and what the two tensor-core kernels of qmm_fp8_b128_grouped share.
 #pragma once
 
+#include "fp8_group_rule.cuh"
 #include "fp8_tc.cuh"
 
 namespace qg {
@@ -152,9 +153,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 // w [E, N, K] in boxes of 128 rows of one expert x 128.
 int weight_map(CUtensorMap* m, const GroupedArgs& a);
 
-int launch_grouped_few(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s);
-// The k blocks that a CTA of launch_grouped_few takes one after the other, if no expert has more than 64 rows.
-long long grouped_few_chain(const DevCtx& dc, const GroupedArgs& a);
+int plan_grouped_few(const DevCtx& dc, const GroupedArgs& a, FewPlan* plan);
+int launch_grouped_few(const DevCtx& dc, const GroupedArgs& a, const FewPlan& plan, cudaStream_t s);
 int launch_grouped_tile(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s);
 
 }  // namespace fp8
