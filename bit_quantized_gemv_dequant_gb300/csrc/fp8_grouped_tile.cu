@@ -17,8 +17,8 @@ namespace {
 // - Fewer are the N side, which comes in steps of 32, and w is M: 140 rows take
 //   160 / 256 of the products' time. Each column has a scale of its own then, so the
 //   accumulators are read in 16 x 256-bit fragments: a thread has four rows and two
-//   of every eight columns, and needs 32 scales per k block. (With a row and all 128
-//   columns it would need 128, and shared memory is busy with the operands. 16 lanes
+//   of every eight columns, and needs up to 24 scales per k block. (With a row and up to
+//   96 columns it would need 96, and shared memory is busy with the operands. 16 lanes
 //   at a time is half of what tensor memory delivers: uniform chunks of 256 rows
 //   take 294 us like that and 243 as M, 16384 rows on 32 experts, N = K = 4096.)
 //
@@ -35,7 +35,8 @@ constexpr int kThreads = 384;
 constexpr int kRegisters = 256 * 216 + 128 * 72;  // what setmaxnreg hands out
 constexpr int kBM = 128, kBN = 256;               // rows of w per CTA, rows of a per pair
 constexpr int kStep = 32;                         // of the columns of a chunk that is not whole
-constexpr int kWhole = 192;
+constexpr int kWhole = 192;                       // the most rows of a chunk that is not whole
+constexpr int kHalf = (kWhole + kStep - 1) / kStep * (kStep / 2);  // and the columns of one epilogue warpgroup then
 constexpr int kStages = 5;
 constexpr int kStage = (kBM + kBN / 2) * 128;     // per CTA
 constexpr int kTileSets = 2;                       // of scales under way
@@ -429,9 +430,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int half = (g.rows + kStep - 1) / kStep * (kStep / 2);  // columns of a warpgroup, a multiple of 16
             const int own0 = warp / 4 * half;
-            float2 acc[64];
+            static_assert(kHalf <= 96, "three units of 32 columns");
+            float2 acc[48];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
+            for (int j = 0; j < 48; ++j) acc[j] = make_float2(0.f, 0.f);
             // 64 columns are under way at once: a load takes about 200 cycles, and a wait is for all of them.
             // (What is read past this group's columns is inside the accumulator and the set.)
             auto sum = [&](auto units) {
@@ -459,14 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (U > 2) f0.load(from + 64);
                         if constexpr (U > 2) s0.load(sp + 64);
                         if constexpr (U > 1) add_scaled(acc + 16, f1, s1);
-                        if constexpr (U > 3) f1.load(from + 96);
-                        if constexpr (U > 3) s1.load(sp + 96);
                         if constexpr (U > 2) {
                             f0.wait();
-                            if constexpr (U > 3) f1.wait();
                             release(tb);
                             add_scaled(acc + 32, f0, s0);
-                            if constexpr (U > 3) add_scaled(acc + 48, f1, s1);
                         }
                         tb ^= 1;
                         tph ^= tb == 0;
@@ -479,8 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            if (half > 96) sum(std::integral_constant<int, 4>{});
-            else if (half > 64) sum(std::integral_constant<int, 3>{});
+            if (half > 64) sum(std::integral_constant<int, 3>{});
             else if (half > 32) sum(std::integral_constant<int, 2>{});
             else sum(std::integral_constant<int, 1>{});
             const long long n0 = (2LL * g.n_tile + rank) * kBM + (warp & 3) * 32;
@@ -492,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 const uint32_t stage = base + kOutOff + warp * 4096;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 3; ++c) {
                     if (c * 32 >= mine) break;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -526,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 12; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int m = 8 * j + 2 * (lane & 3);

@@ -1,5 +1,6 @@
 """The operators between a layer's products where their values or operands lie at an edge: gates whose quotient alone is
-below f32, angles far below a step of the usual ones, operands of which one is unaligned."""
+below f32, angles far below a step of the usual ones, operands of which one is unaligned, rows around
+the border between two ways of the product."""
 import pytest
 import torch
 
@@ -128,3 +129,26 @@ def test_scratch_of_a_call_without_workspace():
         torch.cuda.synchronize()
         assert torch.cuda.memory_allocated() - before <= rows * K + 1024
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [256, 200, 131])
+def test_chunks_around_the_border(N, out):
+    """Chunks of up to 192 rows and of more take different sides of the product; whole numbers and scales of 1 make every
+    order of the sum exact (to half a step of bf16)."""
+    counts = [159, 160, 161, 191, 192, 193, 194, 223, 225, 255, 1, 257, 447, 449]
+    g = torch.Generator("cuda").manual_seed(N)
+    E, rows, K = len(counts), sum(counts), 384
+
+    def codes(*shape):
+        return torch.randint(-3, 4, shape, generator=g, device="cuda").float().to(torch.float8_e4m3fn)
+
+    a, w = codes(rows, K), codes(E, N, K)
+    sa, sw = torch.ones(rows, 3, device="cuda"), torch.ones(E, -(-N // 128), 3, device="cuda")
+    offsets = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
+    y = qg.qmm_fp8_b128_grouped(a, sa, w, sw, offsets, out_dtype=out)
+    at = offsets.tolist()
+    for e in range(E):
+        want = a[at[e]:at[e + 1]].float() @ w[e].float().T
+        assert torch.equal(y[at[e]:at[e + 1]], want.to(out)), e
+    assert qg.device_error() == 0
