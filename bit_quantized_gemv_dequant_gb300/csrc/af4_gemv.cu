@@ -339,7 +339,7 @@ size_t smem_bytes(int M, int cap, int RB) {
 template <int RB, bool PF, int TM>
 int launch(const DevCtx& dc, const Params& p, int blocks, size_t smem, cudaStream_t s) {
     auto kern = af4_gemv_kernel<RB, PF, TM>;
-    static size_t configured[64] = {0};
+    static std::atomic<size_t> configured[64];
     if (smem > 48 * 1024 && dc.device >= 0 && dc.device < 64 && configured[dc.device] < smem) {
         cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

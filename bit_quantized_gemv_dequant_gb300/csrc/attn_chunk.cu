@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <class T, int D, int MODE>
 int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     auto kern = chunk_kernel<T, D, MODE>;
     if (!configured[dc.device]) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);

@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <class T, int D, int RB, bool HALF, bool CAP>
 int launch_one(const DevCtx& dc, const Work& w, cudaStream_t s) {
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     auto kern = few_kernel<T, D, RB, HALF, CAP>;
     if (!configured[dc.device]) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);

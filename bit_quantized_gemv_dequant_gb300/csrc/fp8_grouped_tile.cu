@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <class TY>
 int launch(const DevCtx& dc, const GroupedArgs& a, cudaStream_t s) {
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     auto kern = grouped_tile_kernel<TY>;
     if (!configured[dc.device]) {
         // Were the kernel launched with fewer registers than it hands out, the

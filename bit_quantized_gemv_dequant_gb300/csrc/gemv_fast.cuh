@@ -713,7 +713,7 @@ __global__ void __launch_bounds__((W + 1) * 32, (W == 8 && MT == 1) ? 2 : 1) gem
 template <int FMT, int MT, int R, int W, int GW>
 int launch(const DevCtx& dc, const Params& kp, int grid_x, int smem, bool pdl, cudaStream_t s) {
     auto kern = gemv_fast_kernel<FMT, MT, R, W, GW>;
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     if (dc.device >= 0 && dc.device < 64 && configured[dc.device] < smem) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              dc.max_smem_optin);

@@ -721,7 +721,7 @@ template <int FMT, int MT, int LPR>
 int launch(const DevCtx& dc, const Params& kp, int grid, int warps, int smem, bool pdl,
            cudaStream_t s) {
     auto kern = gemv_stream_kernel<FMT, MT, LPR>;
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     cudaError_t e;
     if (dc.device < 0 || dc.device >= 64 || configured[dc.device] < smem) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, dc.max_smem_optin);

@@ -742,7 +742,7 @@ __global__ void QG_XREG_BOUNDS gemv_xreg_af4_kernel(const Params p,
 template <int FMT, int MT, int NWC, int RPG>
 int launch(const DevCtx& dc, const Params& kp, int grid, int smem, bool pdl, cudaStream_t s) {
     auto kern = gemv_xreg_kernel<FMT, MT, NWC, RPG>;
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     if (dc.device >= 0 && dc.device < 64 && configured[dc.device] < smem) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              dc.max_smem_optin);

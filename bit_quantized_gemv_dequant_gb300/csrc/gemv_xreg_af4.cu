@@ -20,7 +20,7 @@ template <int MT, int NWC>
 int launch_af4(const DevCtx& dc, const xreg::Params& kp, const CUtensorMap& mq,
                const CUtensorMap& mm, int grid, int smem, bool pdl, cudaStream_t s) {
     auto kern = xreg::gemv_xreg_af4_kernel<MT, NWC, xreg::kRPG>;
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     if (dc.device >= 0 && dc.device < 64 && configured[dc.device] < smem) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              dc.max_smem_optin);

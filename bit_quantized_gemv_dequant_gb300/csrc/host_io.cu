@@ -48,7 +48,7 @@ int fetch_host_launch(const DevCtx& dc, const float* src, float* dst, long long 
     // All of the SM's on-chip memory to shared memory, as the GEMV that
     // follows wants it: the GEMV's CTAs may then start beside this kernel's
     // on the same SMs instead of waiting for them to end.
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     if (dc.device >= 0 && dc.device < 64 && !configured[dc.device]) {
         const cudaError_t e = cudaFuncSetAttribute(
             fetch_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);

@@ -619,7 +619,7 @@ int logprobs_launch(const DevCtx& dc, const LogprobArgs& a, cudaStream_t s) {
         while (parts < 8 && a.M * parts * 2 <= 2 * dc.num_sms &&
                a.V >= (long long)parts * 2 * 2 * kThreads * Chunk<T>::kN)
             parts *= 2;
-        static int configured[64] = {0};
+        static std::atomic<int> configured[64];  // set by any thread, all to the same
         if (!configured[dc.device]) {
             const cudaError_t e =
                 cudaFuncSetAttribute(row_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);

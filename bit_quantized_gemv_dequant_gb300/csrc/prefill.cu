@@ -653,7 +653,7 @@ template <bool PACKED, int GK>
 int launch_main(const DevCtx& dc, const CUtensorMap& mq, const CUtensorMap& mx, const Params& kp,
                 dim3 grid, cudaStream_t s) {
     constexpr int smem = Geo<PACKED>::kSmemBytes;
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     auto kern = mma_kernel<PACKED, GK>;
     if (dc.device >= 0 && dc.device < 64 && !configured[dc.device]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

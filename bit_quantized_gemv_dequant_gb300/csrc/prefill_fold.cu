@@ -328,7 +328,7 @@ template <bool PACKED, bool GS16>
 int launch_fold(const DevCtx& dc, const CUtensorMap& mq, const CUtensorMap& mx,
                 const FoldParams& kp, dim3 grid, cudaStream_t s) {
     constexpr int smem = GeoF<PACKED>::kSmemBytes;
-    static int configured[64] = {0};
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
     auto kern = fold_kernel<PACKED, GS16>;
     if (dc.device >= 0 && dc.device < 64 && !configured[dc.device]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

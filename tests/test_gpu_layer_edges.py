@@ -1,10 +1,15 @@
 """The operators between a layer's products where their values or operands lie at an edge: gates whose quotient alone is
 below f32, angles far below a step of the usual ones, operands of which one is unaligned, rows around
-the border between two ways of the product."""
+the border between two ways of the product, first calls of several threads."""
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
 import bit_quantized_gemv_dequant_gb300 as qg
+from test_gpu_serving_calls import ROOT
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +157,47 @@ def test_chunks_around_the_border(N, out):
         want = a[at[e]:at[e + 1]].float() @ w[e].float().T
         assert torch.equal(y[at[e]:at[e + 1]], want.to(out)), e
     assert qg.device_error() == 0
+
+
+def first_calls():
+    """Each thread's first calls are the process's first ones too, of kernels whose shared memory is set at the first call.
+    Later calls give the same."""
+    g = torch.Generator("cuda").manual_seed(7)
+    few, many = experts(8, 12, 4, 256, 512), experts(9, 700, 3, 256, 512)
+    logits = torch.randn(2, 4000, generator=g, device="cuda")
+    codes = torch.randint(0, 16, (256, 4096), generator=g, device="cuda", dtype=torch.uint8)
+    s, b = (torch.rand(256, 64, generator=g, device="cuda").bfloat16() for _ in range(2))
+    plane, meta = qg.prepare_af4_g64(codes, s, b)
+    xs = [torch.randn(m, 4096, generator=g, device="cuda") for m in (3, 5, 9, 16, 24, 32)]
+    a, sa, w, sw, _ = experts(10, 300, 1, 384, 512)
+    plain = (a, sa, w[0], sw[0])
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            out = [qg.qmm_af4_g64(xs[i], plane, meta, 256), qg.qmm_fp8_b128_grouped(*few), qg.qmm_fp8_b128_grouped(*many),
+                   qg.qmm_fp8_b128(*plain), qg.token_logprobs(logits, torch.zeros(2, dtype=torch.int64, device="cuda"), 4)[0]]
+            torch.cuda.current_stream().synchronize()
+        return out
+
+    torch.cuda.synchronize()
+    start, got = threading.Barrier(len(xs)), [None] * len(xs)
+
+    def thread(i):
+        start.wait(60)
+        got[i] = work(i)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(len(xs)):
+        assert got[i] is not None and all(torch.equal(x, y) for x, y in zip(got[i], work(i), strict=True))
+    assert qg.device_error() == 0
+
+
+def test_first_calls_of_several_threads():
+    for _ in range(3):
+        code = "import sys; sys.path[:0] = ['tests', '.']; import test_gpu_layer_edges as t; t.first_calls()"
+        r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0, r.stderr[-2000:]
