@@ -339,12 +339,12 @@ size_t smem_bytes(int M, int cap, int RB) {
 template <int RB, bool PF, int TM>
 int launch(const DevCtx& dc, const Params& p, int blocks, size_t smem, cudaStream_t s) {
     auto kern = af4_gemv_kernel<RB, PF, TM>;
-    static std::atomic<size_t> configured[64];
-    if (smem > 48 * 1024 && dc.device >= 0 && dc.device < 64 && configured[dc.device] < smem) {
+    static std::atomic<int> configured[64];  // set by any thread, all to the same
+    if (smem > 48 * 1024 && dc.device >= 0 && dc.device < 64 && !configured[dc.device]) {
         cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, dc.max_smem_optin);
         if (e != cudaSuccess) return cuda_fail(e);
-        configured[dc.device] = smem;
+        configured[dc.device] = 1;
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks, (unsigned)p.KS, 1);
