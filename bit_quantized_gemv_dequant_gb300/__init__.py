@@ -9,7 +9,8 @@ the serving operators, by the compiled module _serving. It only marshals
 arguments: torch supplies device memory and the current stream, every step of
 the computation runs in the library's kernels. The library is loaded on first
 use, and every call raises if it has not been built or no CUDA device is
-present: there is no CPU fallback.
+present: there is no CPU fallback. Calls run on the current device, and tensors
+of another one are refused.
 
 Workspace: calls that need device scratch (split-K partial sums) get it from
 a torch buffer per (device, stream) that grows on demand, unless the caller
@@ -143,10 +144,10 @@ def _check(rc: int, what: str):
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
-    if type(t) is torch.Tensor and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype):
-        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current device ({torch._C._cuda_getDevice()}), got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:

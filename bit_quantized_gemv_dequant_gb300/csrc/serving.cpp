@@ -53,10 +53,17 @@ void check(int status, const char* what) {
     throw Raised{};
 }
 
+// The current device, asked for once per call.
+thread_local int t_device = -1;
+
+// A tensor that the call's kernels can read: another device's memory is none.
 const Tensor& cuda(PyObject* o, const char* name) {
     if (!THPVariable_Check(o)) value_error("%s must be a CUDA tensor", name);
     const Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda()) value_error("%s must be a CUDA tensor", name);
+    if (t_device < 0) t_device = c10::cuda::current_device();
+    if (t.get_device() != t_device)
+        value_error("%s must be on the current device (%d), got %d", name, t_device, (int)t.get_device());
     return t;
 }
 
@@ -249,6 +256,7 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return nullptr;
     }
     try {
+        t_device = -1;
         std::optional<c10::cuda::CUDAStreamGuard> guard;
         if (N > 1 && a[N - 1] != Py_None)
             guard.emplace(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream_of(a[N - 1])),

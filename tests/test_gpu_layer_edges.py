@@ -201,3 +201,22 @@ def test_first_calls_of_several_threads():
         code = "import sys; sys.path[:0] = ['tests', '.']; import test_gpu_layer_edges as t; t.first_calls()"
         r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
         assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_tensors_of_another_device(monkeypatch):
+    """The kernels run on the current device: tensors elsewhere are refused, not read."""
+    x = torch.ones(4, 256, device="cuda")
+    w = torch.zeros(8 * 18, dtype=torch.uint8, device="cuda")
+    assert qg.silu_mul(x, x).shape == x.shape and qg.qgemv_q4_0(w, x[:1], N=1).shape == (1, 1)
+    here = torch.cuda.current_device()
+    if torch.cuda.device_count() > 1:
+        with torch.cuda.device(1 - min(here, 1)):
+            for call in (lambda: qg.silu_mul(x, x), lambda: qg.rms_norm(x), lambda: qg.quantize_fp8_b128(x),
+                         lambda: qg.qgemv_q4_0(w, x[:1], N=1)):
+                with pytest.raises(ValueError, match="current device"):
+                    call()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: here + 1)
+    with pytest.raises(ValueError, match="current device"):
+        qg.qgemv_q4_0(w, x[:1], N=1, stream=0)
+    monkeypatch.undo()
+    assert qg.device_error() == 0
