@@ -2,7 +2,6 @@
 // cores' M side, up to 64 rows of a on the N side, K split over a thread-block
 // cluster where there are too few tiles for the GPU.
 #include <algorithm>
-#include <mutex>
 
 #include "fp8_groups.cuh"
 
@@ -46,17 +45,6 @@ constexpr int smem_bytes(long long E) { return 1024 + kGroupOff + FewGroups::byt
 static_assert(smem_bytes(kMaxExperts) <= 227 * 1024, "shared memory");
 static_assert(kGroupOff % 8 == 0, "tile numbers are 8 bytes");
 
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(in_cta(addr, rank)) : "memory");
-    return v;
-}
 __device__ __forceinline__ void arrive_in_cta(uint32_t bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, rank)) : "memory");
 }
@@ -129,8 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (split > 1) {  // the other CTAs' barriers are there
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        cluster_sync();
     }
     const uint32_t tmem = *slot;
     const long long tiles = groups.first[p.E];
@@ -334,8 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (split > 1) {  // nobody reads this CTA's parts any more
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        cluster_sync();
     }
     if (warp == 1) {
         tc_fence_after();
@@ -343,39 +329,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// How many clusters of i CTAs the GPU holds at once, asked once per kernel and
-// device.
 template <class TY>
-int cluster_room(const DevCtx& dc, const int** room) {
-    static std::once_flag once[64];
-    static cudaError_t error[64];
-    static int held[64][9];
-    std::call_once(once[dc.device], [&] {
-        auto kern = few_kernel<TY>;
-        cudaError_t& e = error[dc.device];
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMaxExperts));
-        for (int i = 1; i < 9 && e == cudaSuccess; ++i) {
-            cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(i);
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = smem_bytes(kMaxExperts);
-            cudaLaunchAttribute attr{};
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = i;
-            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&held[dc.device][i], kern, &cfg);
-        }
-    });
-    *room = held[dc.device];
-    return error[dc.device] == cudaSuccess ? QG_OK : cuda_fail(error[dc.device]);
+int room_of(const DevCtx& dc, const int** room) {
+    return cluster_room<few_kernel<TY>>(dc, kThreads, smem_bytes(kMaxExperts), room);
 }
 
 template <class TY>
 int launch(const DevCtx& dc, const GroupedArgs& a, int split, cudaStream_t s) {
     const int* room;
-    int rc = cluster_room<TY>(dc, &room);
+    int rc = room_of<TY>(dc, &room);
     CUtensorMap mw, ma;
     if (rc == QG_OK) rc = weight_map(&mw, a);
     if (rc == QG_OK) rc = code_map(&ma, a.a, a.M, a.K, 16);
@@ -403,7 +365,7 @@ int launch(const DevCtx& dc, const GroupedArgs& a, int split, cudaStream_t s) {
 
 int plan_grouped_few(const DevCtx& dc, const GroupedArgs& a, FewPlan* plan) {
     const int* room;
-    const int rc = a.y_dtype == QG_F32 ? cluster_room<float>(dc, &room) : cluster_room<__nv_bfloat16>(dc, &room);
+    const int rc = a.y_dtype == QG_F32 ? room_of<float>(dc, &room) : room_of<__nv_bfloat16>(dc, &room);
     if (rc == QG_OK) *plan = few_plan(room, a.M, a.E, a.N, a.K);
     return rc;
 }

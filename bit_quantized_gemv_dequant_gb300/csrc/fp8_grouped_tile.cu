@@ -56,57 +56,13 @@ static_assert(kGroupOff % 8 == 0, "tile numbers are 8 bytes");
 // border at 192, 297 at 160, 301 at 128, 300 with 256 rows alone.
 __device__ __forceinline__ bool is_whole(int rows) { return rows > kWhole; }
 
-// The address of shared memory `addr` in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-// Loads into this CTA's shared memory that complete on a barrier of the pair.
-__device__ __forceinline__ void load_a_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
+// As tma_load_pair, from w [E, N, K].
 __device__ __forceinline__ void load_w_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
-}
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"(acc)
-        : "memory");
-}
-// Arrives on the barrier at this place in both CTAs when the MMAs so far are done.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
-// Arrives on a barrier of the pair. What the arrival orders is reads of tensor
-// memory, complete and behind a tcgen05 fence: no release over the cluster is
-// needed.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int c0, int c1, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // 32 columns of 16 lanes in fragments: register 4 j + 2 i + c of a thread is lane
@@ -235,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t sb = base + st * kStage, bar = in_cta(full(st), 0);
                     if (rank == 0) mbar_arrive_expect_tx(full(st), bytes);
                     load_w_pair(sb, &map_w, b * 128, n0, g.e, bar);
-                    for (int j = 0; j < boxes; ++j) load_a_pair(sb + kBM * 128 + j * 4096, &map_a, b * 128, m0 + j * 32, bar);
+                    for (int j = 0; j < boxes; ++j) tma_load_pair(sb + kBM * 128 + j * 4096, &map_a, b * 128, m0 + j * 32, bar);
                 }
             }
             // Both CTAs' copies are done when the first one's barrier says so; the

@@ -1,7 +1,6 @@
 // qmm_fp8_b128 for few rows of a: 128 rows of w on the tensor cores' M side, the
 // rows of a on the N side, K split over a thread-block cluster.
 #include <algorithm>
-#include <mutex>
 
 #include "fp8_tc.cuh"
 
@@ -50,21 +49,6 @@ struct Geo {
     static_assert(BN * 128 * 4 <= kStages * kStage, "partial sums reuse the ring");
     static_assert(8 * (2 * kStages + 2 * kBufs + 1) + 8 <= 512, "barriers");
 };
-
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
-    uint32_t at;
-    float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-    return v;
-}
 
 template <int BN, class TY>
 __global__ void __launch_bounds__(Geo<BN>::kThreads, 1)
@@ -239,8 +223,7 @@ __global__ void __launch_bounds__(Geo<BN>::kThreads, 1)
             for (int c = 0; c < G::kOwn; ++c)
                 if (own0 + c < rows) part[(own0 + c) * 128 + row] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
         }
-        cluster_arrive();
-        cluster_wait();
+        cluster_sync();
         for (int e = rank * G::kThreads + threadIdx.x; e < rows * 32; e += split * G::kThreads) {
             float4 v[8];  // all parts under way at once
 #pragma unroll
@@ -256,43 +239,12 @@ __global__ void __launch_bounds__(Geo<BN>::kThreads, 1)
             for (int i = 0; i < 4; ++i)
                 if (col + i < p.N) y[m * p.N + col + i] = from_f32<TY>(o[i]);
         }
-        cluster_arrive();
-        cluster_wait();
+        cluster_sync();
     }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, G::kCols);
     }
-}
-
-// How many clusters of i CTAs the GPU holds at once, asked once per kernel and
-// device.
-template <int BN, class TY>
-int cluster_room(const DevCtx& dc, const int** room) {
-    using G = Geo<BN>;
-    static std::once_flag once[64];
-    static cudaError_t error[64];
-    static int held[64][9];
-    std::call_once(once[dc.device], [&] {
-        auto kern = swap_kernel<BN, TY>;
-        cudaError_t& e = error[dc.device];
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
-        for (int i = 1; i < 9 && e == cudaSuccess; ++i) {
-            cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(i);
-            cfg.blockDim = dim3(G::kThreads);
-            cfg.dynamicSmemBytes = G::kSmem;
-            cudaLaunchAttribute attr{};
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = i;
-            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&held[dc.device][i], kern, &cfg);
-        }
-    });
-    *room = held[dc.device];
-    return error[dc.device] == cudaSuccess ? QG_OK : cuda_fail(error[dc.device]);
 }
 
 // The tiles, and the largest split of K whose clusters all run at once with two
@@ -310,7 +262,7 @@ struct Plan {
 template <int BN, class TY>
 int plan(const DevCtx& dc, const Fp8Args& a, Plan* p) {
     const int* room = nullptr;
-    const int rc = cluster_room<BN, TY>(dc, &room);
+    const int rc = cluster_room<swap_kernel<BN, TY>>(dc, Geo<BN>::kThreads, Geo<BN>::kSmem, &room);
     if (rc) return rc;
     *p = Plan{(a.N + 127) / 128, (a.M + BN - 1) / BN, (a.K + 127) / 128, 1, 1};
     for (int i = 2; i < 9 && p->kb >= 2 * i; ++i)

@@ -2,6 +2,8 @@
 // top of the prefill kernels' ones.
 #pragma once
 
+#include <mutex>
+
 #include "prefill_common.cuh"
 #include "serve_common.cuh"
 
@@ -63,6 +65,60 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t tmem, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
 }
 
+// The address of shared memory `addr` in CTA `rank` of the cluster, and what lies there.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(in_cta(addr, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Pairs of CTAs (cta_group::2). A load into this CTA's shared memory that completes on a
+// barrier of the pair:
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"(acc)
+        : "memory");
+}
+// Arrives on the barrier at this place in both CTAs when the MMAs so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// Arrives on a barrier of the pair. What the arrival orders is reads of tensor
+// memory, complete and behind a tcgen05 fence: no release over the cluster is
+// needed (one costs 1000 cycles in fp8_tile.cu).
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int c0, int c1, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
+}
+
 // Programmatic dependent launch: wait for the kernels before this one on the
 // stream; let the next one start its prologue.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -88,6 +144,34 @@ int launch_tile(const DevCtx& dc, const Fp8Args& a, cudaStream_t s);
 // of a group that has nothing (offsets[g] .. offsets[g + 1] - 1) are left out.
 int pad_rows(const DevCtx& dc, const uint8_t* src, uint8_t* dst, long long rows, long long K, long long pitch, cudaStream_t s,
              const int32_t* offsets = nullptr, long long group = 0);
+
+// How many clusters of i CTAs of a kernel the GPU holds at once, i = 1 .. 8, asked once per
+// kernel and device; the kernel may have that much shared memory from then on.
+template <auto KERN>
+int cluster_room(const DevCtx& dc, int threads, int smem, const int** room) {
+    static std::once_flag once[64];
+    static cudaError_t error[64];
+    static int held[64][9];
+    std::call_once(once[dc.device], [&] {
+        cudaError_t& e = error[dc.device];
+        e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        for (int i = 1; i < 9 && e == cudaSuccess; ++i) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(i);
+            cfg.blockDim = dim3(threads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&held[dc.device][i], KERN, &cfg);
+        }
+    });
+    *room = held[dc.device];
+    return error[dc.device] == cudaSuccess ? QG_OK : cuda_fail(error[dc.device]);
+}
 
 // A 2-D map of rows x cols e4m3 codes, boxes of box_rows x 128, 128-byte swizzle.
 int code_map(CUtensorMap* m, const uint8_t* p, long long rows, long long cols, int box_rows);
