@@ -7,7 +7,11 @@
 namespace qg {
 namespace fp8 {
 
-constexpr int kJoin = 10;  // what joining the parts of a tile takes, in k blocks (fp8_grouped_few.cu)
+// What joining the parts of a tile takes, in k blocks (0.4 us each): parts into shared
+// memory, a barrier of the epilogue's threads, arrivals at every CTA and the wait for theirs,
+// the reads from the others, the outputs, and a second round of barrier and arrivals before
+// the next tile. Charged alike for 1 and for 64 rows (up to 32 KB per CTA to exchange).
+constexpr int kJoin = 10;
 
 // The kernel of few rows: CTAs per cluster (0: the GPU holds none of them), and the k
 // blocks that one of them takes one after the other if no expert has more than 64 rows.
@@ -35,7 +39,9 @@ inline FewPlan few_plan(const int* room, long long M, long long E, long long N, 
 // Whether the kernel of few rows takes them, by the rows that an expert has on average:
 // at 32 it takes 93 us of 32 experts, N = K = 4096, and the other one 100; at 48 107 and
 // 104, at 64 133 and 112. Up to 64 it is also taken where it leaves fewer SMs idle, since
-// it splits K for its last tiles (9 experts of 34 rows, N = 2200, K = 5200).
+// it splits K for its last tiles (9 experts of 34 rows, N = 2200, K = 5200). The host knows
+// no more than the average, and counts rows that no expert has: both kernels are right for
+// every spread.
 inline bool may_be_few(long long M, long long E) { return M <= 64 * E; }
 inline bool takes_few(const FewPlan& p, int sms, long long M, long long E, long long N, long long K) {
     if (p.split == 0 || !may_be_few(M, E)) return false;

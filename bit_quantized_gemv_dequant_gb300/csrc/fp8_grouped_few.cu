@@ -21,8 +21,8 @@ namespace {
 //   warps 4-11  take the accumulators into registers, times both scales (f32):
 //               thread = row of w, and 32 of the 64 rows of a
 //
-// 256 rows on 64 experts, N = K = 4096, bf16: 153 us, 6.7 TB/s. 8 rows on 8 of them, N =
-// 4096, K = 2048: 17.0 us, 4.0 TB/s: 256 tiles on 152 SMs, the second round as slow as
+// 256 rows on 64 experts, N = K = 4096, bf16: 156 us, 6.6 TB/s. 8 rows on 8 of them, N =
+// 4096, K = 2048: 17.8 us, 3.8 TB/s: 256 tiles on 152 SMs, the second round as slow as
 // the first; 3 us until the first k block is there.
 //
 // Tiles that do not fill a round of all CTAs are shared, by K, over a cluster (9

@@ -24,8 +24,8 @@ namespace {
 //
 // A k block of a whole chunk takes about 970 cycles (512 of products; the round trip
 // of accumulators and their promotion), of one of 64 rows 640. 16384 rows unevenly on
-// 32 experts: 290 to 303 us, 1.81 to 1.90 PFLOP/s, SM clock 1950 to 2040 MHz at the power
-// limit.
+// 32 experts: 290 to 309 us by the GPU, 1.78 to 1.90 PFLOP/s, SM clock 1950 to 2040 MHz
+// at the power limit.
 //
 //   warps 0-7    epilogue; 216 registers each, which warps 8-11 give up
 //   warp 8       TMA producer, whose copies complete on the first CTA's barrier

@@ -50,9 +50,11 @@ constexpr int kThreads = 128;
 //
 // PAIRED: 16 values of a head per thread, both members of eight pairs (or two runs
 // of eight that are not turned), so a pair's angle is read and its place worked out
-// once: 8192 tokens, 32 and 8 heads of 128, bf16: 34.1 us, 5.9 TB/s; 57 with eight values
+// once: 8192 tokens, 32 and 8 heads of 128, bf16: 34.5 us, 5.8 TB/s; 57 with eight values
 // per thread, whose partners were loaded a second time. It needs D a multiple of 16 and
-// pairs that lie apart by a multiple of eight; other heads are turned value by value.
+// pairs that lie apart by a multiple of eight; in other heads a run of eight has partners in
+// two runs, so they are turned value by value, each loading its partner by itself (4096
+// tokens, 36 of 128 values turned: 34 us for 17).
 //
 // Angle i lies at chunk (i % 8) / 2, place i / 8: threads beside each other, whose values
 // are beside each other, read 16-byte words beside each other.

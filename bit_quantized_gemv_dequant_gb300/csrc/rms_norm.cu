@@ -14,7 +14,7 @@ namespace {
 // stay in registers as h until the row's sum is known. Rows of more than 16
 // values for each of 1024 threads read the rest a second time (from L2, mostly).
 //
-// 8192 x 4096 bf16 with an f32 residual, to codes: 59.8 us, 6.2 TB/s; one row 2.6 us.
+// 8192 x 4096 bf16 with an f32 residual, to codes: 60.3 us, 6.1 TB/s; one row 2.6 us.
 // With eight values per thread (and twice the threads) the former takes 100 us.
 //
 // A block of up to 1024 threads takes a row, or each warp of a small block does

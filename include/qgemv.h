@@ -307,7 +307,8 @@ QG_API int qmm_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K, size_t* 
  * ceil(K / 128)]; y [M, N] and everything else as in qmm_fp8_b128, the error
  * bound too. offsets is int32 [experts + 1], from 0 up to M. Rows before
  * offsets[0] and at or after offsets[experts] are left alone; an expert whose
- * range is none (outside of 0 .. M, or backwards) has no rows and is recorded.
+ * range is none (outside of 0 .. M, or backwards) has no rows and is recorded
+ * (rows that two other ranges then have in common get the products of one).
  * M = 0 is fine, experts <= 1024, experts * N <= 2^31 - 2^14. The kernel is
  * chosen by M / experts; any spread of the rows is right. The workspace is
  * needed for the same reason as there: calls with K % 16 == 0 and 16-byte
@@ -327,7 +328,8 @@ QG_API int qmm_fp8_b128_grouped_workspace_size(int64_t M, int64_t experts, int64
  *   h = x + residual (x alone if residual is NULL)
  *   y = h / sqrt(mean(h^2) + eps) * (weight_offset + weight)
  * in f32 (squares and their sum too: rows of values past 2^63 / sqrt(K)
- * overflow), with one rounding to y [M, K] of y_dtype. weight [K] may be
+ * overflow, and below 2^-62 values lose bits of their squares, which only an
+ * eps below 2^-120 lets show), with one rounding to y [M, K] of y_dtype. weight [K] may be
  * NULL: a factor of 1 then, weight_offset or not. With a residual (of
  * x_dtype or f32, rows residual_stride apart), residual_out gets h rounded to
  * its type; it may be the residual itself, with the same stride, and must not
